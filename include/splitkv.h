@@ -388,6 +388,114 @@ splitkv_status splitkv_read_static_device_error(int32_t clear, int32_t *raw, spl
 splitkv_status splitkv_read_device_error(int32_t *dev_error_word, void *workspace, int32_t clear,
                                          int32_t *raw, splitkv_stream stream);
 
+/*
+ * Rows of tokens outside the cache, as splitkv_kv_append reads and
+ * splitkv_kv_gather writes them.  Strides are in elements; a row's innermost
+ * elements are contiguous.
+ *  GQA: k and v are [rows][num_kv_heads][head_dim].
+ *  MLA: k is [rows][head_dim_v], the latent columns, and v is
+ *    [rows][head_dim_qk - head_dim_v], the rotary columns; or v is NULL and k is
+ *    [rows][head_dim_qk], whole cache rows.  Head strides are not used.
+ * 16-byte aligned pointers with strides that keep every row 16-byte aligned
+ * (and widths that are multiples of 8) move in 16-byte pieces, others element
+ * by element.
+ */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t k_token_stride;
+    int64_t k_head_stride;
+    int64_t v_token_stride;
+    int64_t v_head_stride;
+    int32_t dtype;                   /* splitkv_dtype of k and v; need not be the cache's */
+    int32_t reserved;                /* 0 */
+} splitkv_kv_rows;
+
+/*
+ * splitkv_kv_append -- write the K/V rows of new tokens into the paged cache
+ * that splitkv_decode reads (the appended tokens of LiquidCP Section 2.1), and
+ * quantise them there when the cache is E4M3 (SPLASH Appendix C.1).
+ *  prob: the same description that the attention call takes (q is not read).
+ *    k_cache and v_cache are written.  Row qo_indptr[b] + i of `rows` is token
+ *    seq_lens[b] - q_len + i of request b: the rows of its q_len new tokens, in
+ *    the slots where the attention expects them.
+ *  Entries: float32 caches take the value, bf16 caches the value rounded to
+ *    nearest even, E4M3 caches the code of sat(x / k_scale) (or v_scale; MLA
+ *    rows take k_scale): the quotient in float32, rounded to nearest even,
+ *    magnitudes above 448 (infinities too) to 448, NaN to the NaN code.
+ *  Positions come from the device arrays seq_lens and qo_indptr, so a captured
+ *    call follows lengths updated in place; the host arrays give the number of
+ *    rows and the argument checks.  Rows behind the device qo_indptr's last
+ *    entry are left alone.
+ *  dev_error_word: device int32 or NULL (errors are then not reported).  A row
+ *    whose position or page id is out of range is not written and reports
+ *    DEVICE_CHECK.  Two requests that share a page must not append to one slot.
+ */
+splitkv_status splitkv_kv_append(const splitkv_problem *prob, const splitkv_kv_rows *rows,
+                                 int32_t *dev_error_word, splitkv_stream stream);
+
+/*
+ * splitkv_kv_gather -- read cached tokens back as rows (to hand a request to
+ * another cache or another KV layout, or to compute on its cached values).
+ *  kv_indptr: device [batch + 1], non-decreasing from 0; kv_begin: device
+ *    [batch] or NULL (0).  Row kv_indptr[b] + i of `rows` is token
+ *    kv_begin[b] + i of request b, which must lie below seq_lens[b].
+ *  num_rows: rows that `rows` holds, >= kv_indptr[batch]; rows behind
+ *    kv_indptr[batch] are left as they were.
+ *  Values: E4M3 codes times k_scale / v_scale in float32, rounded once to the
+ *    row type; other entries are converted to it.
+ *  dev_error_word: as splitkv_kv_append; a refused row is written as zeros.
+ */
+splitkv_status splitkv_kv_gather(const splitkv_problem *prob, const int32_t *kv_indptr, const int32_t *kv_begin,
+                                 int32_t num_rows, const splitkv_kv_rows *rows, int32_t *dev_error_word,
+                                 splitkv_stream stream);
+
+/*
+ * Drafted tokens and the two models' probabilities (speculative decoding: the
+ * step after the attention of a drafted block).  The query rows are the
+ * attention call's: request b's row qo_indptr[b] fed its last accepted token,
+ * the rows after it its q_len - 1 drafts, and row r of target_probs is the
+ * target's distribution of the token that follows row r.  All pointers device.
+ */
+typedef struct {
+    int32_t batch;
+    int32_t total_q;                 /* rows: qo_indptr[batch] */
+    int32_t vocab;
+    int32_t reserved;                /* 0 */
+    const int32_t *qo_indptr;        /* [batch + 1] */
+    const int32_t *tokens;           /* [total_q]: the token that each row fed to the model */
+    const float *target_probs;       /* [total_q][vocab], row stride target_stride */
+    const float *draft_probs;        /* the same layout: row r, the distribution that the draft of row
+                                        r + 1 was drawn from (a request's last row is not read); NULL:
+                                        every draft was proposed with certainty */
+    int64_t target_stride;           /* elements, >= vocab */
+    int64_t draft_stride;
+    const float *accept_u;           /* [total_q] random numbers in [0, 1): row r tests the draft of row r + 1 */
+    const float *sample_u;           /* [batch] random numbers in [0, 1) for the drawn tokens */
+    const int32_t *seq_lens;         /* [batch], or NULL with seq_lens_out */
+    int32_t *seq_lens_out;           /* [batch] or NULL: seq_lens without the refused drafts' slots (may be
+                                        seq_lens itself) */
+    int32_t *out_tokens;             /* [total_q] */
+    int32_t *accepted;               /* [batch] */
+} splitkv_verify;
+
+/*
+ * splitkv_verify_drafts -- accept drafted tokens so that the result follows the
+ * target's distribution.  Draft x at row r + 1 is accepted while
+ * accept_u[r] * q_r(x) < p_r(x) (compared exactly).  accepted[b] is the number
+ * of drafts before the first refusal; at that row one token is drawn from
+ * max(p_r - q_r, 0) (from p_r where that is zero everywhere), after the last
+ * draft, if all are accepted, from p_r: the lowest token whose cumulative
+ * weight exceeds sample_u[b] times the row's total.  Tokens without weight are
+ * never drawn; a row without any gives -1.  Weights that are NaN or negative count as
+ * 0.  out_tokens row r of request b: the accepted drafts, then the drawn token,
+ * then -1.  seq_lens_out[b] = seq_lens[b] - (q_len - 1) + accepted[b].  A
+ * request without rows gets accepted 0 and keeps its length.
+ *  dev_error_word: device int32 or NULL.  A draft outside [0, vocab) is refused
+ *    and reports DEVICE_CHECK, and so does a qo_indptr entry outside total_q.
+ */
+splitkv_status splitkv_verify_drafts(const splitkv_verify *v, int32_t *dev_error_word, splitkv_stream stream);
+
 /* Message for the last error returned on the calling thread. */
 const char *splitkv_last_error_message(void);
 const char *splitkv_status_string(splitkv_status s);
@@ -516,7 +624,10 @@ typedef enum {
     SPLITKV_KERNEL_CHUNK_VCONV = 5,  /* f16 copy of the chunk requests' value pages (before the chunk tiles) */
     SPLITKV_KERNEL_PAIR = 6,         /* tcgen05 paired row blocks (33..128 rows per KV head) */
     SPLITKV_KERNEL_MLA_LATENT = 7,   /* bf16 copy of an E4M3 latent cache's pages (before the MLA kernel) */
-    SPLITKV_KERNEL_COUNT = 8
+    SPLITKV_KERNEL_KV_APPEND = 8,    /* rows into the paged cache */
+    SPLITKV_KERNEL_KV_GATHER = 9,    /* cache entries back to rows */
+    SPLITKV_KERNEL_VERIFY = 10,      /* verification of drafted tokens */
+    SPLITKV_KERNEL_COUNT = 11
 } splitkv_kernel;
 
 typedef struct {

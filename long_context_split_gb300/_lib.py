@@ -102,9 +102,25 @@ class KernelTime(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_int32), ("pad", ctypes.c_int32), ("total_ms", ctypes.c_double)]
 
 
+class KVRows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_token_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
+                ("v_head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class Verify(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("total_q", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("qo_indptr", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("target_probs", ctypes.c_void_p), ("draft_probs", ctypes.c_void_p),
+                ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64),
+                ("accept_u", ctypes.c_void_p), ("sample_u", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("seq_lens_out", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p), ("accepted", ctypes.c_void_p)]
+
+
 # splitkv_kernel ids, in order
 KERNEL_NAMES = ["generic_partial_kernel", "gqa_engine_kernel", "mla_partial_kernel", "chunk_tc_kernel",
-                "merge_states_kernel", "chunk_value_convert_kernel", "pair_tc_kernel", "mla_latent_convert_kernel"]
+                "merge_states_kernel", "chunk_value_convert_kernel", "pair_tc_kernel", "mla_latent_convert_kernel",
+                "kv_append_kernel", "kv_gather_kernel", "verify_drafts_kernel"]
 
 # name -> (restype, argtypes); this list mirrors include/splitkv.h
 _vp, _i32, _i64, _dp = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_double)
@@ -138,6 +154,9 @@ SIGNATURES = {
     "merge_states_typed": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp]),
     "splitkv_decode": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp, _vp]),
     "splitkv_decode_static": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, _vp, _vp, _vp, _vp]),
+    "splitkv_kv_append": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(KVRows), _vp, _vp]),
+    "splitkv_kv_gather": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, _vp, _i32, ctypes.POINTER(KVRows), _vp, _vp]),
+    "splitkv_verify_drafts": (ctypes.c_int, [ctypes.POINTER(Verify), _vp, _vp]),
     "splitkv_read_device_error": (ctypes.c_int, [_vp, _vp, _i32, _ip, _vp]),
     "splitkv_read_static_device_error": (ctypes.c_int, [_i32, _ip, _vp]),
     "splitkv_last_error_message": (ctypes.c_char_p, []),
@@ -389,6 +408,97 @@ def splitkv_decode_static(problem: AttentionProblem, plan: Plan, out: torch.Tens
     scratch is the library's own static device array (see include/splitkv.h)."""
     _check(load().splitkv_decode_static(ctypes.byref(problem._s), plan.handle, _ptr(out), _ptr(lse_out),
                                         _ptr(dev_error_word), _stream_handle(stream)))
+
+
+def _kv_rows(problem: AttentionProblem, rows: int, k: torch.Tensor, v: Optional[torch.Tensor]) -> KVRows:
+    """The ``splitkv_kv_rows`` of row tensors: GQA [rows, Hkv, D] each; MLA [rows, 512]
+    and [rows, 64], or [rows, 576] alone.  Any strides but a contiguous last axis."""
+    if problem.kind == "gqa":
+        shapes = [(rows, problem.num_kv_heads, problem.head_dim_qk)] * 2
+        if v is None:
+            raise TypeError("a GQA cache takes key and value rows")
+    elif v is None:
+        shapes = [(rows, problem.head_dim_qk)]
+    else:
+        shapes = [(rows, problem.head_dim_v), (rows, problem.head_dim_qk - problem.head_dim_v)]
+    strides = [0, 0, 0, 0]
+    for n, (t, shape) in enumerate(zip((k, v), shapes)):
+        if tuple(t.shape) != shape:
+            raise TypeError(f"{'kv'[n]} rows have shape {tuple(t.shape)}, expected {shape}")
+        if t.dtype != k.dtype or t.dtype not in _DTYPES:
+            raise TypeError(f"unsupported row dtype {t.dtype}" if t.dtype not in _DTYPES else "k and v rows differ in dtype")
+        st = t.stride()
+        if st[-1] != 1 and shape[-1] > 1 and rows > 0:
+            raise TypeError(f"the last axis of {'kv'[n]} rows must be contiguous")
+        # (strides of axes of length 1 mean nothing)
+        strides[2 * n] = st[0] if rows > 1 else 0
+        if len(shape) == 3 and shape[1] > 1:
+            strides[2 * n + 1] = st[1]
+    return KVRows(k.data_ptr(), None if v is None else v.data_ptr(), *strides, _DTYPES[k.dtype], 0)
+
+
+def kv_append(problem: AttentionProblem, k_new: torch.Tensor, v_new: Optional[torch.Tensor] = None,
+              dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    """splitkv_kv_append: write the rows of the batch's new tokens (row qo_indptr[b] + i is
+    the i-th of request b's last q_len tokens) into the problem's paged cache, quantised
+    when the cache is E4M3.  GQA: k_new, v_new [total_q, Hkv, D]; MLA: k_new the latent
+    columns [total_q, 512] and v_new the rotary columns [total_q, 64], or k_new
+    [total_q, 576] alone.  float32 or bfloat16, any token and head strides."""
+    rows = _kv_rows(problem, problem.total_q, k_new, v_new)
+    _check(load().splitkv_kv_append(ctypes.byref(problem._s), ctypes.byref(rows), _ptr(dev_error_word),
+                                    _stream_handle(stream)))
+
+
+def kv_gather(problem: AttentionProblem, kv_indptr: torch.Tensor, k_out: torch.Tensor,
+              v_out: Optional[torch.Tensor] = None, kv_begin: Optional[torch.Tensor] = None,
+              dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    """splitkv_kv_gather: rows kv_indptr[b] .. kv_indptr[b+1]-1 of k_out / v_out become the
+    (dequantised) cached tokens kv_begin[b] (0 without it) and following of request b.
+    Shapes as kv_append's, over the rows of k_out; kv_indptr, kv_begin device int32."""
+    for name, t, n in (("kv_indptr", kv_indptr, problem.batch + 1), ("kv_begin", kv_begin, problem.batch)):
+        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n):
+            raise TypeError(f"{name} must be a contiguous int32 tensor of {n} entries")
+    rows = _kv_rows(problem, int(k_out.shape[0]), k_out, v_out)
+    _check(load().splitkv_kv_gather(ctypes.byref(problem._s), _ptr(kv_indptr), _ptr(kv_begin), int(k_out.shape[0]),
+                                    ctypes.byref(rows), _ptr(dev_error_word), _stream_handle(stream)))
+
+
+def verify_drafts(tokens: torch.Tensor, qo_indptr: torch.Tensor, target_probs: torch.Tensor,
+                  draft_probs: Optional[torch.Tensor], accept_u: torch.Tensor, sample_u: torch.Tensor,
+                  out_tokens: Optional[torch.Tensor] = None, accepted: Optional[torch.Tensor] = None, *,
+                  seq_lens: Optional[torch.Tensor] = None, seq_lens_out: Optional[torch.Tensor] = None,
+                  dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    """splitkv_verify_drafts: accept drafted tokens against the target's probabilities and
+    draw each request's next token.  Rows are the attention call's: tokens [total_q] int32
+    (each request's last accepted token, then its drafts), target_probs and draft_probs
+    [total_q, vocab] float32 (row r: the token after row r; draft_probs None: drafts
+    proposed with certainty), accept_u [total_q], sample_u [batch].  With seq_lens the
+    lengths without the refused drafts' slots go to seq_lens_out.  Returns (out_tokens,
+    accepted)."""
+    total, vocab = int(tokens.shape[0]), int(target_probs.shape[-1])
+    batch = int(qo_indptr.shape[0]) - 1
+    out_tokens = torch.empty_like(tokens) if out_tokens is None else out_tokens
+    accepted = torch.empty(batch, dtype=torch.int32, device=tokens.device) if accepted is None else accepted
+    for name, t, n, dt in (("tokens", tokens, total, torch.int32), ("qo_indptr", qo_indptr, batch + 1, torch.int32),
+                           ("accept_u", accept_u, total, torch.float32), ("sample_u", sample_u, batch, torch.float32),
+                           ("out_tokens", out_tokens, total, torch.int32), ("accepted", accepted, batch, torch.int32),
+                           ("seq_lens", seq_lens, batch, torch.int32), ("seq_lens_out", seq_lens_out, batch, torch.int32)):
+        if t is not None and (t.dtype != dt or not t.is_contiguous() or t.numel() != n):
+            raise TypeError(f"{name} must be a contiguous {dt} tensor of {n} entries")
+    stride = [vocab, vocab]
+    for i, t in enumerate((target_probs, draft_probs)):
+        if t is None:
+            continue
+        if t.dtype != torch.float32 or tuple(t.shape) != (total, vocab) or (t.stride(1) != 1 and vocab > 1 and total > 0):
+            raise TypeError(f"probabilities must be float32 [{total}, {vocab}] with contiguous rows")
+        if total > 1:
+            stride[i] = t.stride(0)
+    v = Verify(batch, total, vocab, 0, qo_indptr.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(),
+               None if draft_probs is None else draft_probs.data_ptr(), stride[0], stride[1], accept_u.data_ptr(),
+               sample_u.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
+               None if seq_lens_out is None else seq_lens_out.data_ptr(), out_tokens.data_ptr(), accepted.data_ptr())
+    _check(load().splitkv_verify_drafts(ctypes.byref(v), _ptr(dev_error_word), _stream_handle(stream)))
+    return out_tokens, accepted
 
 
 def read_device_error(dev_error_word: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,

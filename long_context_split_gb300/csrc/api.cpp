@@ -306,6 +306,18 @@ splitkv_status check_workspace(const splitkv_plan_t* pl, void* ws, size_t bytes)
 }  // namespace
 
 namespace skv {
+splitkv_status fail_with(splitkv_status s, const char* fmt, ...) {
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    g_msg = buf;
+    return s;
+}
+
+splitkv_status check_problem_lengths(const splitkv_problem* prob) { return check_problem_shape(prob); }
+
 splitkv_status check_decode_args(const splitkv_problem* prob, const splitkv_plan_t* plan, const void* out,
                                  const float* lse_out, const int32_t* dev_error_word) {
     splitkv_status s = check_plan_matches(prob, plan);
