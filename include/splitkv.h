@@ -451,6 +451,84 @@ splitkv_status splitkv_kv_gather(const splitkv_problem *prob, const int32_t *kv_
                                  splitkv_stream stream);
 
 /*
+ * Latent attention from the model's own queries (SPLASH Section 2 Eq. 1): each
+ * head has 192-wide queries (128 + 64 rotary columns) and weights W_uk, W_uv
+ * (128 x 512 each) that raise a latent row c of the cache to the head's key
+ * (W_uk c, c's rotary columns) and value W_uv c.  Two forms of the same result:
+ *  expanded -- every cached token's keys and values are computed, then
+ *    attended: 2 * 512 * 256 operations per cached token and head, 640 per
+ *    (query, key) pair.  For prompts and chunks of new tokens.
+ *  absorbed -- W_uk is applied to the queries and W_uv to the outputs, and the
+ *    latent rows themselves are attended (splitkv_decode on a
+ *    576-wide problem).  For few query tokens per request.
+ * The problem describes the latent cache and the batch: kind MLA, dtype BF16,
+ * head_dim_qk 576, head_dim_v 512, scale > 0 (1 / sqrt(192) for these widths);
+ * E4M3 caches with k_scale.
+ */
+typedef struct {
+    const void *q;                   /* device bf16 [total_q][num_q_heads][192], heads contiguous */
+    int64_t q_token_stride;          /* elements, a multiple of 8, >= num_q_heads * 192 */
+    const void *w_kv_b;              /* device bf16 [num_q_heads][256][512]: per head W_uk's 128 rows, then W_uv's */
+    void *out;                       /* device bf16 [total_q][num_q_heads][128] */
+    float *lse_out;                  /* device float32 [total_q][num_q_heads] or NULL (expanded form) */
+} splitkv_latent_layer;
+
+/* Opaque host-side plan of the expanded form: its tasks, splits and workspace.  Built once per
+ * batch of lengths, reusable by every layer. */
+typedef struct splitkv_latent_plan_s splitkv_latent_plan_t;
+
+/*
+ * splitkv_latent_plan -- tasks of up to 256 query tokens of one (request, head).
+ * A batch with fewer tasks than SMs has its histories split; the partial
+ * states are merged as splitkv_decode's are.  Errors: INVALID_ARG,
+ * UNSUPPORTED (float32, other widths, scale <= 0).  Free with
+ * splitkv_latent_plan_destroy.
+ */
+splitkv_status splitkv_latent_plan(const splitkv_problem *prob, splitkv_latent_plan_t **out);
+void splitkv_latent_plan_destroy(splitkv_latent_plan_t *plan);
+/* Device workspace of splitkv_latent_expanded: descriptors, the batch's latent rows (1152 bytes per
+ * token) and the keys and values of every head (512 bytes per token and head), partial states.
+ * Must be 256-byte aligned. */
+size_t splitkv_latent_workspace_bytes(const splitkv_latent_plan_t *plan);
+int32_t splitkv_latent_plan_num_tasks(const splitkv_latent_plan_t *plan);
+/* Splits of every request, n_splits[batch]; INVALID_ARG on NULL. */
+splitkv_status splitkv_latent_plan_splits(const splitkv_latent_plan_t *plan, int32_t *n_splits);
+/* As splitkv_plan_upload: once per plan and workspace, and after a device error. */
+splitkv_status splitkv_latent_upload(const splitkv_latent_plan_t *plan, void *workspace, size_t ws_bytes,
+                                     splitkv_stream stream);
+
+/*
+ * splitkv_latent_expanded -- out[token][head] of the expanded form; row i of a
+ * request sees keys 0 .. seq_len - q_len + i.  prob->q is not read.  Keys are
+ * rounded to bf16, values and probabilities to f16, scores, sums and outputs
+ * are float32 until the one rounding of the result.  A finite expanded value
+ * beyond the f16 range reports DEVICE_CHECK.  Cache slots past a request's
+ * last token do not reach the result, whatever they hold.  Calls on the same
+ * workspace must be stream-ordered.
+ */
+splitkv_status splitkv_latent_expanded(const splitkv_problem *prob, const splitkv_latent_plan_t *plan,
+                                       const splitkv_latent_layer *layer, void *workspace, size_t ws_bytes,
+                                       int32_t *dev_error_word, splitkv_stream stream);
+
+/*
+ * The two products of the absorbed form around splitkv_decode.
+ * splitkv_latent_absorb_query: q_abs [total_q][num_q_heads][576] =
+ *   (q_nope W_uk, q_rope), the q of the 576-wide problem; rounded to bf16.
+ * splitkv_latent_project: layer->out [total_q][num_q_heads][128] = o_lat W_uv^T
+ *   from splitkv_decode's out, o_lat [total_q][num_q_heads][512].
+ * total_q is prob->qo_indptr_host[batch].  layer->out and lse_out (layer->q) are not
+ * read by the first (second).  q_abs and o_lat: device bf16, 16-byte aligned.
+ */
+splitkv_status splitkv_latent_absorb_query(const splitkv_problem *prob, const splitkv_latent_layer *layer, void *q_abs,
+                                           int32_t *dev_error_word, splitkv_stream stream);
+splitkv_status splitkv_latent_project(const splitkv_problem *prob, const splitkv_latent_layer *layer, const void *o_lat,
+                                      int32_t *dev_error_word, splitkv_stream stream);
+
+/* 1 when the expanded form is expected to be the faster one for the problem's lengths, 0 for the
+ * absorbed one, -1 when the problem is not one of latent attention (host only). */
+int32_t splitkv_latent_prefers_expanded(const splitkv_problem *prob);
+
+/*
  * Drafted tokens and the two models' probabilities (speculative decoding: the
  * step after the attention of a drafted block).  The query rows are the
  * attention call's: request b's row qo_indptr[b] fed its last accepted token,
@@ -627,7 +705,12 @@ typedef enum {
     SPLITKV_KERNEL_KV_APPEND = 8,    /* rows into the paged cache */
     SPLITKV_KERNEL_KV_GATHER = 9,    /* cache entries back to rows */
     SPLITKV_KERNEL_VERIFY = 10,      /* verification of drafted tokens */
-    SPLITKV_KERNEL_COUNT = 11
+    SPLITKV_KERNEL_LATENT_ROWS = 11,       /* bf16 copy of the batch's latent rows */
+    SPLITKV_KERNEL_LATENT_EXPAND = 12,     /* keys and values of every head */
+    SPLITKV_KERNEL_LATENT_ATTENTION = 13,  /* expanded latent attention */
+    SPLITKV_KERNEL_LATENT_ABSORB = 14,     /* queries times W_uk */
+    SPLITKV_KERNEL_LATENT_PROJECT = 15,    /* latent outputs times W_uv^T */
+    SPLITKV_KERNEL_COUNT = 16
 } splitkv_kernel;
 
 typedef struct {

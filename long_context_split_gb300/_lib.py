@@ -117,10 +117,16 @@ class Verify(ctypes.Structure):
                 ("seq_lens_out", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p), ("accepted", ctypes.c_void_p)]
 
 
+class LatentLayer(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64), ("w_kv_b", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("lse_out", ctypes.c_void_p)]
+
+
 # splitkv_kernel ids, in order
 KERNEL_NAMES = ["generic_partial_kernel", "gqa_engine_kernel", "mla_partial_kernel", "chunk_tc_kernel",
                 "merge_states_kernel", "chunk_value_convert_kernel", "pair_tc_kernel", "mla_latent_convert_kernel",
-                "kv_append_kernel", "kv_gather_kernel", "verify_drafts_kernel"]
+                "kv_append_kernel", "kv_gather_kernel", "verify_drafts_kernel", "latent_rows_kernel", "latent_expand_kernel",
+                "latent_attention_kernel", "latent_absorb_kernel", "latent_project_kernel"]
 
 # name -> (restype, argtypes); this list mirrors include/splitkv.h
 _vp, _i32, _i64, _dp = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_double)
@@ -156,6 +162,17 @@ SIGNATURES = {
     "splitkv_decode_static": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, _vp, _vp, _vp, _vp]),
     "splitkv_kv_append": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(KVRows), _vp, _vp]),
     "splitkv_kv_gather": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, _vp, _i32, ctypes.POINTER(KVRows), _vp, _vp]),
+    "splitkv_latent_plan": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(ctypes.c_void_p)]),
+    "splitkv_latent_plan_destroy": (None, [_vp]),
+    "splitkv_latent_workspace_bytes": (ctypes.c_size_t, [_vp]),
+    "splitkv_latent_plan_num_tasks": (_i32, [_vp]),
+    "splitkv_latent_plan_splits": (ctypes.c_int, [_vp, _ip]),
+    "splitkv_latent_upload": (ctypes.c_int, [_vp, _vp, ctypes.c_size_t, _vp]),
+    "splitkv_latent_expanded": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, ctypes.POINTER(LatentLayer), _vp,
+                                               ctypes.c_size_t, _vp, _vp]),
+    "splitkv_latent_absorb_query": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(LatentLayer), _vp, _vp, _vp]),
+    "splitkv_latent_project": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(LatentLayer), _vp, _vp, _vp]),
+    "splitkv_latent_prefers_expanded": (_i32, [ctypes.POINTER(Problem)]),
     "splitkv_verify_drafts": (ctypes.c_int, [ctypes.POINTER(Verify), _vp, _vp]),
     "splitkv_read_device_error": (ctypes.c_int, [_vp, _vp, _i32, _ip, _vp]),
     "splitkv_read_static_device_error": (ctypes.c_int, [_i32, _ip, _vp]),
@@ -461,6 +478,85 @@ def kv_gather(problem: AttentionProblem, kv_indptr: torch.Tensor, k_out: torch.T
     rows = _kv_rows(problem, int(k_out.shape[0]), k_out, v_out)
     _check(load().splitkv_kv_gather(ctypes.byref(problem._s), _ptr(kv_indptr), _ptr(kv_begin), int(k_out.shape[0]),
                                     ctypes.byref(rows), _ptr(dev_error_word), _stream_handle(stream)))
+
+
+class LatentPlan:
+    """Owner of a ``splitkv_latent_plan_t`` (tasks and workspace of the expanded form)."""
+
+    def __init__(self, problem: AttentionProblem):
+        self._h = None
+        h = ctypes.c_void_p()
+        _check(load().splitkv_latent_plan(ctypes.byref(problem._s), ctypes.byref(h)))
+        self._h = h
+        self.batch = problem.batch
+        self.num_tasks = int(load().splitkv_latent_plan_num_tasks(h))
+        self.workspace_bytes = int(load().splitkv_latent_workspace_bytes(h))
+
+    @property
+    def handle(self):
+        return self._h
+
+    def splits(self) -> np.ndarray:
+        out = np.zeros(self.batch, dtype=np.int32)
+        _check(load().splitkv_latent_plan_splits(self._h, out.ctypes.data_as(_ip)))
+        return out
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and _lib is not None:
+            _lib.splitkv_latent_plan_destroy(h)
+            self._h = None
+
+
+def latent_upload(plan: LatentPlan, workspace: torch.Tensor, stream=None):
+    _check(load().splitkv_latent_upload(plan.handle, _ptr(workspace), workspace.numel(), _stream_handle(stream)))
+
+
+def latent_layer(problem: AttentionProblem, q: Optional[torch.Tensor], w_kv_b: torch.Tensor, out: Optional[torch.Tensor],
+                 lse: Optional[torch.Tensor] = None) -> LatentLayer:
+    """The ``splitkv_latent_layer`` of q [total_q, H, 192] (any token stride that is a multiple of
+    8), w_kv_b [H, 256, 512], out [total_q, H, 128], lse [total_q, H] float32; bfloat16 otherwise."""
+    total, heads = problem.total_q, problem.num_q_heads
+    for name, t, shape, dt in (("q", q, (total, heads, 192), torch.bfloat16), ("w_kv_b", w_kv_b, (heads, 256, 512), torch.bfloat16),
+                               ("out", out, (total, heads, 128), torch.bfloat16), ("lse", lse, (total, heads), torch.float32)):
+        if t is None:
+            continue
+        if t.dtype != dt or tuple(t.shape) != shape:
+            raise TypeError(f"{name} must be {dt} of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+        if name == "q":
+            if total > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != 192)):
+                raise TypeError("the heads of a query token must be contiguous")
+        elif not t.is_contiguous():
+            raise TypeError(f"{name} must be contiguous")
+    stride = heads * 192 if q is None or total <= 1 else q.stride(0)
+    return LatentLayer(None if q is None else q.data_ptr(), stride, w_kv_b.data_ptr(), None if out is None else out.data_ptr(),
+                       None if lse is None else lse.data_ptr())
+
+
+def latent_expanded(problem: AttentionProblem, plan: LatentPlan, layer: LatentLayer, workspace: torch.Tensor,
+                    dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    _check(load().splitkv_latent_expanded(ctypes.byref(problem._s), plan.handle, ctypes.byref(layer), _ptr(workspace),
+                                          workspace.numel(), _ptr(dev_error_word), _stream_handle(stream)))
+
+
+def latent_absorb_query(problem: AttentionProblem, layer: LatentLayer, q_abs: torch.Tensor,
+                        dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    _check(load().splitkv_latent_absorb_query(ctypes.byref(problem._s), ctypes.byref(layer), _ptr(q_abs),
+                                              _ptr(dev_error_word), _stream_handle(stream)))
+
+
+def latent_project(problem: AttentionProblem, layer: LatentLayer, o_lat: torch.Tensor,
+                   dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    _check(load().splitkv_latent_project(ctypes.byref(problem._s), ctypes.byref(layer), _ptr(o_lat),
+                                         _ptr(dev_error_word), _stream_handle(stream)))
+
+
+def latent_prefers_expanded(problem: AttentionProblem) -> bool:
+    """Whether the expanded form is expected to be faster for the problem's lengths."""
+    r = int(load().splitkv_latent_prefers_expanded(ctypes.byref(problem._s)))
+    if r < 0:
+        _check(ERR_INVALID_ARG)
+    return bool(r)
 
 
 def verify_drafts(tokens: torch.Tensor, qo_indptr: torch.Tensor, target_probs: torch.Tensor,

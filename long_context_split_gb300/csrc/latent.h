@@ -1,0 +1,94 @@
+// Types of the latent-attention operators (expanded form, query absorption,
+// value projection) shared by the host entry points and the kernels.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace skv {
+
+constexpr int kLatNope = 128;                      // query / key columns that come from the latent
+constexpr int kLatRope = 64;                       // rotary columns, shared by all heads
+constexpr int kLatQ = kLatNope + kLatRope;
+constexpr int kLatC = 512;                         // latent columns
+constexpr int kLatRow = kLatC + kLatRope;          // cache row
+constexpr int kLatV = 128;                         // value columns of a head
+constexpr int kLatW = kLatNope + kLatV;            // weight rows of a head (key rows, then value rows)
+constexpr int kLatPad = 128;                       // each request's rows are padded to this many
+
+struct LatentReq {
+    int32_t seq_len;
+    int32_t q_len;
+    int32_t q_start;
+    int32_t row_base;       // first of the request's rows in the copies
+    int32_t n_splits;
+    int32_t state_base;     // partial state of token i, head h, split r: state_base + (i * H + h) * n_splits + r
+    int32_t pad[2];
+};
+static_assert(sizeof(LatentReq) == 32, "LatentReq layout");
+
+// Up to 256 query tokens of one (request, head) over the keys [key_begin, key_end) of one split.
+struct LatentTask {
+    int32_t b;
+    int32_t head;
+    int32_t row_begin;
+    int32_t row_end;
+    int32_t key_begin;      // a multiple of 128
+    int32_t key_end;
+    int32_t split;
+    int32_t pad;
+};
+static_assert(sizeof(LatentTask) == 32, "LatentTask layout");
+
+// 128 rows of the copies: request, first token.
+struct LatentBlock {
+    int32_t b;
+    int32_t token;
+};
+static_assert(sizeof(LatentBlock) == 8, "LatentBlock layout");
+
+struct LatentArgs {
+    const void* q;             // bf16 [total_q][H][192], token stride below
+    int64_t q_stride;
+    const void* w;             // bf16 [H][256][512]
+    const void* cache;         // latent cache, bf16 or E4M3
+    const int32_t* page_table;
+    const LatentReq* reqs;
+    const LatentTask* tasks;
+    const LatentBlock* blocks;
+    void* rows;                // bf16 [padded rows][576]: the requests' latent rows
+    void* keys;                // bf16 [H][padded rows][128]
+    void* vals;                // f16 [H][padded rows][128]
+    void* out;                 // bf16 [total_q][H][128]
+    float* lse_out;            // may be null
+    float* o_part;             // partial states of a split batch, or null: the tasks write final rows
+    float* lse_part;
+    Control* ctrl;
+    int32_t* err;
+    int32_t total_q;
+    int32_t heads;
+    int32_t num_tasks;
+    int32_t num_blocks;        // padded rows / 128
+    int32_t page_size;
+    int32_t num_pages;
+    int32_t max_pages;
+    int32_t kv_fp8;
+    float scale_log2;          // scale * k_scale * log2 e
+    float v_scale;             // k_scale: values are codes times it
+    int32_t inject;
+};
+
+// bf16 (exact) copy of the batch's latent rows, padding rows zero
+cudaError_t launch_latent_rows(const LatentArgs& a, cudaStream_t s);
+// keys and values of every head from the copy
+cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s);
+cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s);
+// q_abs [total_q][H][576] = (q_nope W_uk | q_rope); a.q, a.w
+cudaError_t launch_latent_absorb(const LatentArgs& a, void* q_abs, cudaStream_t s);
+// out [total_q][H][128] = o_lat [total_q][H][512] W_uv^T; a.w, a.out
+cudaError_t launch_latent_project(const LatentArgs& a, const void* o_lat, cudaStream_t s);
+
+}  // namespace skv

@@ -1,0 +1,532 @@
+// Expanded latent attention on sm_103a with tcgen05 tensor cores: each head's
+// own keys (128 columns from the latent, 64 rotary columns shared by all heads)
+// and values (128 columns), causal over the appended tokens.
+//
+// What it computes, for up to 256 query tokens of one (request, head) over one
+// split of the request's history: s = scale (q_nope . k_nope + q_rope . k_rope),
+// the softmax of each token's visible keys, o = sum p v -- the final row, or a
+// split's partial state (normalised output, natural-log LSE) for the merge.
+//
+// What bounds it: the tensor pipe (2 * 320 operations per visible pair and
+// head) and, close behind, the exponentials: per 128-row tile and 64 keys 16 k-steps
+// of products take about 670 cycles, 8192 exponentials 512 cycles of the
+// special-function unit.  The keys and values of a (request, head) are read by all
+// of its query tiles, which run together, so they come from L2.
+//
+// How: two 128-token tiles per CTA share each 64-key unit (K 64 x 192, V 64 x 128,
+// 40 KB, a ring of three stages under 96 KB of queries).  A tile's MMA thread
+// issues S = Q K^T of unit u + 1 into one of two tensor-memory buffers before
+// O += P V of unit u; the tile's four softmax warps (a thread per token) take the
+// row maximum, keep a running maximum and sum (base 2; O is rescaled only when a
+// maximum grows by more than 2^8, so P stays below 2^8), and write P over S as f16.
+// P and V are f16 because their product takes one type and f16's 11 significant
+// bits keep both roundings below the output's own; Q and K stay bf16, as given.
+// Sums, maxima and O are float32.  Products run in issue order, so S of unit u + 2
+// replaces P of unit u only after P V of unit u has read it.
+//
+// Warp roles: warp 0 TMA producer and task claimer, warps 1 and 10 the tiles' MMA
+// threads, warps 2..5 and 6..9 their softmax and epilogue.  Waits are bounded; on
+// expiry the CTA records the error word and drains its copies and products.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "latent.h"
+#include "tc_common.cuh"
+
+namespace skv {
+namespace {
+
+constexpr int kRows = 128;                          // query tokens per tile (tensor-memory lanes)
+constexpr int kTiles = 2;
+constexpr int kKeys = 64;                           // keys per unit
+constexpr int kTR = 4;                              // task ring slots
+constexpr int kSoftWarps = 4 * kTiles;
+constexpr int kTaskConsumers = kTiles + kSoftWarps; // per tile an MMA thread and 4 softmax warps
+constexpr int kThreads = (1 + kTiles + kSoftWarps) * 32;
+constexpr int kIssuerWarp1 = 2 + kSoftWarps;
+constexpr float kRescaleThreshold = 8.0f;           // log2 units
+constexpr int kTmemTile = 256;                      // tensor-memory columns per tile: O (128) | S/P | S/P
+constexpr int kColS = 128;
+constexpr int kTmemCols = kTiles * kTmemTile;
+
+constexpr int kQBoxes = kLatQ / 64, kVBoxes = kLatV / 64;
+constexpr int kQBox = kRows * 128;
+constexpr int kKvBox = kKeys * 128;
+constexpr int kQTile = kQBoxes * kQBox;
+constexpr int kQBytes = kTiles * kQTile;
+constexpr int kKBytes = kQBoxes * kKvBox;
+constexpr int kStage = kKBytes + kVBoxes * kKvBox;
+constexpr int NS = 3;
+
+struct Bars {
+    unsigned long long task_full[kTR], task_empty[kTR];
+    int task_slot[kTR];
+    unsigned long long stage_full[NS];
+    unsigned long long stage_empty[kTiles][NS];   // per tile: its P V product of the stage's unit is done
+    unsigned long long q_full, q_empty;
+    unsigned long long s_full[kTiles][2], p_full[kTiles][2];
+    unsigned long long o_full[kTiles], o_empty[kTiles];
+    unsigned long long drain[kTiles];
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+constexpr size_t kSmemBytes = 1024 + kQBytes + (size_t)NS * kStage + sizeof(Bars);
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+// what every role derives from a task
+struct Task {
+    int head, row0, split, kb, kend, n_units;
+    int rows[kTiles];     // valid tokens of each tile
+    int nu[kTiles];       // units each tile attends
+    LatentReq r;
+};
+
+__device__ __forceinline__ Task read_task(const LatentArgs& a, int id) {
+    Task t;
+    const LatentTask d = a.tasks[id];
+    t.r = a.reqs[d.b];
+    t.head = d.head;
+    t.row0 = d.row_begin;
+    t.split = d.split;
+    t.kb = t.kend = d.key_begin;
+    t.n_units = 0;
+#pragma unroll
+    for (int x = 0; x < kTiles; ++x) {
+        const int r0 = d.row_begin + x * kRows;
+        t.rows[x] = max(0, min(kRows, d.row_end - r0));
+        t.nu[x] = 0;
+        if (t.rows[x] > 0) {
+            // keys the tile's last token may see, within the split
+            const int ke = min(d.key_end, t.r.seq_len - t.r.q_len + r0 + t.rows[x]);
+            if (ke > t.kb) {
+                t.nu[x] = (ke - t.kb + kKeys - 1) / kKeys;
+                t.kend = max(t.kend, ke);
+                t.n_units = max(t.n_units, t.nu[x]);
+            }
+        }
+    }
+    return t;
+}
+
+struct Ring {
+    uint32_t n = 0;
+    // next task id (-1: no more); -2 when the wait gave up
+    __device__ __forceinline__ int next(Bars& B, volatile int* abort_flag, int lane, bool whole_warp) {
+        const int slot = (int)(n % kTR);
+        const uint32_t par = (n / kTR) & 1;
+        int ok = 1;
+        if (lane == 0) ok = wait_bar(smem_u32(&B.task_full[slot]), par, abort_flag, true) ? 1 : 0;
+        if (whole_warp) ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) return -2;
+        (void)mbar_try(smem_u32(&B.task_full[slot]), par);
+        const int id = ((volatile int*)B.task_slot)[slot];
+        if (whole_warp) __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&B.task_empty[slot]));
+        ++n;
+        return id;
+    }
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                        const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ CUtensorMap tmap_v, LatentArgs a) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    unsigned char* sQ = smem;                              // tile x at x * kQTile
+    unsigned char* sStage = sQ + kQBytes;                  // stage: 2 key boxes, the rotary box, 2 value boxes
+    Bars& B = *(Bars*)(sStage + NS * kStage);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kTR; ++s) {
+            mbar_init(smem_u32(&B.task_full[s]), 1);
+            mbar_init(smem_u32(&B.task_empty[s]), kTaskConsumers);
+        }
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(smem_u32(&B.stage_full[s]), 1);
+            for (int x = 0; x < kTiles; ++x) mbar_init(smem_u32(&B.stage_empty[x][s]), 1);
+        }
+        mbar_init(smem_u32(&B.q_full), 1);
+        mbar_init(smem_u32(&B.q_empty), kTiles);
+        for (int x = 0; x < kTiles; ++x) {
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&B.s_full[x][b]), 1);
+                mbar_init(smem_u32(&B.p_full[x][b]), 4);
+            }
+            mbar_init(smem_u32(&B.o_full[x]), 1);
+            mbar_init(smem_u32(&B.o_empty[x]), 4);
+            mbar_init(smem_u32(&B.drain[x]), 1);
+        }
+        B.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = B.tmem_base;
+    volatile int* abort_flag = &B.abort_flag;
+    const int padded = a.num_blocks * kLatPad;
+    auto give_up = [&](int site) {
+        if (!*abort_flag) {
+            set_error(a.err, ERR_TIMEOUT | site);
+            *abort_flag = 1;
+        }
+    };
+
+    if (warp == 0) {
+        // ===================== producer and task claimer (lane 0) =====================
+        if (lane == 0) {
+            uint32_t item = 0, qn = 0, claimed = 0;
+            uint32_t occ = 0, opar = 0, nph = 0;   // per (tile, stage), bit 8 x + s: the tile attends the stage's unit;
+                                                   // its release's parity; the next one's
+            bool ok = a.inject != 1;               // (test hook: publish nothing)
+            while (ok) {
+                const int slot = (int)(claimed % kTR);
+                if (!wait_bar(smem_u32(&B.task_empty[slot]), ((claimed / kTR) & 1) ^ 1, abort_flag, true)) {
+                    give_up(SITE_EMPTY_WAIT);
+                    break;
+                }
+                int id = atomicAdd(&a.ctrl->chunk_head, 1);
+                if (id >= a.num_tasks) id = -1;
+                ((volatile int*)B.task_slot)[slot] = id;
+                mbar_arrive(smem_u32(&B.task_full[slot]));
+                ++claimed;
+                if (id < 0) break;
+                const Task t = read_task(a, id);
+                if (t.n_units == 0) continue;
+                // both tiles' queries (rows past the request are other tokens, or the zero fill past
+                // the tensor; they are never written back)
+                if (!wait_bar(smem_u32(&B.q_empty), (qn & 1) ^ 1, abort_flag, true)) {
+                    give_up(SITE_EMPTY_WAIT);
+                    break;
+                }
+                mbar_expect_tx(smem_u32(&B.q_full), kQBytes);
+                for (int x = 0; x < kTiles; ++x)
+                    for (int j = 0; j < kQBoxes; ++j)
+                        tma_2d(smem_u32(sQ + x * kQTile + j * kQBox), &tmap_q, t.head * kLatQ + 64 * j,
+                               t.r.q_start + t.row0 + x * kRows, smem_u32(&B.q_full));
+                ++qn;
+                for (int u = 0; u < t.n_units; ++u, ++item) {
+                    const int s = (int)(item % NS);
+                    bool freed = true;
+                    for (int x = 0; x < kTiles && freed; ++x) {
+                        const uint32_t bit = 1u << (8 * x + s);
+                        if (occ & bit) freed = wait_bar(smem_u32(&B.stage_empty[x][s]), (opar & bit) ? 1u : 0u, abort_flag, true);
+                    }
+                    if (!freed) {
+                        give_up(SITE_EMPTY_WAIT);
+                        ok = false;
+                        break;
+                    }
+                    for (int x = 0; x < kTiles; ++x) {
+                        const uint32_t bit = 1u << (8 * x + s);
+                        if (u < t.nu[x]) {
+                            occ |= bit;
+                            opar = (opar & ~bit) | (nph & bit);
+                            nph ^= bit;
+                        } else {
+                            occ &= ~bit;
+                        }
+                    }
+                    const uint32_t full = smem_u32(&B.stage_full[s]);
+                    const uint32_t st = smem_u32(sStage + s * kStage);
+                    const int y = t.r.row_base + t.kb + u * kKeys;   // row of the copies
+                    const int yh = t.head * padded + y;
+                    mbar_expect_tx(full, kStage);
+                    tma_2d(st, &tmap_k, 0, yh, full);
+                    tma_2d(st + kKvBox, &tmap_k, 64, yh, full);
+                    tma_2d(st + 2 * kKvBox, &tmap_r, kLatC, y, full);
+                    tma_2d(st + kKBytes, &tmap_v, 0, yh, full);
+                    tma_2d(st + kKBytes + kKvBox, &tmap_v, 64, yh, full);
+                }
+            }
+            // no copy may still be landing when the CTA leaves
+            for (uint32_t k = 0; k < (uint32_t)NS && k < item; ++k) {
+                const uint32_t last = item - 1 - k;
+                if (!wait_bar(smem_u32(&B.stage_full[last % NS]), (last / NS) & 1, abort_flag, false))
+                    set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+            }
+            if (qn && !wait_bar(smem_u32(&B.q_full), (qn - 1) & 1, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp == 1 || warp == kIssuerWarp1) {
+        // ===================== MMA issuer of tile x (lane 0) =====================
+        const int x = warp == 1 ? 0 : 1;
+        if (lane == 0) {
+            constexpr uint32_t id_s = idesc_bf16(kRows, kKeys, 0);
+            constexpr uint32_t id_o = idesc_f16(kRows, kLatV, 1);     // P and V both f16
+            const uint64_t qd = desc_sw128(smem_u32(sQ + x * kQTile), 16, 1024);
+            const uint32_t ocol = tmem + x * kTmemTile, bufcol = ocol + kColS;
+            uint32_t item = 0, qn = 0;
+            uint32_t pc = 0;      // units this tile attended so far
+            uint32_t tn = 0;      // tasks this tile finished
+            bool ok = true;
+            Ring ring;
+            while (ok) {
+                const int id = ring.next(B, abort_flag, 0, false);
+                if (id == -2) { give_up(SITE_FULL_WAIT); break; }
+                if (id < 0) break;
+                const Task t = read_task(a, id);
+                if (t.n_units == 0) continue;
+                const uint32_t item0 = item;      // stage of unit u: (item0 + u) % NS
+                item += t.n_units;
+                const int nu = x ? t.nu[1] : t.nu[0];
+                if (!wait_bar(smem_u32(&B.q_full), qn & 1, abort_flag, true)) { give_up(SITE_FULL_WAIT); break; }
+                ++qn;
+                if (nu == 0) {                    // nothing to attend: release the queries
+                    mbar_arrive(smem_u32(&B.q_empty));
+                    continue;
+                }
+                tc_fence_after();
+                auto issue_s = [&](int u) -> bool {
+                    const uint32_t gi = item0 + u;
+                    const int stage = (int)(gi % NS);
+                    if (!wait_bar(smem_u32(&B.stage_full[stage]), (gi / NS) & 1, abort_flag, true)) return false;
+                    tc_fence_after();
+                    const uint32_t gs = pc + u;
+                    const uint32_t scol = bufcol + kKeys * (gs & 1);
+                    const uint64_t kd = desc_sw128(smem_u32(sStage + stage * kStage), 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < kLatQ / 16; ++kk) {
+                        const uint64_t ad = qd + (uint64_t)((((kk >> 2) * kQBox) + (kk & 3) * 32) >> 4);
+                        const uint64_t bd = kd + (uint64_t)((((kk >> 2) * kKvBox) + (kk & 3) * 32) >> 4);
+                        if (kk == 0) mma_f16c<0>(scol, ad, bd, id_s);
+                        else mma_f16c<1>(scol, ad, bd, id_s);
+                    }
+                    mma_commit(smem_u32(&B.s_full[x][gs & 1]));
+                    return true;
+                };
+                auto issue_pv = [&](int u) -> bool {
+                    if (u == 0 && !wait_bar(smem_u32(&B.o_empty[x]), (tn & 1) ^ 1, abort_flag, true)) return false;
+                    const uint32_t gp = pc + u;
+                    if (!wait_bar(smem_u32(&B.p_full[x][gp & 1]), (gp >> 1) & 1, abort_flag, true)) return false;
+                    tc_fence_after();
+                    const uint32_t pcol = bufcol + kKeys * (gp & 1);
+                    const int stage = (int)((item0 + u) % NS);
+                    const uint64_t vd = desc_sw128(smem_u32(sStage + stage * kStage + kKBytes), kKvBox, 1024);
+                    mma_f16_ts(ocol, pcol, vd, id_o, u > 0 ? 1u : 0u);
+#pragma unroll
+                    for (int kk = 1; kk < 4; ++kk) mma_f16_tsc<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o);
+                    mma_commit(smem_u32(&B.stage_empty[x][stage]));
+                    return true;
+                };
+                ok = issue_s(0);
+                for (int u = 0; ok && u + 1 < nu; ++u) ok = issue_s(u + 1) && issue_pv(u);
+                if (ok) mma_commit(smem_u32(&B.q_empty));   // every S of the task is issued
+                if (ok) ok = issue_pv(nu - 1);
+                if (!ok) { give_up(SITE_FULL_WAIT); break; }
+                mma_commit(smem_u32(&B.o_full[x]));
+                pc += nu;
+                ++tn;
+            }
+            // every product issued here completes before tensor memory is released
+            mma_commit(smem_u32(&B.drain[x]));
+            if (!wait_bar(smem_u32(&B.drain[x]), 0, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+        }
+        __syncwarp();
+    } else {
+        // ===================== softmax + epilogue (thread = query token of tile x) =====================
+        const int x = (warp - 2) >> 2;
+        const int row = ((warp & 3) << 5) + lane;                 // tensor-memory lane
+        const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) << 5) << 16) + x * kTmemTile;
+        const float c2 = a.scale_log2;
+        uint32_t sn = 0, on = 0, item = 0;
+        uint32_t ph = 0;                     // per stage: phase parity of this tile's next release
+        bool ok = true;
+        Ring ring;
+        while (ok) {
+            const int id = ring.next(B, abort_flag, lane, true);
+            if (id == -2) { give_up(SITE_FULL_WAIT); break; }
+            if (id < 0) break;
+            const Task t = read_task(a, id);
+            const int trows = x ? t.rows[1] : t.rows[0];
+            const int nu = x ? t.nu[1] : t.nu[0];
+            const uint32_t item0 = item;
+            item += t.n_units;
+            if (trows == 0) continue;
+            const bool valid = row < trows;
+            const int i = t.row0 + x * kRows + (valid ? row : 0);  // token of the request
+            // last key this token sees in the split
+            const int limit = valid ? min(t.kend - 1, t.r.seq_len - t.r.q_len + i) : -1;
+            float m = -INFINITY, l = 0.f;
+            for (int u = 0; u < nu; ++u) {
+                const uint32_t gi = sn;
+                const int b2 = (int)(gi & 1);
+                if (!warp_wait(smem_u32(&B.s_full[x][b2]), (gi >> 1) & 1, abort_flag, lane)) { give_up(SITE_FULL_WAIT); ok = false; break; }
+                tc_fence_after();
+                uint32_t sr[64];
+                SKV_LD32(lane_addr + kColS + kKeys * b2, sr);
+                SKV_LD32(lane_addr + kColS + kKeys * b2 + 32, (sr + 32));
+                tc_wait_ld();
+                ++sn;
+                const int key0 = t.kb + u * kKeys;
+                // warp-uniform: the tensor-memory instructions below are warp-collective
+                const bool unmasked = __all_sync(0xffffffffu, key0 + kKeys - 1 <= limit);
+                // the scale is positive, so the maximum is taken before it
+                const float mx = (unmasked ? row_max64<false>(sr, 64) : row_max64<true>(sr, limit - key0 + 1)) * c2;
+                float scale_o = 1.f;
+                bool need = false;
+                if (m == -INFINITY) {
+                    m = mx;
+                } else if (mx > m + kRescaleThreshold) {
+                    scale_o = exp2f(m - mx);
+                    m = mx;
+                    need = true;
+                }
+                if (__any_sync(0xffffffffu, need)) {
+                    if (u >= 1) {
+                        // P V of unit u - 1 has updated O once this tile released that unit's stage; the
+                        // release barrier moves on only with this softmax's next P
+                        const int rs = (int)((item0 + u - 1) % NS);
+                        if (!warp_wait(smem_u32(&B.stage_empty[x][rs]), ((ph >> rs) & 1u) ^ 1u, abort_flag, lane)) {
+                            give_up(SITE_EMPTY_WAIT);
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                    }
+                    l *= scale_o;
+                    for (int c = 0; c < kLatV; c += 32) {
+                        uint32_t o[32];
+                        SKV_LD32(lane_addr + c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale_o);
+                        SKV_ST32(lane_addr + c, o);
+                    }
+                }
+                const float base = (m == -INFINITY) ? 0.f : m;
+                const uint32_t pcol = lane_addr + kColS + kKeys * b2;
+                l += unmasked ? write_p16<false>(sr, c2, base, key0, limit, pcol)
+                              : write_p16<true>(sr, c2, base, key0, limit, pcol);
+                tc_wait_st();
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&B.p_full[x][b2]));
+                ph ^= 1u << ((item0 + u) % NS);
+            }
+            if (!ok) break;
+            if (nu > 0) {
+                if (!warp_wait(smem_u32(&B.o_full[x]), on & 1, abort_flag, lane)) { give_up(SITE_FULL_WAIT); ok = false; break; }
+                ++on;
+                tc_fence_after();
+            }
+            // a token that sees no key of the split has an empty state; a sum that is not positive
+            // over visible keys (NaN, or every score -inf) goes through, as in the formula
+            const bool empty_row = limit < t.kb;
+            const float inv = empty_row ? 0.f : a.v_scale / l;
+            const float lse = empty_row ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            const size_t orow = (size_t)(t.r.q_start + i) * a.heads + t.head;
+            const size_t st = (size_t)t.r.state_base + ((size_t)i * a.heads + t.head) * t.r.n_splits + t.split;
+            const bool direct = a.o_part == nullptr;
+            for (int c = 0; c < kLatV; c += 32) {
+                uint32_t o[32];
+                if (nu > 0) {
+                    SKV_LD32(lane_addr + c, o);
+                    tc_wait_ld();
+                }
+                if (!valid) continue;
+                if (nu == 0 || empty_row) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0u;
+                }
+                if (direct) {
+                    uint4* op = (uint4*)((__nv_bfloat16*)a.out + orow * kLatV + c);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const __nv_bfloat162 p2 = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]) * inv,
+                                                                            __uint_as_float(o[j + 2 * e + 1]) * inv);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+                        }
+                        op[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *(float4*)(a.o_part + st * kLatV + c + j) =
+                            make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
+                                        __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                }
+            }
+            if (valid) {
+                if (!direct) a.lse_part[st] = lse;
+                else if (a.lse_out) a.lse_out[orow] = lse;
+            }
+            if (nu > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&B.o_empty[x]));
+            }
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    if (threadIdx.x == 0) {
+        // the last CTA resets the queue for the next call on this workspace
+        __threadfence();
+        if (atomicAdd(&a.ctrl->chunk_exit, 1) == (int)gridDim.x - 1) {
+            atomicExch(&a.ctrl->chunk_head, 0);
+            atomicExch(&a.ctrl->chunk_exit, 0);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+cudaError_t make_map(CUtensorMap* m, const void* base, long long cols, long long rows, long long stride_elems, int box_rows,
+                     CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+    auto enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)stride_elems * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    cuuint32_t es[2] = {1, 1};
+    CUresult r = enc(m, dtype, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s) {
+    if (a.num_tasks <= 0) return cudaSuccess;
+    const long long rows = (long long)a.num_blocks * kLatPad;
+    CUtensorMap mq, mk, mr, mv;
+    cudaError_t e;
+    if ((e = make_map(&mq, a.q, (long long)a.heads * kLatQ, a.total_q, a.q_stride, kRows)) != cudaSuccess) return e;
+    if ((e = make_map(&mk, a.keys, kLatNope, a.heads * rows, kLatNope, kKeys)) != cudaSuccess) return e;
+    if ((e = make_map(&mr, a.rows, kLatRow, rows, kLatRow, kKeys)) != cudaSuccess) return e;
+    if ((e = make_map(&mv, a.vals, kLatV, a.heads * rows, kLatV, kKeys, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != cudaSuccess) return e;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&]() {
+        attr_err = cudaFuncSetAttribute(latent_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    int dev = 0, sms = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    {
+        ProfileScope ps(SPLITKV_KERNEL_LATENT_ATTENTION, s);
+        latent_attention_kernel<<<std::min(sms, a.num_tasks), kThreads, kSmemBytes, s>>>(mq, mk, mr, mv, a);
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace skv

@@ -1,13 +1,19 @@
 // C-ABI entry points of the operators around the attention call: cache rows in
-// and out, and the verification of drafted tokens.  Argument checks only; the
+// and out, latent attention from the model's own queries, and the verification
+// of drafted tokens.  Argument checks and the expanded form's plan; the
 // arithmetic runs in the CUDA kernels.
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <new>
+#include <vector>
 
 #include <cuda_runtime.h>
 
 #include "splitkv.h"
 #include "internal.h"
+#include "latent.h"
 
 using namespace skv;
 
@@ -108,11 +114,334 @@ splitkv_status check_rows_ptrs(const splitkv_problem* p, const CacheRowsArgs& a,
     return check_ptr(err, "dev_error_word", true);
 }
 
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int device_sms() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess &&
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
+        return n;
+    cudaGetLastError();
+    return 152;   // GB300, where no device is visible
+}
+
+splitkv_status check_latent_problem(const splitkv_problem* p) {
+    splitkv_status s = check_problem_lengths(p);
+    if (s) return s;
+    if (p->kind != SPLITKV_MLA) return fail_with(SPLITKV_ERR_INVALID_ARG, "latent attention takes an MLA problem");
+    if (p->v_cache) return fail_with(SPLITKV_ERR_INVALID_ARG, "an MLA cache has no v_cache");
+    if (p->dtype != SPLITKV_BF16 || p->head_dim_qk != kLatRow || p->head_dim_v != kLatC)
+        return fail_with(SPLITKV_ERR_UNSUPPORTED, "latent attention needs BF16, head_dim_qk 576 and head_dim_v 512");
+    if (!(p->scale > 0.f)) return fail_with(SPLITKV_ERR_UNSUPPORTED, "latent attention needs scale > 0");
+    return SPLITKV_OK;
+}
+
+splitkv_status check_layer(const splitkv_problem* p, const splitkv_latent_layer* l, bool need_q, bool need_out) {
+    splitkv_status s;
+    if (!l) return fail_with(SPLITKV_ERR_INVALID_ARG, "layer is NULL");
+    if (need_q && (l->q_token_stride % 8 || l->q_token_stride < (int64_t)p->num_q_heads * kLatQ || l->q_token_stride > (1LL << 38)))
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "q_token_stride %lld: need a multiple of 8, at least num_q_heads * 192",
+                         (long long)l->q_token_stride);
+    if ((need_q && ((uintptr_t)l->q & 15)) || ((uintptr_t)l->w_kv_b & 15) || (need_out && ((uintptr_t)l->out & 15)))
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "q, w_kv_b and out must be 16-byte aligned");
+    if (need_q && (s = check_ptr(l->q, "q", false))) return s;
+    if ((s = check_ptr(l->w_kv_b, "w_kv_b", false))) return s;
+    if (need_out && (s = check_ptr(l->out, "out", false))) return s;
+    return SPLITKV_OK;
+}
+
+LatentArgs layer_args(const splitkv_problem* p, const splitkv_latent_layer* l, int32_t* err) {
+    LatentArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.q = l->q;
+    a.q_stride = l->q_token_stride;
+    a.w = l->w_kv_b;
+    a.out = l->out;
+    a.err = err;
+    a.total_q = p->qo_indptr_host[p->batch];
+    a.heads = p->num_q_heads;
+    a.inject = debug_inject();
+    return a;
+}
+
 int cache_kind(const splitkv_problem* p) { return p->kv_fp8 ? 2 : p->dtype == SPLITKV_BF16 ? 1 : 0; }
 
 }  // namespace
 
+struct splitkv_latent_plan_s {
+    int32_t batch = 0, heads = 0, page = 0, max_pages = 0, kv_fp8 = 0, total_q = 0;
+    std::vector<int32_t> seq_len, qo;
+    std::vector<LatentReq> reqs;
+    std::vector<LatentTask> tasks;
+    std::vector<LatentBlock> blocks;
+    std::vector<int32_t> state_indptr;      // empty when nothing is split
+    int64_t num_states = 0;
+    std::vector<unsigned char> image;       // control block and descriptors
+    size_t off_tasks = 0, off_reqs = 0, off_blocks = 0, off_indptr = 0;
+    size_t off_rows = 0, off_keys = 0, off_vals = 0, off_opart = 0, off_lse = 0, ws_bytes = 0;
+};
+
+namespace {
+
+splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t* pl) {
+    constexpr int kTaskRows = 256;
+    const int B = p->batch, H = p->num_q_heads;
+    pl->batch = B;
+    pl->heads = H;
+    pl->page = p->page_size;
+    pl->max_pages = p->max_pages_per_req;
+    pl->kv_fp8 = p->kv_fp8;
+    pl->seq_len.assign(p->seq_lens_host, p->seq_lens_host + B);
+    pl->qo.assign(p->qo_indptr_host, p->qo_indptr_host + B + 1);
+    pl->total_q = pl->qo[B];
+    long long unsplit = 0, rows = 0;
+    for (int b = 0; b < B; ++b) unsplit += (long long)((pl->qo[b + 1] - pl->qo[b] + kTaskRows - 1) / kTaskRows) * H;
+    if (unsplit > (1 << 28)) return fail_with(SPLITKV_ERR_INVALID_ARG, "too many tasks");
+    const int sms = device_sms();
+    pl->reqs.resize(B);
+    for (int b = 0; b < B; ++b) {
+        LatentReq& r = pl->reqs[b];
+        std::memset(&r, 0, sizeof r);
+        r.seq_len = pl->seq_len[b];
+        r.q_start = pl->qo[b];
+        r.q_len = pl->qo[b + 1] - pl->qo[b];
+        r.row_base = (int32_t)rows;
+        // fewer tasks than SMs: cut the histories so that the SMs are filled once, in splits of at
+        // least 1024 keys
+        r.n_splits = 1;
+        if (unsplit > 0 && unsplit < sms)
+            r.n_splits = (int32_t)std::max<long long>(1, std::min<long long>((sms + unsplit - 1) / unsplit, r.seq_len / 1024));
+        if (r.q_len == 0) continue;          // nothing to attend: its rows are not copied
+        const int blocks = (r.seq_len + kLatPad - 1) / kLatPad;
+        for (int k = 0; k < blocks; ++k) pl->blocks.push_back(LatentBlock{b, k * kLatPad});
+        rows += (long long)blocks * kLatPad;
+        if (rows * H >= (1LL << 31)) return fail_with(SPLITKV_ERR_UNSUPPORTED, "num_q_heads * cached tokens exceeds 2^31");
+    }
+    // The tasks of a (request, head, split) read the same keys and values: together, longest first,
+    // so that those stay in L2; the request with the longest task first.
+    std::vector<int> order(B);
+    for (int b = 0; b < B; ++b) order[b] = b;
+    std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return pl->reqs[x].seq_len > pl->reqs[y].seq_len; });
+    for (int b : order) {
+        const LatentReq& r = pl->reqs[b];
+        const int nblk = (r.seq_len + kLatPad - 1) / kLatPad, per = nblk / r.n_splits, extra = nblk % r.n_splits;
+        for (int h = 0; h < H; ++h)
+            for (int s = 0; s < r.n_splits; ++s) {
+                const int first = s * per + std::min(s, extra), count = per + (s < extra ? 1 : 0);
+                for (int row = (r.q_len - 1) / kTaskRows * kTaskRows; r.q_len > 0 && row >= 0; row -= kTaskRows) {
+                    LatentTask t;
+                    std::memset(&t, 0, sizeof t);
+                    t.b = b;
+                    t.head = h;
+                    t.row_begin = row;
+                    t.row_end = std::min(r.q_len, row + kTaskRows);
+                    t.key_begin = std::min(first * kLatPad, r.seq_len);
+                    t.key_end = std::min((first + count) * kLatPad, r.seq_len);
+                    t.split = s;
+                    pl->tasks.push_back(t);
+                }
+            }
+    }
+    // with any request split, every row of the batch goes through the merge (one state or more)
+    bool split = false;
+    for (const LatentReq& r : pl->reqs) split = split || (r.n_splits > 1 && r.q_len > 0);
+    if (split) {
+        for (LatentReq& r : pl->reqs) {
+            r.state_base = (int32_t)pl->num_states;
+            pl->num_states += (int64_t)r.q_len * H * r.n_splits;
+            if (pl->num_states >= (1LL << 31) - 1) return fail_with(SPLITKV_ERR_INVALID_ARG, "too many partial states");
+        }
+        pl->state_indptr.resize((size_t)pl->total_q * H + 1);
+        for (const LatentReq& r : pl->reqs)
+            for (int64_t x = 0; x < (int64_t)r.q_len * H; ++x)
+                pl->state_indptr[(size_t)r.q_start * H + x] = r.state_base + (int32_t)(x * r.n_splits);
+        pl->state_indptr[(size_t)pl->total_q * H] = (int32_t)pl->num_states;
+    }
+    size_t off = sizeof(Control);
+    pl->off_tasks = off;
+    off = align256(off + pl->tasks.size() * sizeof(LatentTask));
+    pl->off_reqs = off;
+    off = align256(off + pl->reqs.size() * sizeof(LatentReq));
+    pl->off_blocks = off;
+    off = align256(off + pl->blocks.size() * sizeof(LatentBlock));
+    pl->off_indptr = off;
+    off = align256(off + pl->state_indptr.size() * sizeof(int32_t));
+    pl->image.assign(off, 0);
+    auto put = [&](size_t at, const void* src, size_t n) {
+        if (n) std::memcpy(pl->image.data() + at, src, n);
+    };
+    put(pl->off_tasks, pl->tasks.data(), pl->tasks.size() * sizeof(LatentTask));
+    put(pl->off_reqs, pl->reqs.data(), pl->reqs.size() * sizeof(LatentReq));
+    put(pl->off_blocks, pl->blocks.data(), pl->blocks.size() * sizeof(LatentBlock));
+    put(pl->off_indptr, pl->state_indptr.data(), pl->state_indptr.size() * sizeof(int32_t));
+    pl->off_rows = off;
+    off = align256(off + (size_t)rows * kLatRow * 2);
+    pl->off_keys = off;
+    off = align256(off + (size_t)rows * H * kLatNope * 2);
+    pl->off_vals = off;
+    off = align256(off + (size_t)rows * H * kLatV * 2);
+    pl->off_opart = off;
+    off = align256(off + (size_t)pl->num_states * kLatV * 4);
+    pl->off_lse = off;
+    off = align256(off + (size_t)pl->num_states * 4);
+    pl->ws_bytes = off;
+    return SPLITKV_OK;
+}
+
+splitkv_status check_latent_workspace(const splitkv_latent_plan_t* pl, const void* ws, size_t bytes) {
+    if (!pl) return fail_with(SPLITKV_ERR_INVALID_ARG, "plan is NULL");
+    if (!ws) return fail_with(SPLITKV_ERR_WORKSPACE, "workspace is NULL");
+    if ((uintptr_t)ws & 255) return fail_with(SPLITKV_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (bytes < pl->ws_bytes)
+        return fail_with(SPLITKV_ERR_WORKSPACE, "workspace has %zu bytes, plan needs %zu", bytes, pl->ws_bytes);
+    return check_ptr(ws, "workspace", false);
+}
+
+}  // namespace
+
 extern "C" {
+
+splitkv_status splitkv_latent_plan(const splitkv_problem* prob, splitkv_latent_plan_t** out) {
+    if (!out) return fail_with(SPLITKV_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    splitkv_status s = check_latent_problem(prob);
+    if (s) return s;
+    splitkv_latent_plan_t* pl = nullptr;
+    try {
+        pl = new splitkv_latent_plan_t();
+        if ((s = build_latent_plan(prob, pl))) {
+            delete pl;
+            return s;
+        }
+    } catch (const std::bad_alloc&) {
+        delete pl;
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "no host memory for the plan");
+    }
+    *out = pl;
+    return ok();
+}
+
+void splitkv_latent_plan_destroy(splitkv_latent_plan_t* plan) { delete plan; }
+
+size_t splitkv_latent_workspace_bytes(const splitkv_latent_plan_t* plan) { return plan ? plan->ws_bytes : 0; }
+
+int32_t splitkv_latent_plan_num_tasks(const splitkv_latent_plan_t* plan) { return plan ? (int32_t)plan->tasks.size() : -1; }
+
+splitkv_status splitkv_latent_plan_splits(const splitkv_latent_plan_t* plan, int32_t* n_splits) {
+    if (!plan || !n_splits) return fail_with(SPLITKV_ERR_INVALID_ARG, "NULL argument");
+    for (int b = 0; b < plan->batch; ++b) n_splits[b] = plan->reqs[b].n_splits;
+    return ok();
+}
+
+splitkv_status splitkv_latent_upload(const splitkv_latent_plan_t* plan, void* workspace, size_t ws_bytes,
+                                     splitkv_stream stream) {
+    splitkv_status s = check_latent_workspace(plan, workspace, ws_bytes);
+    if (s) return s;
+    cudaError_t e = cudaMemcpyAsync(workspace, plan->image.data(), plan->image.size(), cudaMemcpyHostToDevice,
+                                    (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "plan upload");
+    return ok();
+}
+
+splitkv_status splitkv_latent_expanded(const splitkv_problem* prob, const splitkv_latent_plan_t* plan,
+                                       const splitkv_latent_layer* layer, void* workspace, size_t ws_bytes,
+                                       int32_t* dev_error_word, splitkv_stream stream) {
+    if (!plan) return fail_with(SPLITKV_ERR_INVALID_ARG, "plan is NULL");
+    splitkv_status s = check_latent_problem(prob);
+    if (s) return s;
+    if (prob->batch != plan->batch || prob->num_q_heads != plan->heads || prob->page_size != plan->page ||
+        prob->max_pages_per_req != plan->max_pages || prob->kv_fp8 != plan->kv_fp8)
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "problem shape differs from the plan's");
+    if (std::memcmp(prob->seq_lens_host, plan->seq_len.data(), plan->seq_len.size() * 4) ||
+        std::memcmp(prob->qo_indptr_host, plan->qo.data(), plan->qo.size() * 4))
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "lengths differ from the plan's");
+    if (plan->total_q == 0) return ok();
+    if ((s = check_latent_workspace(plan, workspace, ws_bytes))) return s;
+    if ((s = check_layer(prob, layer, true, true))) return s;
+    if ((uintptr_t)prob->k_cache & 15) return fail_with(SPLITKV_ERR_INVALID_ARG, "k_cache must be 16-byte aligned");
+    if ((s = check_ptr(prob->k_cache, "k_cache", false))) return s;
+    if ((s = check_ptr(prob->page_table, "page_table", false))) return s;
+    if ((s = check_ptr(layer->lse_out, "lse_out", true))) return s;
+    if ((s = check_ptr(dev_error_word, "dev_error_word", true))) return s;
+    unsigned char* base = (unsigned char*)workspace;
+    Control* ctrl = (Control*)base;
+    LatentArgs a = layer_args(prob, layer, dev_error_word ? dev_error_word : &ctrl->error_word);
+    a.lse_out = layer->lse_out;
+    a.cache = prob->k_cache;
+    a.page_table = prob->page_table;
+    a.reqs = (const LatentReq*)(base + plan->off_reqs);
+    a.tasks = (const LatentTask*)(base + plan->off_tasks);
+    a.blocks = (const LatentBlock*)(base + plan->off_blocks);
+    a.rows = base + plan->off_rows;
+    a.keys = base + plan->off_keys;
+    a.vals = base + plan->off_vals;
+    if (plan->num_states > 0) {
+        a.o_part = (float*)(base + plan->off_opart);
+        a.lse_part = (float*)(base + plan->off_lse);
+    }
+    a.ctrl = ctrl;
+    a.num_tasks = (int32_t)plan->tasks.size();
+    a.num_blocks = (int32_t)plan->blocks.size();
+    a.page_size = prob->page_size;
+    a.num_pages = prob->num_pages;
+    a.max_pages = prob->max_pages_per_req;
+    a.kv_fp8 = prob->kv_fp8;
+    a.v_scale = prob->kv_fp8 ? prob->k_scale : 1.f;
+    a.scale_log2 = (float)((double)prob->scale * a.v_scale * 1.4426950408889634);
+    cudaError_t e;
+    if ((e = launch_latent_rows(a, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "latent rows launch");
+    if ((e = launch_latent_expand(a, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "latent expansion launch");
+    if ((e = launch_latent_attention(a, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "latent attention launch");
+    if (plan->num_states > 0) {
+        e = launch_merge(a.o_part, 0, a.lse_part, (const int32_t*)(base + plan->off_indptr), plan->total_q * plan->heads, kLatV,
+                         layer->out, 1, layer->lse_out, (cudaStream_t)stream);
+        if (e != cudaSuccess) return cuda_fail(e, "merge launch");
+    }
+    return ok();
+}
+
+splitkv_status splitkv_latent_absorb_query(const splitkv_problem* prob, const splitkv_latent_layer* layer, void* q_abs,
+                                           int32_t* dev_error_word, splitkv_stream stream) {
+    splitkv_status s = check_latent_problem(prob);
+    if (s) return s;
+    if (prob->qo_indptr_host[prob->batch] == 0) return ok();
+    if ((uintptr_t)q_abs & 15) return fail_with(SPLITKV_ERR_INVALID_ARG, "q_abs must be 16-byte aligned");
+    if ((s = check_layer(prob, layer, true, false))) return s;
+    if ((s = check_ptr(q_abs, "q_abs", false))) return s;
+    if ((s = check_ptr(dev_error_word, "dev_error_word", true))) return s;
+    cudaError_t e = launch_latent_absorb(layer_args(prob, layer, dev_error_word), q_abs, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "query absorption launch");
+    return ok();
+}
+
+splitkv_status splitkv_latent_project(const splitkv_problem* prob, const splitkv_latent_layer* layer, const void* o_lat,
+                                      int32_t* dev_error_word, splitkv_stream stream) {
+    splitkv_status s = check_latent_problem(prob);
+    if (s) return s;
+    if (prob->qo_indptr_host[prob->batch] == 0) return ok();
+    if ((uintptr_t)o_lat & 15) return fail_with(SPLITKV_ERR_INVALID_ARG, "o_lat must be 16-byte aligned");
+    if ((s = check_layer(prob, layer, false, true))) return s;
+    if ((s = check_ptr(o_lat, "o_lat", false))) return s;
+    if ((s = check_ptr(dev_error_word, "dev_error_word", true))) return s;
+    cudaError_t e = launch_latent_project(layer_args(prob, layer, dev_error_word), o_lat, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "value projection launch");
+    return ok();
+}
+
+int32_t splitkv_latent_prefers_expanded(const splitkv_problem* prob) {
+    if (check_latent_problem(prob)) return -1;
+    // operations per head: see splitkv_latent_layer; the absorbed kernel computes its scores in both
+    // halves of the output columns and its probabilities as a high part and a residual
+    double tokens = 0, pairs = 0;
+    for (int b = 0; b < prob->batch; ++b) {
+        const double n = prob->seq_lens_host[b], t = prob->qo_indptr_host[b + 1] - prob->qo_indptr_host[b];
+        if (t == 0) continue;
+        tokens += n;
+        pairs += t * (n - t) + t * (t + 1) / 2;
+    }
+    const double expanded = tokens * 262144 + pairs * 640, absorbed = pairs * 4352;
+    return expanded < absorbed ? 1 : 0;
+}
 
 splitkv_status splitkv_kv_append(const splitkv_problem* prob, const splitkv_kv_rows* rows, int32_t* dev_error_word,
                                  splitkv_stream stream) {
