@@ -220,12 +220,16 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream_handle(stream) -> ctypes.c_void_p:
+def _stream_handle(stream) -> Optional[int]:
+    """The raw handle of `stream`, of the current stream when None."""
     if stream is None:
-        if not torch.cuda.is_available():
-            return ctypes.c_void_p(0)   # argument checks still run; no launch can follow
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        if not torch.cuda.is_initialized():
+            if not torch.cuda.is_available():
+                return None   # argument checks still run; no launch can follow
+            torch.cuda.init()
+        # the handle alone: a torch.cuda.Stream object costs 3 us a call on the host
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
@@ -427,31 +431,36 @@ def splitkv_decode_static(problem: AttentionProblem, plan: Plan, out: torch.Tens
                                         _ptr(dev_error_word), _stream_handle(stream)))
 
 
+def _kv_part(name: str, t: torch.Tensor, shape: tuple, dtype):
+    """(token stride, head stride) of row tensor t, checked."""
+    if t.shape != shape:
+        raise TypeError(f"{name} rows have shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype is not dtype or dtype not in _DTYPES:
+        raise TypeError("k and v rows differ in dtype" if t.dtype is not dtype else f"unsupported row dtype {dtype}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1 and shape[0] > 0:
+        raise TypeError(f"the last axis of {name} rows must be contiguous")
+    # (strides of axes of length 1 mean nothing)
+    return st[0] if shape[0] > 1 else 0, st[1] if len(shape) == 3 and shape[1] > 1 else 0
+
+
 def _kv_rows(problem: AttentionProblem, rows: int, k: torch.Tensor, v: Optional[torch.Tensor]) -> KVRows:
     """The ``splitkv_kv_rows`` of row tensors: GQA [rows, Hkv, D] each; MLA [rows, 512]
     and [rows, 64], or [rows, 576] alone.  Any strides but a contiguous last axis."""
+    dt = k.dtype
     if problem.kind == "gqa":
-        shapes = [(rows, problem.num_kv_heads, problem.head_dim_qk)] * 2
         if v is None:
             raise TypeError("a GQA cache takes key and value rows")
+        shape = vshape = (rows, problem.num_kv_heads, problem.head_dim_qk)
     elif v is None:
-        shapes = [(rows, problem.head_dim_qk)]
+        shape = (rows, problem.head_dim_qk)
     else:
-        shapes = [(rows, problem.head_dim_v), (rows, problem.head_dim_qk - problem.head_dim_v)]
-    strides = [0, 0, 0, 0]
-    for n, (t, shape) in enumerate(zip((k, v), shapes)):
-        if tuple(t.shape) != shape:
-            raise TypeError(f"{'kv'[n]} rows have shape {tuple(t.shape)}, expected {shape}")
-        if t.dtype != k.dtype or t.dtype not in _DTYPES:
-            raise TypeError(f"unsupported row dtype {t.dtype}" if t.dtype not in _DTYPES else "k and v rows differ in dtype")
-        st = t.stride()
-        if st[-1] != 1 and shape[-1] > 1 and rows > 0:
-            raise TypeError(f"the last axis of {'kv'[n]} rows must be contiguous")
-        # (strides of axes of length 1 mean nothing)
-        strides[2 * n] = st[0] if rows > 1 else 0
-        if len(shape) == 3 and shape[1] > 1:
-            strides[2 * n + 1] = st[1]
-    return KVRows(k.data_ptr(), None if v is None else v.data_ptr(), *strides, _DTYPES[k.dtype], 0)
+        shape, vshape = (rows, problem.head_dim_v), (rows, problem.head_dim_qk - problem.head_dim_v)
+    kt, kh = _kv_part("k", k, shape, dt)
+    if v is None:
+        return KVRows(k.data_ptr(), None, kt, kh, 0, 0, _DTYPES[dt], 0)
+    vt, vh = _kv_part("v", v, vshape, dt)
+    return KVRows(k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, _DTYPES[dt], 0)
 
 
 def kv_append(problem: AttentionProblem, k_new: torch.Tensor, v_new: Optional[torch.Tensor] = None,

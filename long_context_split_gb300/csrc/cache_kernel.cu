@@ -12,12 +12,13 @@
 // rows the chain of dependent reads (indptr, length, page id).  So the row's
 // data is loaded before that chain is waited for (append), a warp finds a
 // row's request with one 32-way probe per factor of 32 in the batch size, and
-// each thread keeps a fixed column of the token (part, head, 8 elements) and
-// walks tokens with kUnroll of them in flight.
+// each thread keeps a fixed column of the token (part, head, 8 or 16 elements) and
+// walks tokens with several of them in flight.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "internal.h"
 
@@ -25,73 +26,109 @@ namespace skv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;        // tokens in flight per thread
 constexpr int kMaxTokens = 64;    // tokens per block
 
 struct E4M3 {
     uint8_t code;
 };
 
-// VEC consecutive elements in registers as float32
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&x)[VEC]) {
-    if constexpr (VEC == 1) {
-        if constexpr (sizeof(T) == 4) x[0] = *(const float*)p;
-        else if constexpr (sizeof(T) == 2) x[0] = __bfloat162float(*(const __nv_bfloat16*)p);
-        else x[0] = (float)*(const __nv_fp8_e4m3*)p;
-    } else if constexpr (sizeof(T) == 4) {
+// BYTES consecutive bytes in registers
+template <int BYTES>
+struct Raw {
+    uint32_t w[(BYTES + 3) / 4];
+};
+
+// streaming loads and stores of a piece in accesses of at most 32 bytes
+template <int BYTES>
+__device__ __forceinline__ void load_raw(Raw<BYTES>& r, const void* p) {
+    if constexpr (BYTES >= 32) {
 #pragma unroll
-        for (int k = 0; k < VEC / 4; ++k) {
-            const float4 v = __ldcs((const float4*)p + k);
-            x[4 * k] = v.x; x[4 * k + 1] = v.y; x[4 * k + 2] = v.z; x[4 * k + 3] = v.w;
+        for (int k = 0; k < BYTES / 32; ++k) {
+            uint32_t* w = r.w + 8 * k;
+            asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                         : "l"((const char*)p + 32 * k));
         }
-    } else if constexpr (sizeof(T) == 2) {
+    } else if constexpr (BYTES == 16) {
         const uint4 v = __ldcs((const uint4*)p);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            x[2 * k] = __uint_as_float(w[k] << 16);
-            x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-        }
-    } else {
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else if constexpr (BYTES == 8) {
         const uint2 v = __ldcs((const uint2*)p);
-        const uint32_t w[2] = {v.x, v.y};
+        r.w[0] = v.x; r.w[1] = v.y;
+    } else if constexpr (BYTES == 4) {
+        r.w[0] = *(const uint32_t*)p;
+    } else if constexpr (BYTES == 2) {
+        r.w[0] = *(const uint16_t*)p;
+    } else {
+        r.w[0] = *(const uint8_t*)p;
+    }
+}
+
+template <int BYTES>
+__device__ __forceinline__ void store_raw(void* p, const Raw<BYTES>& r) {
+    if constexpr (BYTES >= 32) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu),
-                                                             __NV_E4M3);
-            const float2 f = __half22float2(__half2(h));
+        for (int k = 0; k < BYTES / 32; ++k) {
+            const uint32_t* w = r.w + 8 * k;
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"((char*)p + 32 * k), "r"(w[0]), "r"(w[1]),
+                         "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
+        }
+    } else if constexpr (BYTES == 16) {
+        *(uint4*)p = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    } else if constexpr (BYTES == 8) {
+        *(uint2*)p = make_uint2(r.w[0], r.w[1]);
+    } else if constexpr (BYTES == 4) {
+        *(uint32_t*)p = r.w[0];
+    } else if constexpr (BYTES == 2) {
+        *(uint16_t*)p = (uint16_t)r.w[0];
+    } else {
+        *(uint8_t*)p = (uint8_t)r.w[0];
+    }
+}
+
+// the VEC elements of type T in a piece, as float32
+template <typename T, int VEC>
+__device__ __forceinline__ void decode(const Raw<VEC * (int)sizeof(T)>& r, float (&x)[VEC]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) x[k] = __uint_as_float(r.w[k]);
+    } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) x[k] = __uint_as_float((k & 1) ? r.w[k / 2] & 0xFFFF0000u : r.w[k / 2] << 16);
+    } else {
+#pragma unroll
+        for (int k = 0; k < (VEC + 1) / 2; ++k) {
+            const uint32_t two = (r.w[k / 2] >> (16 * (k & 1))) & 0xFFFFu;
+            const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
             x[2 * k] = f.x;
-            x[2 * k + 1] = f.y;
+            if (2 * k + 1 < VEC) x[2 * k + 1] = f.y;
         }
     }
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-    return lo | (hi << 16);
-}
-
+// float32 values rounded to type T (E4M3: saturated), packed
 template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&x)[VEC]) {
-    if constexpr (VEC == 1) {
-        if constexpr (sizeof(T) == 4) *(float*)p = x[0];
-        else if constexpr (sizeof(T) == 2) *(__nv_bfloat16*)p = __float2bfloat16_rn(x[0]);
-        else *(uint8_t*)p = __nv_cvt_float_to_fp8(x[0], __NV_SATFINITE, __NV_E4M3);
-    } else if constexpr (sizeof(T) == 4) {
+__device__ __forceinline__ void encode(Raw<VEC * (int)sizeof(T)>& r, const float (&x)[VEC]) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int k = 0; k < VEC / 4; ++k)
-            ((float4*)p)[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        for (int k = 0; k < VEC; ++k) r.w[k] = __float_as_uint(x[k]);
+    } else if constexpr (VEC == 1) {
+        if constexpr (sizeof(T) == 2) r.w[0] = __bfloat16_as_ushort(__float2bfloat16_rn(x[0]));
+        else r.w[0] = __nv_cvt_float_to_fp8(x[0], __NV_SATFINITE, __NV_E4M3);
     } else if constexpr (sizeof(T) == 2) {
-        *(uint4*)p = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+#pragma unroll
+        for (int k = 0; k < VEC / 2; ++k) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+            r.w[k] = *reinterpret_cast<const uint32_t*>(&v);
+        }
     } else {
-        *(uint2*)p = make_uint2(pack_e4m3(x[0], x[1], x[2], x[3]), pack_e4m3(x[4], x[5], x[6], x[7]));
+#pragma unroll
+        for (int k = 0; k < VEC / 4; ++k) {
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * k], x[4 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * k + 2], x[4 * k + 3]), __NV_SATFINITE, __NV_E4M3);
+            r.w[k] = lo | (hi << 16);
+        }
     }
 }
 
@@ -144,9 +181,15 @@ __device__ __forceinline__ void locate(const CacheRowsArgs& a, int r0, int n, lo
     }
 }
 
-// blockDim = (columns, token lanes); a thread's column is (part, head, VEC elements)
+// blockDim = (columns, token lanes); a thread's column is (part, head, VEC elements).  Pieces
+// stay in registers as they were read (kUnroll tokens of them, 32 registers) until they are
+// converted and stored.
 template <typename Rows, typename Cache, int VEC, bool APPEND>
 __global__ void __launch_bounds__(kThreads) cache_rows_kernel(CacheRowsArgs a, int tokens_per_block) {
+    using Src = std::conditional_t<APPEND, Rows, Cache>;
+    using Dst = std::conditional_t<APPEND, Cache, Rows>;
+    constexpr int kSrc = VEC * (int)sizeof(Src), kDst = VEC * (int)sizeof(Dst);
+    constexpr int kUnroll = VEC == 1 ? 4 : std::min(8, std::max(2, 128 / kSrc));
     __shared__ long long where[kMaxTokens];
     const int r0 = blockIdx.x * tokens_per_block;
     const int n = min(tokens_per_block, a.rows - r0);
@@ -161,12 +204,13 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(CacheRowsArgs a, i
         const int h = cc / per, e = (cc % per) * VEC;
         Rows* rows = (Rows*)p.rows + (size_t)r0 * p.token_stride + h * p.head_stride + e;
         Cache* cache = (Cache*)p.cache + (size_t)h * a.page_size * p.row_width + p.col + e;
+        const float scale = p.scale;
         for (int t0 = threadIdx.y; t0 < n || !located; t0 += kUnroll * blockDim.y) {
-            float x[kUnroll][VEC];
+            Raw<kSrc> src[kUnroll];
             if (APPEND) {
 #pragma unroll
                 for (int k = 0; k < kUnroll; ++k)
-                    if (on && t0 + k * (int)blockDim.y < n) load_vec<Rows, VEC>(rows + (t0 + k * blockDim.y) * p.token_stride, x[k]);
+                    if (on && t0 + k * (int)blockDim.y < n) load_raw<kSrc>(src[k], rows + (t0 + k * blockDim.y) * p.token_stride);
             }
             if (!located) {   // once per block, on every thread's first pass
                 locate<APPEND>(a, r0, n, where);
@@ -174,71 +218,77 @@ __global__ void __launch_bounds__(kThreads) cache_rows_kernel(CacheRowsArgs a, i
                 located = true;
             }
             if (!on) break;
-            long long w[kUnroll];
-#pragma unroll
-            for (int k = 0; k < kUnroll; ++k) w[k] = t0 + k * (int)blockDim.y < n ? where[t0 + k * blockDim.y] : -2;
-            if (APPEND) {
+            if (!APPEND) {
 #pragma unroll
                 for (int k = 0; k < kUnroll; ++k) {
-                    if (w[k] < 0) continue;
+                    const long long w = t0 + k * (int)blockDim.y < n ? where[t0 + k * blockDim.y] : -2;
+#pragma unroll
+                    for (int j = 0; j < (kSrc + 3) / 4; ++j) src[k].w[j] = 0u;   // a refused row reads as zeros
+                    if (w >= 0) load_raw<kSrc>(src[k], cache + w * p.row_width);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k) {
+                const int t = t0 + k * (int)blockDim.y;
+                if (t >= n) break;
+                const long long w = where[t];
+                if (APPEND ? w < 0 : w == -2) continue;
+                Dst* to = APPEND ? (Dst*)(cache + w * p.row_width) : (Dst*)(rows + t * p.token_stride);
+                if constexpr (std::is_same_v<Src, Dst>) {
+                    store_raw<kSrc>(to, src[k]);
+                } else {
+                    float x[VEC];
+                    decode<Src, VEC>(src[k], x);
                     if constexpr (sizeof(Cache) == 1) {
 #pragma unroll
-                        for (int j = 0; j < VEC; ++j) x[k][j] = x[k][j] / p.scale;
+                        for (int j = 0; j < VEC; ++j) x[j] = APPEND ? x[j] / scale : x[j] * scale;
                     }
-                    store_vec<Cache, VEC>(cache + w[k] * p.row_width, x[k]);
-                }
-            } else {
-#pragma unroll
-                for (int k = 0; k < kUnroll; ++k) {
-#pragma unroll
-                    for (int j = 0; j < VEC; ++j) x[k][j] = 0.f;   // a refused row reads as zeros
-                    if (w[k] >= 0) load_vec<Cache, VEC>(cache + w[k] * p.row_width, x[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < kUnroll; ++k) {
-                    if (w[k] == -2) continue;
-                    if constexpr (sizeof(Cache) == 1) {
-#pragma unroll
-                        for (int j = 0; j < VEC; ++j) x[k][j] *= p.scale;
-                    }
-                    store_vec<Rows, VEC>(rows + (t0 + k * blockDim.y) * p.token_stride, x[k]);
+                    Raw<kDst> dst;
+                    encode<Dst, VEC>(dst, x);
+                    store_raw<kDst>(to, dst);
                 }
             }
         }
     }
 }
 
-// 8 elements per access where every row and entry address is a multiple of 16 bytes (8 for
-// E4M3 entries); one element otherwise
-bool vectors_fit(const CacheRowsArgs& a, int rows_size, int cache_size) {
+// Whether every row and entry address is a multiple of a piece's access (VEC elements, at most 32 bytes)
+bool vectors_fit(const CacheRowsArgs& a, int vec, int rows_size, int cache_size) {
+    const int rb = std::min(32, vec * rows_size), cb = std::min(32, vec * cache_size);
     for (const CachePart& p : a.part) {
         if (p.width == 0) continue;
-        const int ra = 16 / rows_size, ca = cache_size == 1 ? 8 : 16 / cache_size;
-        if (p.width % 8 || p.token_stride % ra || p.head_stride % ra || ((uintptr_t)p.rows & 15)) return false;
-        if (p.row_width % ca || p.col % ca || ((uintptr_t)p.cache & (cache_size == 1 ? 7 : 15))) return false;
+        if (p.width % vec || p.token_stride * rows_size % rb || p.head_stride * rows_size % rb || (uintptr_t)p.rows % rb) return false;
+        if (p.row_width * cache_size % cb || p.col * cache_size % cb || (uintptr_t)p.cache % cb) return false;
     }
     return true;
 }
 
-template <typename Rows, typename Cache, bool APPEND>
-cudaError_t launch_rows(const CacheRowsArgs& a, cudaStream_t s) {
+template <typename Rows, typename Cache, int VEC, bool APPEND>
+cudaError_t launch_vec(const CacheRowsArgs& a, cudaStream_t s) {
     int dev = 0, sms = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const bool vec = vectors_fit(a, sizeof(Rows), sizeof(Cache));
-    const int v = vec ? 8 : 1;
-    const int cols = a.heads * (a.part[0].width / v) + a.heads * (a.part[1].width / v);
+    const int cols = a.heads * (a.part[0].width / VEC) + a.heads * (a.part[1].width / VEC);
     const int bx = std::min(kThreads, (cols + 31) / 32 * 32);
     const int by = std::max(1, kThreads / bx);
-    // tokens per block: enough that a thread has kUnroll in flight, fewer while that leaves SMs idle
-    const int per = std::min(kMaxTokens, std::max(by, std::min(by * kUnroll, a.rows / (2 * sms))));
+    // tokens per block: about 8 blocks per SM (as many as fit), so that a block waits for its chain of
+    // dependent reads once for many tokens; few rows get a block per `by` tokens
+    const int per = std::min(kMaxTokens, std::max(by, a.rows / (8 * sms)));
     const int blocks = (a.rows + per - 1) / per;
-    const dim3 block(bx, by);
     ProfileScope ps(APPEND ? SPLITKV_KERNEL_KV_APPEND : SPLITKV_KERNEL_KV_GATHER, s);
-    if (vec) cache_rows_kernel<Rows, Cache, 8, APPEND><<<blocks, block, 0, s>>>(a, per);
-    else cache_rows_kernel<Rows, Cache, 1, APPEND><<<blocks, block, 0, s>>>(a, per);
+    cache_rows_kernel<Rows, Cache, VEC, APPEND><<<blocks, dim3(bx, by), 0, s>>>(a, per);
     return cudaGetLastError();
+}
+
+// The widest piece that every address allows: 16 elements for E4M3 caches (16 bytes of codes), 8 for
+// others, element by element for odd widths and offsets
+template <typename Rows, typename Cache, bool APPEND>
+cudaError_t launch_rows(const CacheRowsArgs& a, cudaStream_t s) {
+    if constexpr (sizeof(Cache) == 1)
+        if (vectors_fit(a, 16, sizeof(Rows), 1)) return launch_vec<Rows, Cache, 16, APPEND>(a, s);
+    if (vectors_fit(a, 8, sizeof(Rows), sizeof(Cache))) return launch_vec<Rows, Cache, 8, APPEND>(a, s);
+    return launch_vec<Rows, Cache, 1, APPEND>(a, s);
 }
 
 template <bool APPEND>

@@ -12,13 +12,13 @@
 // vocabulary, read once.  A cluster of CTAs takes a request, a warp a
 // contiguous segment of the vocabulary: one pass sums every segment; the
 // segments' sums, shared through distributed shared memory, show which one the
-// draw falls in, and that warp reads its own segment again (from L2).
+// draw falls in, and the CTA that owns it reads that segment again (from L2), a step of 128
+// tokens per warp, and sums, picks the step and then the token in the same way.
 //
-// Arithmetic: products and differences of two float32 values are exact in
-// float64, but float64 adds run at a small fraction of the float32 rate, so a
-// lane sums its weights as an unevaluated pair of float32 (each difference and
-// each addition split into a rounded value and its exact error) and the pairs
-// become float64 once per lane.  The order of every sum is fixed.
+// Arithmetic: float64 adds run at 1/64 of the float32 rate here (a scan of 16 sums by every
+// warp of a CTA took 7 us), so sums are unevaluated pairs of float32, about 48 bits: each
+// difference and each addition is split into a rounded value and its exact error.
+// The order of every sum is fixed.
 #include <algorithm>
 
 #include "internal.h"
@@ -31,8 +31,9 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 constexpr int kLoads = 4;          // loads of p and of q in flight per lane
 
+// hi + lo, |lo| at most half a unit in the last place of hi once normalised
 struct Pair {
-    float hi = 0.f, lo = 0.f;
+    float hi, lo;
 };
 
 // s + e = a + b exactly
@@ -42,13 +43,40 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
     e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
 }
 
-// the weight of a token, max(p - q, 0), as hi + lo (NaN and negative weigh nothing)
+__device__ __forceinline__ Pair normal(float s, float e) {
+    Pair r;
+    r.hi = __fadd_rn(s, e);
+    r.lo = __fsub_rn(e, __fsub_rn(r.hi, s));
+    return r;
+}
+
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+    float s, e;
+    two_sum(a.hi, b.hi, s, e);
+    return normal(s, __fadd_rn(e, __fadd_rn(a.lo, b.lo)));
+}
+
+__device__ __forceinline__ Pair sub(Pair a, Pair b) { return add(a, Pair{-b.hi, -b.lo}); }
+
+__device__ __forceinline__ Pair scale(float u, Pair a) {
+    const float p = __fmul_rn(u, a.hi);
+    return normal(p, __fmaf_rn(u, a.lo, __fmaf_rn(u, a.hi, -p)));
+}
+
+__device__ __forceinline__ bool greater(Pair a, Pair b) { return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo); }
+
+__device__ __forceinline__ Pair shfl(Pair a, int from) {
+    return Pair{__shfl_sync(0xffffffffu, a.hi, from), __shfl_sync(0xffffffffu, a.lo, from)};
+}
+
+// the weight of a token, max(p - q, 0) (NaN and negative weigh nothing)
 __device__ __forceinline__ Pair weight(float p, float q) {
-    Pair w;
+    Pair w{0.f, 0.f};
     if (p > q) two_sum(p, -q, w.hi, w.lo);
     return w;
 }
 
+// s += w without normalising: lo only collects errors far below hi
 __device__ __forceinline__ void accumulate(Pair& s, Pair w) {
     float hi, e;
     two_sum(s.hi, w.hi, hi, e);
@@ -96,18 +124,74 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ double remote_double(const double* local, uint32_t rank) {
+__device__ __forceinline__ Pair remote_pair(const Pair* local, uint32_t rank) {
     uint32_t addr;
-    double v;
+    Pair v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.hi), "=f"(v.lo) : "r"(addr) : "memory");
     return v;
+}
+
+// sum over the warp (lane 0's value is the one used)
+__device__ __forceinline__ Pair warp_sum(Pair s) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+        s = add(s, Pair{__shfl_xor_sync(0xffffffffu, s.hi, d), __shfl_xor_sync(0xffffffffu, s.lo, d)});
+    return s;
+}
+
+// sum over the lanes up to this one
+__device__ __forceinline__ Pair warp_scan(Pair x, int lane) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const Pair y{__shfl_up_sync(0xffffffffu, x.hi, d), __shfl_up_sync(0xffffffffu, x.lo, d)};
+        if (lane >= d) x = add(y, x);
+    }
+    return x;
+}
+
+struct Pick {
+    Pair before;   // sum of the weights before the picked entry
+    int index;     // the picked entry; -1: no weight
+    bool over;     // its running sum exceeds the draw (else it is the last entry with weight)
+};
+
+// The lowest of 32 * N entries (N consecutive ones per lane, `excl` the sum before the
+// lane's) whose running sum exceeds `at`, among those with weight; the last one with weight if
+// none does.  The same result in every lane.
+template <int N>
+__device__ __forceinline__ Pick pick(const Pair (&part)[N], Pair excl, Pair at, int lane) {
+    Pair c = excl, over_before = excl, last_before = excl;
+    int over = -1, last = -1;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const Pair next = add(c, part[k]);
+        if (part[k].hi > 0.f) {
+            last = k;
+            last_before = c;
+            if (over < 0 && greater(next, at)) {
+                over = k;
+                over_before = c;
+            }
+        }
+        c = next;
+    }
+    const unsigned has = __ballot_sync(0xffffffffu, last >= 0), hit = __ballot_sync(0xffffffffu, over >= 0);
+    const int from = hit ? __ffs(hit) - 1 : has ? 31 - __clz(has) : 0;
+    Pick d;
+    d.over = hit != 0;
+    d.before = shfl(hit ? over_before : last_before, from);
+    d.index = __shfl_sync(0xffffffffu, hit ? over : last, from);
+    if (d.index >= 0) d.index += N * from;
+    return d;
 }
 
 template <int VEC>
 __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(VerifyArgs a, int cluster) {
-    __shared__ double seg_sum[2][kWarps];
-    __shared__ int s_accepted;
+    __shared__ __align__(8) Pair seg_sum[2][kWarps], step_sum[kWarps];
+    __shared__ Pair s_at;
+    __shared__ Pick s_seg;
+    __shared__ int s_accepted, s_token;
     const int b = blockIdx.x / cluster, rank = (int)cluster_ctarank();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r0 = a.qo_indptr[b], rows = a.qo_indptr[b + 1] - r0, n = rows - 1;
@@ -161,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(VerifyArgs a
     bool mine = false, none = false;
     // the second pass, over p alone, only where max(p - q, 0) is zero everywhere
     for (int pass = 0; pass < 2; ++pass) {
-        Pair s;
+        Pair s{0.f, 0.f};
         for (int v = v0 + lane * VEC; v < v1; v += kLoads * kStep) {
             Tokens<VEC> t[kLoads];
 #pragma unroll
@@ -171,102 +255,76 @@ __global__ void __launch_bounds__(kThreads, 2) verify_drafts_kernel(VerifyArgs a
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) accumulate(s, weight(t[k].p[j], t[k].q[j]));
         }
-        double sum = (double)s.hi + (double)s.lo;
-#pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) seg_sum[pass][warp] = sum;
+        s = warp_sum(s);
+        if (lane == 0) seg_sum[pass][warp] = s;
         cluster_sync();
-        // ---- the segment of the draw: every warp scans all segments' sums the same way ----
-        double part[kMaxCluster * kWarps / 32], run = 0.0;
+        // ---- the segment of the draw: warp 0 of every CTA scans all segments' sums the same way ----
+        if (warp == 0) {
+            constexpr int kPer = kMaxCluster * kWarps / 32;      // consecutive segments per lane
+            Pair part[kPer], own{0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < kMaxCluster * kWarps / 32; ++k) {
-            const int i = 32 * k + lane;
-            part[k] = i < warps ? remote_double(&seg_sum[pass][i % kWarps], i / kWarps) : 0.0;
-        }
-        double before = 0.0, total = 0.0;
-        int owner = -1, last = -1;
-        double incl[kMaxCluster * kWarps / 32];
-#pragma unroll
-        for (int k = 0; k < kMaxCluster * kWarps / 32; ++k) {
-            double x = part[k];
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
+            for (int k = 0; k < kPer; ++k) {
+                const int i = kPer * lane + k;
+                part[k] = i < warps ? remote_pair(&seg_sum[pass][i % kWarps], i / kWarps) : Pair{0.f, 0.f};
+                own = add(own, part[k]);
             }
-            incl[k] = run + x;
-            run = __shfl_sync(0xffffffffu, incl[k], 31);
+            const Pair incl = warp_scan(own, lane);
+            const Pair at = scale(a.sample_u[b], shfl(incl, 31));
+            const Pick d = pick<kPer>(part, sub(incl, own), at, lane);
+            if (lane == 0) {
+                s_at = at;
+                s_seg = d;
+            }
         }
-        total = run;
-        if (!(total > 0.0)) {
-            if (q == nullptr && excluded < 0) {          // p itself has no mass: no token
+        __syncthreads();
+        const int segment = s_seg.index;
+        if (segment < 0) {                                       // no weight at all
+            if (q == nullptr && excluded < 0) {
                 none = true;
                 break;
             }
             q = nullptr;
             excluded = -1;
+            __syncthreads();
             continue;
         }
-        const double at = (double)a.sample_u[b] * total;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster * kWarps / 32; ++k) {
-            const unsigned has = __ballot_sync(0xffffffffu, part[k] > 0.0);
-            const unsigned over = __ballot_sync(0xffffffffu, part[k] > 0.0 && incl[k] > at);
-            if (has) last = 32 * k + 31 - __clz(has);
-            if (over && owner < 0) owner = 32 * k + __ffs(over) - 1;
-        }
-        if (owner < 0) owner = last;                     // u at the very end of the distribution
-        mine = owner == w;
-        if (!mine) break;
-#pragma unroll
-        for (int k = 0; k < kMaxCluster * kWarps / 32; ++k) {
-            const double excl = __shfl_sync(0xffffffffu, incl[k] - part[k], owner & 31);
-            if (k == owner / 32) before = excl;
-        }
-        // ---- the token inside the segment: steps of 32 * VEC tokens in order ----
-        for (int s0 = v0; s0 < v1; s0 += kStep) {
-            const int v = s0 + lane * VEC;
+        if (segment / kWarps != rank) break;
+        // ---- the token inside the segment, by the CTA that owns it: a step per warp ----
+        mine = true;
+        const int g0 = segment * seg, g1 = min(g0 + seg, V);
+        const Pair at = s_at;
+        Pair before = s_seg.before;
+        for (int base = g0; base < g1; base += kWarps * kStep) {
             Tokens<VEC> t;
-            load_tokens<VEC>(t, p, q, v, v1, excluded);
-            Pair m[VEC];
-            Pair sum_lane;
+            const int v = base + warp * kStep + lane * VEC;
+            load_tokens<VEC>(t, p, q, v, g1, excluded);
+            Pair m[VEC], sum{0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < VEC; ++j) {
                 m[j] = weight(t.p[j], t.q[j]);
-                accumulate(sum_lane, m[j]);
+                sum = add(sum, m[j]);
             }
-            const double own = (double)sum_lane.hi + (double)sum_lane.lo;
-            double x = own;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const double y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d) x += y;
+            const Pair step = warp_sum(sum);
+            if (lane == 0) step_sum[warp] = step;
+            __syncthreads();
+            // every warp picks the step (16 sums, a lane each)
+            const Pair part[1] = {lane < kWarps ? step_sum[lane] : Pair{0.f, 0.f}};
+            const Pair incl = warp_scan(part[0], lane);
+            const Pick d = pick<1>(part, add(before, sub(incl, part[0])), at, lane);
+            if (d.index == warp) {
+                const Pair own = warp_scan(sum, lane);
+                const Pick in = pick<VEC>(m, add(d.before, sub(own, sum)), at, lane);
+                if (lane == 0) s_token = base + warp * kStep + in.index;
             }
-            const unsigned has = __ballot_sync(0xffffffffu, own > 0.0);
-            const unsigned over = __ballot_sync(0xffffffffu, own > 0.0 && before + x > at);
-            const int pick = over ? __ffs(over) - 1 : has ? 31 - __clz(has) : -1;
-            if (pick >= 0) {
-                // within the lane: the first token over the draw, else its last one with mass
-                double c = before + (x - own);
-                int found = -1, tail = -1;
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) {
-                    c += (double)m[j].hi + (double)m[j].lo;
-                    if (m[j].hi > 0.f) {
-                        tail = v + j;
-                        if (found < 0 && c > at) found = v + j;
-                    }
-                }
-                const int cand = over && found >= 0 ? found : tail;
-                token = __shfl_sync(0xffffffffu, cand, pick);
-            }
-            if (over) break;
-            before += __shfl_sync(0xffffffffu, x, 31);
+            before = add(before, shfl(incl, 31));
+            __syncthreads();
+            if (d.index >= 0) token = s_token;
+            if (d.over) break;
         }
         break;
     }
-    // ---- outputs: one warp has the token; no mass anywhere gives -1 ----
-    if (mine && lane == 0) a.out_tokens[r0 + acc] = token;
+    // ---- outputs: one CTA has the token; no weight anywhere gives -1 ----
+    if (mine && threadIdx.x == 0) a.out_tokens[r0 + acc] = token;
     if (rank == 0) {
         if (none && threadIdx.x == 0) a.out_tokens[r0 + acc] = -1;
         for (int i = threadIdx.x; i < rows; i += kThreads)
