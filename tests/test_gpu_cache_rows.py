@@ -216,6 +216,32 @@ def test_append_a_broadcast_row_and_a_large_batch():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("scale", [0.05, 0.0625, 1.0 / 3.0, 1e-3, 7.77, 1.0, 448.0, 1e-30, 2.0 ** -126, 3e38])
+def test_every_bf16_value_quantises_as_the_quotient(scale):
+    # all 65,536 bit patterns (infinities and NaN among them), for scales whose quotient takes a
+    # reciprocal and for extreme ones: codes equal those of the float32 quotient
+    B = Batch([64], [64], cache="e4m3", heads=8, dim=128, page=64, seed=40)
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(64, 8, 128)
+    problem = B.make_problem(k_scale=scale, v_scale=scale)
+    skv.kv_append(problem, x.cuda(), x.cuda())
+    torch.cuda.synchronize()
+    page, slot = B.slots(0, 0, 64)
+    k = B.k.clone()
+    k[page, :, slot] = encode(x, "e4m3", scale)
+    assert same_codes(B.k_dev, k)
+    # float32 rows next to every border between two codes
+    at = torch.from_numpy((_ALL[1:] + _ALL[:-1]) / 2 * np.float32(scale)).float()
+    near = torch.stack([torch.nextafter(at, torch.zeros(())), at, torch.nextafter(at, torch.full((), 3e38))]).reshape(-1)
+    f = torch.zeros(64 * 8 * 128)
+    f[:len(near)], f[1000:1000 + len(near)] = near, -near
+    f = f.view(64, 8, 128)
+    skv.kv_append(problem, f.cuda(), f.cuda())
+    torch.cuda.synchronize()
+    k[page, :, slot] = encode(f, "e4m3", scale)
+    assert same_codes(B.k_dev, k)
+
+
+@pytest.mark.gpu
 def test_append_refuses_bad_pages_and_reports_them():
     B = Batch([40, 40], [20, 20], cache="bf16", seed=5)
     g = torch.Generator().manual_seed(9)
