@@ -459,7 +459,7 @@ splitkv_status splitkv_kv_gather(const splitkv_problem *prob, const int32_t *kv_
  *    attended: 2 * 512 * 256 operations per cached token and head, 640 per
  *    (query, key) pair.  For prompts and chunks of new tokens.
  *  absorbed -- W_uk is applied to the queries and W_uv to the outputs, and the
- *    latent rows themselves are attended (splitkv_decode on a
+ *    latent rows themselves are attended (splitkv_partial on a
  *    576-wide problem).  For few query tokens per request.
  * The problem describes the latent cache and the batch: kind MLA, dtype BF16,
  * head_dim_qk 576, head_dim_v 512, scale > 0 (1 / sqrt(192) for these widths);
@@ -470,7 +470,7 @@ typedef struct {
     int64_t q_token_stride;          /* elements, a multiple of 8, >= num_q_heads * 192 */
     const void *w_kv_b;              /* device bf16 [num_q_heads][256][512]: per head W_uk's 128 rows, then W_uv's */
     void *out;                       /* device bf16 [total_q][num_q_heads][128] */
-    float *lse_out;                  /* device float32 [total_q][num_q_heads] or NULL (expanded form) */
+    float *lse_out;                  /* device float32 [total_q][num_q_heads] or NULL */
 } splitkv_latent_layer;
 
 /* Opaque host-side plan of the expanded form: its tasks, splits and workspace.  Built once per
@@ -511,17 +511,21 @@ splitkv_status splitkv_latent_expanded(const splitkv_problem *prob, const splitk
                                        int32_t *dev_error_word, splitkv_stream stream);
 
 /*
- * The two products of the absorbed form around splitkv_decode.
+ * The two ends of the absorbed form, around splitkv_partial on the 576-wide problem.
  * splitkv_latent_absorb_query: q_abs [total_q][num_q_heads][576] =
- *   (q_nope W_uk, q_rope), the q of the 576-wide problem; rounded to bf16.
- * splitkv_latent_project: layer->out [total_q][num_q_heads][128] = o_lat W_uv^T
- *   from splitkv_decode's out, o_lat [total_q][num_q_heads][512].
- * total_q is prob->qo_indptr_host[batch].  layer->out and lse_out (layer->q) are not
- * read by the first (second).  q_abs and o_lat: device bf16, 16-byte aligned.
+ *   (q_nope W_uk, q_rope), the q of that problem; rounded to bf16.  Device
+ *   bf16, 16-byte aligned; layer->out and lse_out are not used.
+ * splitkv_latent_project: merges the 512-wide partial states of every row (as
+ *   merge_states_typed does: o_part of o_part_dtype, lse_part, state_indptr) and
+ *   projects them: layer->out [total_q][num_q_heads][128] = o_lat W_uv^T, and
+ *   lse_out when it is given.  o_lat is float32 until it meets the weights
+ *   (as two bf16 parts).  layer->q is not used.
+ * total_q is prob->qo_indptr_host[batch].  dev_error_word: device int32 or NULL.
  */
 splitkv_status splitkv_latent_absorb_query(const splitkv_problem *prob, const splitkv_latent_layer *layer, void *q_abs,
                                            int32_t *dev_error_word, splitkv_stream stream);
-splitkv_status splitkv_latent_project(const splitkv_problem *prob, const splitkv_latent_layer *layer, const void *o_lat,
+splitkv_status splitkv_latent_project(const splitkv_problem *prob, const splitkv_latent_layer *layer, const void *o_part,
+                                      int32_t o_part_dtype, const float *lse_part, const int32_t *state_indptr,
                                       int32_t *dev_error_word, splitkv_stream stream);
 
 /* 1 when the expanded form is expected to be the faster one for the problem's lengths, 0 for the
@@ -709,7 +713,7 @@ typedef enum {
     SPLITKV_KERNEL_LATENT_EXPAND = 12,     /* keys and values of every head */
     SPLITKV_KERNEL_LATENT_ATTENTION = 13,  /* expanded latent attention */
     SPLITKV_KERNEL_LATENT_ABSORB = 14,     /* queries times W_uk */
-    SPLITKV_KERNEL_LATENT_PROJECT = 15,    /* latent outputs times W_uv^T */
+    SPLITKV_KERNEL_LATENT_PROJECT = 15,    /* merge of latent outputs, times W_uv^T */
     SPLITKV_KERNEL_COUNT = 16
 } splitkv_kernel;
 

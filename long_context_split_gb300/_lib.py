@@ -171,7 +171,8 @@ SIGNATURES = {
     "splitkv_latent_expanded": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, ctypes.POINTER(LatentLayer), _vp,
                                                ctypes.c_size_t, _vp, _vp]),
     "splitkv_latent_absorb_query": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(LatentLayer), _vp, _vp, _vp]),
-    "splitkv_latent_project": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(LatentLayer), _vp, _vp, _vp]),
+    "splitkv_latent_project": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(LatentLayer), _vp, _i32, _vp, _vp,
+                                              _vp, _vp]),
     "splitkv_latent_prefers_expanded": (_i32, [ctypes.POINTER(Problem)]),
     "splitkv_verify_drafts": (ctypes.c_int, [ctypes.POINTER(Verify), _vp, _vp]),
     "splitkv_read_device_error": (ctypes.c_int, [_vp, _vp, _i32, _ip, _vp]),
@@ -554,10 +555,10 @@ def latent_absorb_query(problem: AttentionProblem, layer: LatentLayer, q_abs: to
                                               _ptr(dev_error_word), _stream_handle(stream)))
 
 
-def latent_project(problem: AttentionProblem, layer: LatentLayer, o_lat: torch.Tensor,
-                   dev_error_word: Optional[torch.Tensor] = None, stream=None):
-    _check(load().splitkv_latent_project(ctypes.byref(problem._s), ctypes.byref(layer), _ptr(o_lat),
-                                         _ptr(dev_error_word), _stream_handle(stream)))
+def latent_project(problem: AttentionProblem, layer: LatentLayer, o_part: torch.Tensor, lse_part: torch.Tensor,
+                   state_indptr: torch.Tensor, dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    _check(load().splitkv_latent_project(ctypes.byref(problem._s), ctypes.byref(layer), _ptr(o_part), _DTYPES[o_part.dtype],
+                                         _ptr(lse_part), _ptr(state_indptr), _ptr(dev_error_word), _stream_handle(stream)))
 
 
 def latent_prefers_expanded(problem: AttentionProblem) -> bool:

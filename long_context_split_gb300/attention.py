@@ -109,10 +109,13 @@ class LatentAttention:
             _lib.latent_upload(self.plan, self.workspace, stream)
         else:
             self.q_abs = torch.empty(total, heads, 576, dtype=torch.bfloat16, device=dev)
-            self.o_lat = torch.empty(total, heads, 512, dtype=torch.bfloat16, device=dev)
             self.problem = make(self.q_abs)
-            self._decode = SplitKVAttention(self.problem, params, stream)
-            self.plan, self.workspace, self.error_word = self._decode.plan, self._decode.workspace, self._decode.error_word
+            base = SplitKVAttention(self.problem, params, stream)
+            self.plan, self.workspace, self.error_word = base.plan, base.workspace, base.error_word
+            self.state_indptr = base.state_indptr
+            states = max(1, self.plan.num_states)
+            self.o_part = torch.empty(states, 512, dtype=self.plan.partial_dtype, device=dev)
+            self.lse_part = torch.empty(states, dtype=torch.float32, device=dev)
 
     def __call__(self, q: torch.Tensor, out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, stream=None):
         """out [total_q, H, 128] bfloat16 (allocated when None); lse [total_q, H] float32, written when given."""
@@ -124,8 +127,8 @@ class LatentAttention:
             _lib.latent_expanded(p, self.plan, layer, self.workspace, self.error_word, stream)
         else:
             _lib.latent_absorb_query(p, layer, self.q_abs, self.error_word, stream)
-            _lib.splitkv_decode(p, self.plan, self.workspace, self.o_lat, lse, self.error_word, stream)
-            _lib.latent_project(p, layer, self.o_lat, self.error_word, stream)
+            _lib.splitkv_partial(p, self.plan, self.workspace, self.o_part, self.lse_part, self.error_word, stream)
+            _lib.latent_project(p, layer, self.o_part, self.lse_part, self.state_indptr, self.error_word, stream)
         return out
 
     def check_device_error(self, clear: bool = True):

@@ -88,7 +88,9 @@ cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s);
 cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s);
 // q_abs [total_q][H][576] = (q_nope W_uk | q_rope); a.q, a.w
 cudaError_t launch_latent_absorb(const LatentArgs& a, void* q_abs, cudaStream_t s);
-// out [total_q][H][128] = o_lat [total_q][H][512] W_uv^T; a.w, a.out
-cudaError_t launch_latent_project(const LatentArgs& a, const void* o_lat, cudaStream_t s);
+// out [total_q][H][128] = (merged latent output) W_uv^T from the 512-wide partial states of row
+// x = token * H + head, states indptr[x] .. indptr[x + 1]-1; a.w, a.out, a.lse_out
+cudaError_t launch_latent_project(const LatentArgs& a, const void* o_part, int part_bf16, const float* lse_part,
+                                  const int32_t* indptr, cudaStream_t s);
 
 }  // namespace skv

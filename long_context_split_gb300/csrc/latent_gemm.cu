@@ -5,7 +5,6 @@
 // Eq. 1 writes them as the up-projections of the latent c):
 //   expand   k = c W_uk^T, v = c W_uv^T      M = cached tokens, K = 512, N = 256
 //   absorb   q_lat = q_nope W_uk             M = query tokens,  K = 128, N = 512
-//   project  o = o_lat W_uv^T                M = query tokens,  K = 512, N = 128
 // One kernel body: tiles of 128 rows by N columns of one head, a TMA producer
 // warp, an MMA thread, and four epilogue warps that empty one accumulator while
 // the other fills (tensor memory holds two).  Both operands are staged in
@@ -16,9 +15,8 @@
 // product) and leave through shared memory by TMA stores of 32 rows x 64
 // columns, one epilogue warp's part each, which clip the rows past the tensor.
 //
-// What bounds them: absorb and project move 33.5 MB of weights for 128 heads
-// and few query rows (bytes); expand is 2 * 512 * 256 operations per token and
-// head (tensor cores).
+// What bounds them: absorb moves 16.8 MB of weights for 128 heads and few query
+// rows (bytes); expand is 2 * 512 * 256 operations per token and head (tensor cores).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -35,11 +33,11 @@ constexpr int kEpiWarps = 4;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kABytes = kM * 128;                // 128 rows x 64 columns
 
-enum Mode { kExpand, kAbsorb, kProject };
+enum Mode { kExpand, kAbsorb };
 
 template <int MODE>
 struct Cfg {
-    static constexpr int N = MODE == kProject ? 128 : 256;
+    static constexpr int N = 256;
     static constexpr int K = MODE == kAbsorb ? 128 : 512;
     static constexpr int KB = K / 64;                        // k-blocks
     static constexpr int B_BYTES = N * 128;                  // N x 64 elements
@@ -158,9 +156,6 @@ latent_gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant
                     if (MODE == kExpand) {
                         tma_2d(sa, &ma, 64 * kb, x.m0, full);
                         tma_2d(sb, &mb, 64 * kb, x.h * kLatW, full);
-                    } else if (MODE == kProject) {
-                        tma_2d(sa, &ma, x.h * kLatC + 64 * kb, x.m0, full);
-                        tma_2d(sb, &mb, 64 * kb, x.h * kLatW + kLatNope, full);
                     } else {
                         // 64 key rows of W_uk by 256 latent columns: four boxes, columns innermost
                         tma_2d(sa, &ma, x.h * kLatQ + 64 * kb, x.m0, full);
@@ -228,12 +223,19 @@ latent_gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant
             const int y = x.m0 + 32 * quad;
             if (MODE == kAbsorb && x.half == 0) {
                 // the rotary columns pass through: 128 bytes of each of the warp's rows
-                for (int i = lane; i < 32 * 8; i += 32) {
-                    const int r = y + (i >> 3);
-                    if (r < a.total_q) {
-                        const uint4 v = *((const uint4*)((const __nv_bfloat16*)a.q + (size_t)r * a.q_stride + x.h * kLatQ + kLatNope) + (i & 7));
-                        *((uint4*)((__nv_bfloat16*)q_abs + ((size_t)r * a.heads + x.h) * kLatRow + kLatC) + (i & 7)) = v;
-                    }
+                // (eight loads in flight per lane: one after the other they cost 6 us a call)
+                uint4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = y + 4 * k + (lane >> 3);
+                    if (r < a.total_q)
+                        v[k] = *((const uint4*)((const __nv_bfloat16*)a.q + (size_t)r * a.q_stride + x.h * kLatQ + kLatNope) + (lane & 7));
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int r = y + 4 * k + (lane >> 3);
+                    if (r < a.total_q)
+                        *((uint4*)((__nv_bfloat16*)q_abs + ((size_t)r * a.heads + x.h) * kLatRow + kLatC) + (lane & 7)) = v[k];
                 }
             }
             if (!warp_wait(smem_u32(&B.acc_full[buf]), (n >> 1) & 1, abort_flag, lane)) {
@@ -286,7 +288,7 @@ latent_gemm_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant
                         if (f16) tma_store_2d(&mo2, src, c - kLatNope, yo);
                         else tma_store_2d(&mo, src, c, yo);
                     } else if (y < a.total_q) {
-                        tma_store_2d(&mo, src, MODE == kProject ? x.h * kLatV + c : x.h * kLatRow + x.half * 256 + c, y);
+                        tma_store_2d(&mo, src, x.h * kLatRow + x.half * 256 + c, y);
                     }
                     store_commit();
                 }
@@ -420,18 +422,6 @@ cudaError_t launch_latent_absorb(const LatentArgs& a, void* q_abs, cudaStream_t 
     if ((e = make_map(&mo, q_abs, (long long)a.heads * kLatRow, a.total_q, (long long)a.heads * kLatRow, 64, 32)) != cudaSuccess)
         return e;
     return launch_gemm<kAbsorb>(a, ma, mb, mo, mo, q_abs, (a.total_q + kM - 1) / kM, SPLITKV_KERNEL_LATENT_ABSORB, s);
-}
-
-cudaError_t launch_latent_project(const LatentArgs& a, const void* o_lat, cudaStream_t s) {
-    if (a.total_q <= 0) return cudaSuccess;
-    CUtensorMap ma, mb, mo;
-    cudaError_t e;
-    if ((e = make_map(&ma, o_lat, (long long)a.heads * kLatC, a.total_q, (long long)a.heads * kLatC, 64, kM)) != cudaSuccess)
-        return e;
-    if ((e = make_map(&mb, a.w, kLatC, (long long)a.heads * kLatW, kLatC, 64, kLatV)) != cudaSuccess) return e;
-    if ((e = make_map(&mo, a.out, (long long)a.heads * kLatV, a.total_q, (long long)a.heads * kLatV, 64, 32)) != cudaSuccess)
-        return e;
-    return launch_gemm<kProject>(a, ma, mb, mo, mo, nullptr, (a.total_q + kM - 1) / kM, SPLITKV_KERNEL_LATENT_PROJECT, s);
 }
 
 }  // namespace skv

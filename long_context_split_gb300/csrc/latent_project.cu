@@ -1,0 +1,270 @@
+// The end of absorbed latent attention in one kernel: the splits' partial states of
+// each (token, head) are merged (LiquidCP Eq. 1) and the merged 512-wide latent
+// output is projected by the head's W_uv.
+//
+// What it computes: o_lat = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp(lse_s),
+// out = o_lat W_uv^T, a CTA per head and 32 tokens.
+//
+// What bounds it: bytes (128 KB of weights per head, 2 KB per state) and, for one
+// token, the chain weights -> states -> product.  So the weights' copy starts first;
+// the states are read with eight 16-byte loads in flight per thread, and when there are
+// fewer than four tokens the splits of a row are shared out over the CTA's four groups of
+// 128 threads.  The product is taken transposed, D[v][token] = W_uv[v][:] . o_lat[token][:]
+// (M = 128 value columns, N = 32 tokens, K = 512), so that few tokens waste little.
+//
+// o_lat stays float32 until it meets the weights, as a bf16 high part and a bf16
+// residual (two products with the same weights, 16 significant bits): rounding it to
+// one bf16 would cost as much as the result's own rounding.
+#include "latent.h"
+#include "tc_common.cuh"
+
+namespace skv {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kGroups = kThreads / 128;
+constexpr int kTok = 32;                             // tokens per CTA (N of the product)
+constexpr int kBoxes = kLatC / 64;
+constexpr int kWBox = kLatV * 128;                   // 128 weight rows x 64 columns
+constexpr int kOBox = kTok * 128;                    // 32 tokens x 64 columns
+
+struct Shared {
+    unsigned long long w_full, done;
+    uint32_t tmem_base;
+    int abort_flag;
+    float lse[kTok];
+    int first[kTok], count[kTok];
+    float4 part[kGroups][128];
+};
+
+constexpr size_t kSmemBytes = 1024 + kBoxes * (size_t)(kWBox + 2 * kOBox) + sizeof(Shared);
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+template <bool BF16>
+__device__ __forceinline__ float4 load_state(const void* o_part, int state, int col4) {
+    if (BF16) {
+        const uint2 v = *((const uint2*)((const __nv_bfloat16*)o_part + (size_t)state * kLatC) + col4);
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xFFFF0000u));
+    }
+    return *((const float4*)((const float*)o_part + (size_t)state * kLatC) + col4);
+}
+
+__device__ __forceinline__ void fma4(float4& s, float w, const float4& v) {
+    s.x = fmaf(w, v.x, s.x);
+    s.y = fmaf(w, v.y, s.y);
+    s.z = fmaf(w, v.z, s.z);
+    s.w = fmaf(w, v.w, s.w);
+}
+
+// the token's four columns as bf16 high parts and residuals, in the swizzled operand boxes
+__device__ __forceinline__ void put(unsigned char* hi, unsigned char* lo, int tok, int col4, const float4& s) {
+    uint32_t h[2], l[2];
+    split_bf16(s.x, s.y, h[0], l[0]);
+    split_bf16(s.z, s.w, h[1], l[1]);
+    const int c = col4 * 4, at = (c >> 6) * kOBox + tok * 128 + ((((c & 63) >> 3) ^ (tok & 7)) << 4) + (c & 7) * 2;
+    *(uint2*)(hi + at) = make_uint2(h[0], h[1]);
+    *(uint2*)(lo + at) = make_uint2(l[0], l[1]);
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, const void* o_part, const float* lse_part,
+                      const int32_t* indptr) {
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* sW = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    unsigned char* sHi = sW + kBoxes * kWBox;
+    unsigned char* sLo = sHi + kBoxes * kOBox;
+    Shared& S = *(Shared*)(sLo + kBoxes * kOBox);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = blockIdx.x % a.heads, t0 = blockIdx.x / a.heads * kTok;
+    const int n = min(kTok, a.total_q - t0);
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&S.w_full), 1);
+        mbar_init(smem_u32(&S.done), 1);
+        S.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        mbar_expect_tx(smem_u32(&S.w_full), kBoxes * kWBox);
+        for (int j = 0; j < kBoxes; ++j)
+            tma_2d(smem_u32(sW + j * kWBox), &mw, 64 * j, head * kLatW + kLatNope, smem_u32(&S.w_full));
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem_base)), "r"(kTok)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // ---- log-sum-exp of each row over its states: a warp per row, a lane per state ----
+    for (int t = warp; t < n; t += kThreads / 32) {
+        const size_t x = (size_t)(t0 + t) * a.heads + head;
+        const int s0 = indptr[x], cnt = indptr[x + 1] - s0;
+        float m = -INFINITY, sum = 0.f;
+        for (int s = lane; s < cnt; s += 32) m = fmaxf(m, lse_part[s0 + s]);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        for (int s = lane; s < cnt; s += 32) sum += m == -INFINITY ? 0.f : expf(lse_part[s0 + s] - m);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) {
+            const float lse = m == -INFINITY ? -INFINITY : m + logf(sum);
+            S.lse[t] = lse;
+            S.first[t] = s0;
+            S.count[t] = cnt;
+            if (a.lse_out) a.lse_out[x] = lse;
+        }
+    }
+    __syncthreads();
+    // ---- merge: a group of 128 threads covers a row, four columns each ----
+    const int group = threadIdx.x >> 7, col4 = threadIdx.x & 127;
+    auto weight = [&](int t, int s) {
+        const float l = lse_part[S.first[t] + s];
+        return l == -INFINITY ? 0.f : expf(l - S.lse[t]);
+    };
+    if (n < kGroups) {
+        // few rows: the groups take every fourth split of a row and add up through shared memory
+        for (int t = 0; t < n; ++t) {
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int cnt = S.count[t];
+            for (int s = group; s < cnt; s += 8 * kGroups) {
+                float4 v[8];
+                float w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int x = s + k * kGroups;
+                    w[k] = 0.f;
+                    if (x < cnt) {
+                        v[k] = load_state<BF16>(o_part, S.first[t] + x, col4);
+                        w[k] = weight(t, x);
+                    } else {
+                        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) fma4(sum, w[k], v[k]);
+            }
+            S.part[group][col4] = sum;
+            __syncthreads();
+            if (group == 0) {
+                sum = S.part[0][col4];
+#pragma unroll
+                for (int g = 1; g < kGroups; ++g) fma4(sum, 1.f, S.part[g][col4]);
+                put(sHi, sLo, t, col4, sum);
+            }
+            __syncthreads();
+        }
+    } else {
+        // four rows of the group at a time, two splits of each in flight
+        for (int r0 = group; r0 < n; r0 += 4 * kGroups) {
+            float4 sum[4];
+            int most = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int t = r0 + j * kGroups;
+                if (t < n) most = max(most, S.count[t]);
+            }
+            for (int s = 0; s < most; s += 2) {
+                float4 v[4][2];
+                float w[4][2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = r0 + j * kGroups;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        w[j][k] = 0.f;
+                        v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (t < n && s + k < S.count[t]) {
+                            v[j][k] = load_state<BF16>(o_part, S.first[t] + s + k, col4);
+                            w[j][k] = weight(t, s + k);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) fma4(sum[j], w[j][k], v[j][k]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (r0 + j * kGroups < n) put(sHi, sLo, r0 + j * kGroups, col4, sum[j]);
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = S.tmem_base;
+    volatile int* abort_flag = &S.abort_flag;
+    // ---- D[v][token]: the high parts, then the residuals (rows past n are not written back) ----
+    if (threadIdx.x == 0) {
+        const bool ok = wait_bar(smem_u32(&S.w_full), 0, abort_flag, false);
+        if (ok) {
+            tc_fence_after();
+            constexpr uint32_t id = idesc_bf16(kLatV, kTok, 0);
+#pragma unroll 1
+            for (int part = 0; part < 2; ++part)
+#pragma unroll 1
+                for (int j = 0; j < kBoxes; ++j) {
+                    const uint64_t wd = desc_sw128(smem_u32(sW + j * kWBox), 16, 1024);
+                    const uint64_t od = desc_sw128(smem_u32((part ? sLo : sHi) + j * kOBox), 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_f16(tmem, wd + (uint64_t)((k * 32) >> 4), od + (uint64_t)((k * 32) >> 4), id, (part | j | k) ? 1u : 0u);
+                }
+        } else {
+            if (a.err) set_error(a.err, ERR_TIMEOUT | SITE_FULL_WAIT);
+            *abort_flag = 1;
+        }
+        mma_commit(smem_u32(&S.done));
+    }
+    if (warp < 4) {
+        if (warp_wait(smem_u32(&S.done), 0, abort_flag, lane)) {
+            tc_fence_after();
+            uint32_t d[32];
+            SKV_LD32(tmem + ((uint32_t)(warp * 32) << 16), d);
+            tc_wait_ld();
+            __nv_bfloat16* out = (__nv_bfloat16*)a.out + ((size_t)t0 * a.heads + head) * kLatV + threadIdx.x;
+            if (!*abort_flag) {
+#pragma unroll
+                for (int t = 0; t < kTok; ++t)
+                    if (t < n) out[(size_t)t * a.heads * kLatV] = __float2bfloat16_rn(__uint_as_float(d[t]));
+            }
+        } else if (lane == 0 && a.err) {
+            set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTok) : "memory");
+}
+
+}  // namespace
+
+cudaError_t launch_latent_project(const LatentArgs& a, const void* o_part, int part_bf16, const float* lse_part,
+                                  const int32_t* indptr, cudaStream_t s) {
+    if (a.total_q <= 0) return cudaSuccess;
+    auto enc = encode_fn();
+    if (!enc) return cudaErrorNotSupported;
+    CUtensorMap mw;
+    cuuint64_t dims[2] = {(cuuint64_t)kLatC, (cuuint64_t)a.heads * kLatW};
+    cuuint64_t strides[1] = {(cuuint64_t)kLatC * 2};
+    cuuint32_t box[2] = {64, (cuuint32_t)kLatV}, es[2] = {1, 1};
+    if (enc(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.w), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&]() {
+        attr_err = cudaFuncSetAttribute(latent_project_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (attr_err == cudaSuccess)
+            attr_err = cudaFuncSetAttribute(latent_project_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    const int ctas = a.heads * ((a.total_q + kTok - 1) / kTok);
+    ProfileScope ps(SPLITKV_KERNEL_LATENT_PROJECT, s);
+    if (part_bf16) latent_project_kernel<true><<<ctas, kThreads, kSmemBytes, s>>>(mw, a, o_part, lse_part, indptr);
+    else latent_project_kernel<false><<<ctas, kThreads, kSmemBytes, s>>>(mw, a, o_part, lse_part, indptr);
+    return cudaGetLastError();
+}
+
+}  // namespace skv

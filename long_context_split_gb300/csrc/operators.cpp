@@ -414,16 +414,24 @@ splitkv_status splitkv_latent_absorb_query(const splitkv_problem* prob, const sp
     return ok();
 }
 
-splitkv_status splitkv_latent_project(const splitkv_problem* prob, const splitkv_latent_layer* layer, const void* o_lat,
+splitkv_status splitkv_latent_project(const splitkv_problem* prob, const splitkv_latent_layer* layer, const void* o_part,
+                                      int32_t o_part_dtype, const float* lse_part, const int32_t* state_indptr,
                                       int32_t* dev_error_word, splitkv_stream stream) {
     splitkv_status s = check_latent_problem(prob);
     if (s) return s;
+    if (o_part_dtype != SPLITKV_F32 && o_part_dtype != SPLITKV_BF16)
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "o_part_dtype %d", o_part_dtype);
     if (prob->qo_indptr_host[prob->batch] == 0) return ok();
-    if ((uintptr_t)o_lat & 15) return fail_with(SPLITKV_ERR_INVALID_ARG, "o_lat must be 16-byte aligned");
+    if ((uintptr_t)o_part & 15) return fail_with(SPLITKV_ERR_INVALID_ARG, "o_part must be 16-byte aligned");
     if ((s = check_layer(prob, layer, false, true))) return s;
-    if ((s = check_ptr(o_lat, "o_lat", false))) return s;
+    if ((s = check_ptr(o_part, "o_part", false))) return s;
+    if ((s = check_ptr(lse_part, "lse_part", false))) return s;
+    if ((s = check_ptr(state_indptr, "state_indptr", false))) return s;
+    if ((s = check_ptr(layer->lse_out, "lse_out", true))) return s;
     if ((s = check_ptr(dev_error_word, "dev_error_word", true))) return s;
-    cudaError_t e = launch_latent_project(layer_args(prob, layer, dev_error_word), o_lat, (cudaStream_t)stream);
+    LatentArgs a = layer_args(prob, layer, dev_error_word);
+    a.lse_out = layer->lse_out;
+    cudaError_t e = launch_latent_project(a, o_part, o_part_dtype == SPLITKV_BF16, lse_part, state_indptr, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "value projection launch");
     return ok();
 }
