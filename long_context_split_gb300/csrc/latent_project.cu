@@ -3,14 +3,17 @@
 // output is projected by the head's W_uv.
 //
 // What it computes: o_lat = sum_s exp(lse_s - lse) o_s, lse = log sum_s exp(lse_s),
-// out = o_lat W_uv^T, a CTA per head and 32 tokens.
+// out = o_lat W_uv^T, a CTA per head and 64 tokens.
 //
 // What bounds it: bytes (128 KB of weights per head, 2 KB per state) and, for one
-// token, the chain weights -> states -> product.  So the weights' copy starts first;
-// the states are read with eight 16-byte loads in flight per thread, and when there are
-// fewer than four tokens the splits of a row are shared out over the CTA's four groups of
-// 128 threads.  The product is taken transposed, D[v][token] = W_uv[v][:] . o_lat[token][:]
-// (M = 128 value columns, N = 32 tokens, K = 512), so that few tokens waste little.
+// token, the chain index -> log-sum-exps -> states -> product.  So the weights' copy starts
+// first; all rows' weights are computed at once (16 lanes a row); the states are read with
+// eight 16-byte loads in flight per thread, and when there are fewer than eight tokens the
+// splits of a row are shared out over the CTA's eight groups of 128 threads.  64 tokens a CTA
+// keep a decode batch of 64 at one CTA per head (with 32: two waves of CTAs, 20 us instead
+// of XX); their operands fill 128 KB, so the weights pass through a ring of four 16 KB
+// boxes.  The product is taken transposed, D[v][token] = W_uv[v][:] . o_lat[token][:]
+// (M = 128 value columns, N = 64 tokens, K = 512), so that few tokens waste little.
 //
 // o_lat stays float32 until it meets the weights, as a bf16 high part and a bf16
 // residual (two products with the same weights, 16 significant bits): rounding it to
@@ -21,23 +24,26 @@
 namespace skv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kGroups = kThreads / 128;
-constexpr int kTok = 32;                             // tokens per CTA (N of the product)
+constexpr int kTok = 64;                             // tokens per CTA (N of the product)
+constexpr int kRing = 4;                             // weight boxes in shared memory
+constexpr int kTable = 32;                           // splits of a row whose weights are kept
 constexpr int kBoxes = kLatC / 64;
 constexpr int kWBox = kLatV * 128;                   // 128 weight rows x 64 columns
-constexpr int kOBox = kTok * 128;                    // 32 tokens x 64 columns
+constexpr int kOBox = kTok * 128;                    // 64 tokens x 64 columns
 
 struct Shared {
-    unsigned long long w_full, done;
+    unsigned long long w_full[kRing], w_empty[kRing], done;
     uint32_t tmem_base;
     int abort_flag;
     float lse[kTok];
     int first[kTok], count[kTok];
     float4 part[kGroups][128];
+    float weight[kTok][kTable];
 };
 
-constexpr size_t kSmemBytes = 1024 + kBoxes * (size_t)(kWBox + 2 * kOBox) + sizeof(Shared);
+constexpr size_t kSmemBytes = 1024 + kRing * (size_t)kWBox + kBoxes * (size_t)(2 * kOBox) + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 template <bool BF16>
@@ -73,39 +79,47 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
                       const int32_t* indptr) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sW = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char* sHi = sW + kBoxes * kWBox;
+    unsigned char* sHi = sW + kRing * kWBox;
     unsigned char* sLo = sHi + kBoxes * kOBox;
     Shared& S = *(Shared*)(sLo + kBoxes * kOBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.heads, t0 = blockIdx.x / a.heads * kTok;
     const int n = min(kTok, a.total_q - t0);
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&S.w_full), 1);
+        for (int j = 0; j < kRing; ++j) {
+            mbar_init(smem_u32(&S.w_full[j]), 1);
+            mbar_init(smem_u32(&S.w_empty[j]), 1);
+        }
         mbar_init(smem_u32(&S.done), 1);
         S.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        mbar_expect_tx(smem_u32(&S.w_full), kBoxes * kWBox);
-        for (int j = 0; j < kBoxes; ++j)
-            tma_2d(smem_u32(sW + j * kWBox), &mw, 64 * j, head * kLatW + kLatNope, smem_u32(&S.w_full));
+        for (int j = 0; j < kRing; ++j) {
+            mbar_expect_tx(smem_u32(&S.w_full[j]), kWBox);
+            tma_2d(smem_u32(sW + j * kWBox), &mw, 64 * j, head * kLatW + kLatNope, smem_u32(&S.w_full[j]));
+        }
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem_base)), "r"(kTok)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // ---- log-sum-exp of each row over its states: a warp per row, a lane per state ----
-    for (int t = warp; t < n; t += kThreads / 32) {
-        const size_t x = (size_t)(t0 + t) * a.heads + head;
-        const int s0 = indptr[x], cnt = indptr[x + 1] - s0;
+    // ---- each row's log-sum-exp over its states, and their weights: 16 lanes per row ----
+    {
+        const int t = threadIdx.x >> 4, sub = threadIdx.x & 15;
+        const bool on = t < n;
+        const size_t x = (size_t)(t0 + (on ? t : 0)) * a.heads + head;
+        const int s0 = indptr[x], cnt = on ? indptr[x + 1] - s0 : 0;
         float m = -INFINITY, sum = 0.f;
-        for (int s = lane; s < cnt; s += 32) m = fmaxf(m, lse_part[s0 + s]);
+        for (int s = sub; s < cnt; s += 16) m = fmaxf(m, lse_part[s0 + s]);
 #pragma unroll
-        for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        for (int s = lane; s < cnt; s += 32) sum += m == -INFINITY ? 0.f : expf(lse_part[s0 + s] - m);
+        for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        for (int s = sub; s < cnt; s += 16) sum += m == -INFINITY ? 0.f : expf(lse_part[s0 + s] - m);
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) {
-            const float lse = m == -INFINITY ? -INFINITY : m + logf(sum);
+        for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        const float lse = m == -INFINITY ? -INFINITY : m + logf(sum);
+        for (int s = sub; s < min(cnt, kTable); s += 16)
+            S.weight[t][s] = m == -INFINITY ? 0.f : expf(lse_part[s0 + s] - lse);
+        if (on && sub == 0) {
             S.lse[t] = lse;
             S.first[t] = s0;
             S.count[t] = cnt;
@@ -116,11 +130,12 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
     // ---- merge: a group of 128 threads covers a row, four columns each ----
     const int group = threadIdx.x >> 7, col4 = threadIdx.x & 127;
     auto weight = [&](int t, int s) {
+        if (s < kTable) return S.weight[t][s];
         const float l = lse_part[S.first[t] + s];
-        return l == -INFINITY ? 0.f : expf(l - S.lse[t]);
+        return S.lse[t] == -INFINITY ? 0.f : expf(l - S.lse[t]);
     };
     if (n < kGroups) {
-        // few rows: the groups take every fourth split of a row and add up through shared memory
+        // few rows: the groups take every eighth split of a row and add up through shared memory
         for (int t = 0; t < n; ++t) {
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
             const int cnt = S.count[t];
@@ -194,39 +209,51 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
     tc_fence_after();
     const uint32_t tmem = S.tmem_base;
     volatile int* abort_flag = &S.abort_flag;
-    // ---- D[v][token]: the high parts, then the residuals (rows past n are not written back) ----
+    // ---- D[v][token], box by box of 64 columns (rows past n are not written back) ----
+    if (threadIdx.x == 32) {
+        // the ring's second round of weights (also waited for by the products below)
+        for (int j = kRing; j < kBoxes; ++j) {
+            if (!wait_bar(smem_u32(&S.w_empty[j - kRing]), 0, abort_flag, true)) break;
+            mbar_expect_tx(smem_u32(&S.w_full[j - kRing]), kWBox);
+            tma_2d(smem_u32(sW + (j - kRing) * kWBox), &mw, 64 * j, head * kLatW + kLatNope, smem_u32(&S.w_full[j - kRing]));
+        }
+    }
     if (threadIdx.x == 0) {
-        const bool ok = wait_bar(smem_u32(&S.w_full), 0, abort_flag, false);
-        if (ok) {
+        constexpr uint32_t id = idesc_bf16(kLatV, kTok, 0);
+#pragma unroll 1
+        for (int j = 0; j < kBoxes; ++j) {
+            if (!wait_bar(smem_u32(&S.w_full[j % kRing]), j / kRing, abort_flag, false)) {
+                if (a.err) set_error(a.err, ERR_TIMEOUT | SITE_FULL_WAIT);
+                *abort_flag = 1;
+                break;
+            }
             tc_fence_after();
-            constexpr uint32_t id = idesc_bf16(kLatV, kTok, 0);
-#pragma unroll 1
-            for (int part = 0; part < 2; ++part)
-#pragma unroll 1
-                for (int j = 0; j < kBoxes; ++j) {
-                    const uint64_t wd = desc_sw128(smem_u32(sW + j * kWBox), 16, 1024);
-                    const uint64_t od = desc_sw128(smem_u32((part ? sLo : sHi) + j * kOBox), 16, 1024);
+            const uint64_t wd = desc_sw128(smem_u32(sW + (j % kRing) * kWBox), 16, 1024);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(tmem, wd + (uint64_t)((k * 32) >> 4), od + (uint64_t)((k * 32) >> 4), id, (part | j | k) ? 1u : 0u);
-                }
-        } else {
-            if (a.err) set_error(a.err, ERR_TIMEOUT | SITE_FULL_WAIT);
-            *abort_flag = 1;
+            for (int part = 0; part < 2; ++part) {
+                const uint64_t od = desc_sw128(smem_u32((part ? sLo : sHi) + j * kOBox), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_f16(tmem, wd + (uint64_t)((k * 32) >> 4), od + (uint64_t)((k * 32) >> 4), id, (part | j | k) ? 1u : 0u);
+            }
+            if (j + kRing < kBoxes) mma_commit(smem_u32(&S.w_empty[j % kRing]));
         }
         mma_commit(smem_u32(&S.done));
     }
-    if (warp < 4) {
+    __syncwarp();
+    if (warp < 8) {
+        // warps 0..3 the first 32 tokens, 4..7 the others; a thread per value column
+        const int c0 = (warp >> 2) * 32, quad = warp & 3;
         if (warp_wait(smem_u32(&S.done), 0, abort_flag, lane)) {
             tc_fence_after();
             uint32_t d[32];
-            SKV_LD32(tmem + ((uint32_t)(warp * 32) << 16), d);
+            SKV_LD32(tmem + ((uint32_t)(quad * 32) << 16) + c0, d);
             tc_wait_ld();
-            __nv_bfloat16* out = (__nv_bfloat16*)a.out + ((size_t)t0 * a.heads + head) * kLatV + threadIdx.x;
+            __nv_bfloat16* out = (__nv_bfloat16*)a.out + ((size_t)(t0 + c0) * a.heads + head) * kLatV + 32 * quad + lane;
             if (!*abort_flag) {
 #pragma unroll
-                for (int t = 0; t < kTok; ++t)
-                    if (t < n) out[(size_t)t * a.heads * kLatV] = __float2bfloat16_rn(__uint_as_float(d[t]));
+                for (int t = 0; t < 32; ++t)
+                    if (c0 + t < n) out[(size_t)t * a.heads * kLatV] = __float2bfloat16_rn(__uint_as_float(d[t]));
             }
         } else if (lane == 0 && a.err) {
             set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
