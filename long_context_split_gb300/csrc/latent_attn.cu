@@ -110,6 +110,67 @@ __device__ __forceinline__ Task read_task(const LatentArgs& a, int id) {
     return t;
 }
 
+// ---- the softmax of an unmasked unit, in the fewest instructions: a thread's serial work per unit
+// sets this kernel's pace (two softmax warps per scheduler), so maxima take three operands and
+// scaling and sums two values per instruction ----
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ float unit_max(const uint32_t (&s)[64]) {
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[4 + k]));
+#pragma unroll
+    for (int j = 8; j < 64; j += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = max3(m[k], __uint_as_float(s[j + k]), __uint_as_float(s[j + 4 + k]));
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
+// P = 2^(s c2 - base) as f16 pairs over the unit's S (key 2k in the low half of column k); the sum of P
+__device__ __forceinline__ float unit_p(const uint32_t (&s)[64], float c2, float base, uint32_t pcol) {
+    const uint64_t scale = pack2(c2, c2), shift = pack2(-base, -base);
+    uint64_t sum[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int j = 16 * h + 2 * e;
+            float x0, x1;
+            unpack2(fma2(pack2(__uint_as_float(s[j]), __uint_as_float(s[j + 1])), scale, shift), x0, x1);
+            x0 = ex2_ftz(x0);
+            x1 = ex2_ftz(x1);
+            sum[h] = e == 0 ? pack2(x0, x1) : add2(sum[h], pack2(x0, x1));
+            const __half2 p2 = __floats2half2_rn(x0, x1);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&p2);
+        }
+        SKV_ST8(pcol + 8 * h, pk);
+    }
+    float a, b;
+    unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+    return a + b;
+}
+
 struct Ring {
     uint32_t n = 0;
     // next task id (-1: no more); -2 when the wait gave up
@@ -371,7 +432,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 // warp-uniform: the tensor-memory instructions below are warp-collective
                 const bool unmasked = __all_sync(0xffffffffu, key0 + kKeys - 1 <= limit);
                 // the scale is positive, so the maximum is taken before it
-                const float mx = (unmasked ? row_max64<false>(sr, 64) : row_max64<true>(sr, limit - key0 + 1)) * c2;
+                const float mx = (unmasked ? unit_max(sr) : row_max64<true>(sr, limit - key0 + 1)) * c2;
                 float scale_o = 1.f;
                 bool need = false;
                 if (m == -INFINITY) {
@@ -405,10 +466,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 }
                 const float base = (m == -INFINITY) ? 0.f : m;
                 const uint32_t pcol = lane_addr + kColS + kKeys * b2;
-                l += unmasked ? write_p16<false>(sr, c2, base, key0, limit, pcol)
-                              : write_p16<true>(sr, c2, base, key0, limit, pcol);
+                l += unmasked ? unit_p(sr, c2, base, pcol) : write_p16<true>(sr, c2, base, key0, limit, pcol);
                 tc_wait_st();
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&B.p_full[x][b2]));
