@@ -7,18 +7,23 @@
 // the softmax of each token's visible keys, o = sum p v -- the final row, or a
 // split's partial state (normalised output, natural-log LSE) for the merge.
 //
-// What bounds it: the tensor pipe (2 * 320 operations per visible pair and
-// head) and, close behind, the exponentials: per 128-row tile and 64 keys 16 k-steps
-// of products take about 670 cycles, 8192 exponentials 512 cycles of the
-// special-function unit.  The keys and values of a (request, head) are read by all
-// of its query tiles, which run together, so they come from L2.
+// What bounds it: the tensor pipe (2 * 320 operations per visible pair and head).  S with
+// N = 64 keys reads both operands from shared memory at that memory's rate, 48 cycles a
+// k-step for 32 of arithmetic, so a unit of 64 keys takes 832 cycles per 128-row tile
+// instead of 640 (the products alone, softmax left out: 680 us where the whole takes 812,
+// 1 k + 2 k tokens after 14 k + 19 k at 32 heads).  The keys and values of a
+// (request, head) are read by all of its query tiles, which run together, so they come
+// from L2.
 //
-// How: two 128-token tiles per CTA share each 64-key unit (K 64 x 192, V 64 x 128,
-// 40 KB, a ring of three stages under 96 KB of queries).  A tile's MMA thread
-// issues S = Q K^T of unit u + 1 into one of two tensor-memory buffers before
-// O += P V of unit u; the tile's four softmax warps (a thread per token) take the
-// row maximum, keep a running maximum and sum (base 2; O is rescaled only when a
-// maximum grows by more than 2^8, so P stays below 2^8), and write P over S as f16.
+// How: two 128-token tiles per CTA share each 64-key unit (K 64 x 192, V 64 x 128) under
+// 96 KB of queries, in rings of three slots each: keys are released when both tiles' S is
+// done, values when their P V is (released together, unit u + 3 waits for the softmax of
+// unit u).  A tile's MMA thread issues S = Q K^T of unit u + 1 into one of two
+// tensor-memory buffers before O += P V of unit u; the tile's four softmax warps (a thread
+// per token) take the row maximum, keep a running maximum and sum (base 2; O is rescaled
+// only when a maximum grows by more than 2^8, so P stays below 2^8), and write P over S as
+// f16.  Two threads per token (eight warps a tile, maxima exchanged through shared
+// memory) measured slower, 944 us against 849 on two 3.6k-token prompts.
 // P and V are f16 because their product takes one type and f16's 11 significant
 // bits keep both roundings below the output's own; Q and K stay bf16, as given.
 // Sums, maxima and O are float32.  Products run in issue order, so S of unit u + 2
@@ -33,6 +38,11 @@
 
 #include "latent.h"
 #include "tc_common.cuh"
+
+#define SKV_LD8(taddr, r)                                                                                            \
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"                            \
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])    \
+                 : "r"(taddr))
 
 namespace skv {
 namespace {
@@ -55,24 +65,27 @@ constexpr int kQBox = kRows * 128;
 constexpr int kKvBox = kKeys * 128;
 constexpr int kQTile = kQBoxes * kQBox;
 constexpr int kQBytes = kTiles * kQTile;
-constexpr int kKBytes = kQBoxes * kKvBox;
-constexpr int kStage = kKBytes + kVBoxes * kKvBox;
-constexpr int NS = 3;
+constexpr int kKBytes = kQBoxes * kKvBox;            // a unit's keys: 24 KB
+constexpr int kVBytes = kVBoxes * kKvBox;            // a unit's values: 16 KB
+constexpr int NS = 3;                                // slots of the key ring, and of the value ring
 
 struct Bars {
     unsigned long long task_full[kTR], task_empty[kTR];
     int task_slot[kTR];
-    unsigned long long stage_full[NS];
-    unsigned long long stage_empty[kTiles][NS];   // per tile: its P V product of the stage's unit is done
+    unsigned long long k_full[NS], v_full[NS];
+    unsigned long long s_full[kTiles][NS];        // per tile and key slot: S of the slot's unit is done (for its
+                                                  // softmax, and the tile's release of the keys)
+    unsigned long long pv_done[kTiles][NS];       // per tile and value slot: P V of the slot's unit is done (the
+                                                  // tile's release of the values; O is up to date)
     unsigned long long q_full, q_empty;
-    unsigned long long s_full[kTiles][2], p_full[kTiles][2];
+    unsigned long long p_full[kTiles][2];
     unsigned long long o_full[kTiles], o_empty[kTiles];
     unsigned long long drain[kTiles];
     uint32_t tmem_base;
     int abort_flag;
 };
 
-constexpr size_t kSmemBytes = 1024 + kQBytes + (size_t)NS * kStage + sizeof(Bars);
+constexpr size_t kSmemBytes = 1024 + kQBytes + (size_t)NS * (kKBytes + kVBytes) + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 // what every role derives from a task
@@ -178,7 +191,7 @@ struct Ring {
         const int slot = (int)(n % kTR);
         const uint32_t par = (n / kTR) & 1;
         int ok = 1;
-        if (lane == 0) ok = wait_bar(smem_u32(&B.task_full[slot]), par, abort_flag, true) ? 1 : 0;
+        if (lane == 0) ok = spin_bar(smem_u32(&B.task_full[slot]), par, abort_flag, true) ? 1 : 0;
         if (whole_warp) ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) return -2;
         (void)mbar_try(smem_u32(&B.task_full[slot]), par);
@@ -190,14 +203,50 @@ struct Ring {
     }
 };
 
+// The producer's view of one ring: which tiles attend each slot's unit (only those release it),
+// and the phase parities of the tiles' releases and of the slot's loads.
+struct SlotUse {
+    uint32_t occ = 0, par = 0, next = 0;   // bit 8 x + s: tile x attends slot s; its release's parity; the next one's
+    uint32_t used = 0, loads = 0;          // bit s: the slot has been loaded; parity of its latest load
+
+    __device__ __forceinline__ bool wait_free(unsigned long long (&done)[kTiles][NS], int s, volatile int* abort_flag) {
+        for (int x = 0; x < kTiles; ++x) {
+            const uint32_t bit = 1u << (8 * x + s);
+            if ((occ & bit) && !spin_bar(smem_u32(&done[x][s]), (par & bit) ? 1u : 0u, abort_flag, true)) return false;
+        }
+        return true;
+    }
+    __device__ __forceinline__ void use(int s, bool tile0, bool tile1) {
+        for (int x = 0; x < kTiles; ++x) {
+            const uint32_t bit = 1u << (8 * x + s);
+            if (x ? tile1 : tile0) {
+                occ |= bit;
+                par = (par & ~bit) | (next & bit);
+                next ^= bit;
+            } else {
+                occ &= ~bit;
+            }
+        }
+        loads = (used >> s) & 1u ? loads ^ (1u << s) : loads;
+        used |= 1u << s;
+    }
+    __device__ __forceinline__ bool drain(unsigned long long (&full)[NS], volatile int* abort_flag) {
+        bool ok = true;
+        for (int s = 0; s < NS; ++s)
+            if ((used >> s) & 1u) ok = spin_bar(smem_u32(&full[s]), (loads >> s) & 1u, abort_flag, false) && ok;
+        return ok;
+    }
+};
+
 __global__ void __launch_bounds__(kThreads, 1)
 latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ CUtensorMap tmap_v, LatentArgs a) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char* sQ = smem;                              // tile x at x * kQTile
-    unsigned char* sStage = sQ + kQBytes;                  // stage: 2 key boxes, the rotary box, 2 value boxes
-    Bars& B = *(Bars*)(sStage + NS * kStage);
+    unsigned char* sK = sQ + kQBytes;                      // slot: 2 key boxes, the rotary box
+    unsigned char* sV = sK + NS * kKBytes;                 // slot: 2 value boxes
+    Bars& B = *(Bars*)(sV + NS * kVBytes);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -206,16 +255,17 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             mbar_init(smem_u32(&B.task_empty[s]), kTaskConsumers);
         }
         for (int s = 0; s < NS; ++s) {
-            mbar_init(smem_u32(&B.stage_full[s]), 1);
-            for (int x = 0; x < kTiles; ++x) mbar_init(smem_u32(&B.stage_empty[x][s]), 1);
+            mbar_init(smem_u32(&B.k_full[s]), 1);
+            mbar_init(smem_u32(&B.v_full[s]), 1);
+            for (int x = 0; x < kTiles; ++x) {
+                mbar_init(smem_u32(&B.s_full[x][s]), 1);
+                mbar_init(smem_u32(&B.pv_done[x][s]), 1);
+            }
         }
         mbar_init(smem_u32(&B.q_full), 1);
         mbar_init(smem_u32(&B.q_empty), kTiles);
         for (int x = 0; x < kTiles; ++x) {
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(smem_u32(&B.s_full[x][b]), 1);
-                mbar_init(smem_u32(&B.p_full[x][b]), 4);
-            }
+            for (int b = 0; b < 2; ++b) mbar_init(smem_u32(&B.p_full[x][b]), 4);
             mbar_init(smem_u32(&B.o_full[x]), 1);
             mbar_init(smem_u32(&B.o_empty[x]), 4);
             mbar_init(smem_u32(&B.drain[x]), 1);
@@ -245,13 +295,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
     if (warp == 0) {
         // ===================== producer and task claimer (lane 0) =====================
         if (lane == 0) {
-            uint32_t item = 0, qn = 0, claimed = 0;
-            uint32_t occ = 0, opar = 0, nph = 0;   // per (tile, stage), bit 8 x + s: the tile attends the stage's unit;
-                                                   // its release's parity; the next one's
+            uint32_t items = 0, qn = 0, claimed = 0;   // items: units of the tasks so far
+            SlotUse ku, vu;
             bool ok = a.inject != 1;               // (test hook: publish nothing)
             while (ok) {
                 const int slot = (int)(claimed % kTR);
-                if (!wait_bar(smem_u32(&B.task_empty[slot]), ((claimed / kTR) & 1) ^ 1, abort_flag, true)) {
+                if (!spin_bar(smem_u32(&B.task_empty[slot]), ((claimed / kTR) & 1) ^ 1, abort_flag, true)) {
                     give_up(SITE_EMPTY_WAIT);
                     break;
                 }
@@ -265,7 +314,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 if (t.n_units == 0) continue;
                 // both tiles' queries (rows past the request are other tokens, or the zero fill past
                 // the tensor; they are never written back)
-                if (!wait_bar(smem_u32(&B.q_empty), (qn & 1) ^ 1, abort_flag, true)) {
+                if (!spin_bar(smem_u32(&B.q_empty), (qn & 1) ^ 1, abort_flag, true)) {
                     give_up(SITE_EMPTY_WAIT);
                     break;
                 }
@@ -275,47 +324,42 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                         tma_2d(smem_u32(sQ + x * kQTile + j * kQBox), &tmap_q, t.head * kLatQ + 64 * j,
                                t.r.q_start + t.row0 + x * kRows, smem_u32(&B.q_full));
                 ++qn;
-                for (int u = 0; u < t.n_units; ++u, ++item) {
-                    const int s = (int)(item % NS);
-                    bool freed = true;
-                    for (int x = 0; x < kTiles && freed; ++x) {
-                        const uint32_t bit = 1u << (8 * x + s);
-                        if (occ & bit) freed = wait_bar(smem_u32(&B.stage_empty[x][s]), (opar & bit) ? 1u : 0u, abort_flag, true);
-                    }
-                    if (!freed) {
-                        give_up(SITE_EMPTY_WAIT);
-                        ok = false;
-                        break;
-                    }
-                    for (int x = 0; x < kTiles; ++x) {
-                        const uint32_t bit = 1u << (8 * x + s);
-                        if (u < t.nu[x]) {
-                            occ |= bit;
-                            opar = (opar & ~bit) | (nph & bit);
-                            nph ^= bit;
-                        } else {
-                            occ &= ~bit;
-                        }
-                    }
-                    const uint32_t full = smem_u32(&B.stage_full[s]);
-                    const uint32_t st = smem_u32(sStage + s * kStage);
+                // Keys two units ahead of values, the order in which the tiles release them: P V of unit
+                // u - 3 (the values' slot) is issued before S of unit u - 1 (the keys' slot of u + 2)
+                auto load_keys = [&](int u) -> bool {
+                    const int s = (int)((items + u) % NS);
+                    if (!ku.wait_free(B.s_full, s, abort_flag)) return false;
+                    ku.use(s, u < t.nu[0], u < t.nu[1]);
+                    const uint32_t full = smem_u32(&B.k_full[s]), to = smem_u32(sK + s * kKBytes);
                     const int y = t.r.row_base + t.kb + u * kKeys;   // row of the copies
-                    const int yh = t.head * padded + y;
-                    mbar_expect_tx(full, kStage);
-                    tma_2d(st, &tmap_k, 0, yh, full);
-                    tma_2d(st + kKvBox, &tmap_k, 64, yh, full);
-                    tma_2d(st + 2 * kKvBox, &tmap_r, kLatC, y, full);
-                    tma_2d(st + kKBytes, &tmap_v, 0, yh, full);
-                    tma_2d(st + kKBytes + kKvBox, &tmap_v, 64, yh, full);
+                    mbar_expect_tx(full, kKBytes);
+                    tma_2d(to, &tmap_k, 0, t.head * padded + y, full);
+                    tma_2d(to + kKvBox, &tmap_k, 64, t.head * padded + y, full);
+                    tma_2d(to + 2 * kKvBox, &tmap_r, kLatC, y, full);
+                    return true;
+                };
+                auto load_values = [&](int u) -> bool {
+                    const int s = (int)((items + u) % NS);
+                    if (!vu.wait_free(B.pv_done, s, abort_flag)) return false;
+                    vu.use(s, u < t.nu[0], u < t.nu[1]);
+                    const uint32_t full = smem_u32(&B.v_full[s]), to = smem_u32(sV + s * kVBytes);
+                    const int y = t.head * padded + t.r.row_base + t.kb + u * kKeys;
+                    mbar_expect_tx(full, kVBytes);
+                    tma_2d(to, &tmap_v, 0, y, full);
+                    tma_2d(to + kKvBox, &tmap_v, 64, y, full);
+                    return true;
+                };
+                ok = load_keys(0) && (t.n_units < 2 || load_keys(1));
+                for (int u = 0; ok && u < t.n_units; ++u) ok = load_values(u) && (u + 2 >= t.n_units || load_keys(u + 2));
+                if (!ok) {
+                    give_up(SITE_EMPTY_WAIT);
+                    break;
                 }
+                items += t.n_units;
             }
             // no copy may still be landing when the CTA leaves
-            for (uint32_t k = 0; k < (uint32_t)NS && k < item; ++k) {
-                const uint32_t last = item - 1 - k;
-                if (!wait_bar(smem_u32(&B.stage_full[last % NS]), (last / NS) & 1, abort_flag, false))
-                    set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
-            }
-            if (qn && !wait_bar(smem_u32(&B.q_full), (qn - 1) & 1, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+            if (!ku.drain(B.k_full, abort_flag) || !vu.drain(B.v_full, abort_flag)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+            if (qn && !spin_bar(smem_u32(&B.q_full), (qn - 1) & 1, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
         }
         __syncwarp();
     } else if (warp == 1 || warp == kIssuerWarp1) {
@@ -337,10 +381,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 if (id < 0) break;
                 const Task t = read_task(a, id);
                 if (t.n_units == 0) continue;
-                const uint32_t item0 = item;      // stage of unit u: (item0 + u) % NS
+                const uint32_t item0 = item;      // slot of unit u: (item0 + u) % NS
                 item += t.n_units;
                 const int nu = x ? t.nu[1] : t.nu[0];
-                if (!wait_bar(smem_u32(&B.q_full), qn & 1, abort_flag, true)) { give_up(SITE_FULL_WAIT); break; }
+                if (!spin_bar(smem_u32(&B.q_full), qn & 1, abort_flag, true)) { give_up(SITE_FULL_WAIT); break; }
                 ++qn;
                 if (nu == 0) {                    // nothing to attend: release the queries
                     mbar_arrive(smem_u32(&B.q_empty));
@@ -349,12 +393,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 tc_fence_after();
                 auto issue_s = [&](int u) -> bool {
                     const uint32_t gi = item0 + u;
-                    const int stage = (int)(gi % NS);
-                    if (!wait_bar(smem_u32(&B.stage_full[stage]), (gi / NS) & 1, abort_flag, true)) return false;
+                    const int slot = (int)(gi % NS);
+                    if (!spin_bar(smem_u32(&B.k_full[slot]), (gi / NS) & 1, abort_flag, true)) return false;
                     tc_fence_after();
-                    const uint32_t gs = pc + u;
-                    const uint32_t scol = bufcol + kKeys * (gs & 1);
-                    const uint64_t kd = desc_sw128(smem_u32(sStage + stage * kStage), 16, 1024);
+                    const uint32_t scol = bufcol + kKeys * ((pc + u) & 1);
+                    const uint64_t kd = desc_sw128(smem_u32(sK + slot * kKBytes), 16, 1024);
 #pragma unroll
                     for (int kk = 0; kk < kLatQ / 16; ++kk) {
                         const uint64_t ad = qd + (uint64_t)((((kk >> 2) * kQBox) + (kk & 3) * 32) >> 4);
@@ -362,21 +405,22 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                         if (kk == 0) mma_f16c<0>(scol, ad, bd, id_s);
                         else mma_f16c<1>(scol, ad, bd, id_s);
                     }
-                    mma_commit(smem_u32(&B.s_full[x][gs & 1]));
+                    mma_commit(smem_u32(&B.s_full[x][slot]));
                     return true;
                 };
                 auto issue_pv = [&](int u) -> bool {
-                    if (u == 0 && !wait_bar(smem_u32(&B.o_empty[x]), (tn & 1) ^ 1, abort_flag, true)) return false;
-                    const uint32_t gp = pc + u;
-                    if (!wait_bar(smem_u32(&B.p_full[x][gp & 1]), (gp >> 1) & 1, abort_flag, true)) return false;
+                    if (u == 0 && !spin_bar(smem_u32(&B.o_empty[x]), (tn & 1) ^ 1, abort_flag, true)) return false;
+                    const uint32_t gi = item0 + u, gp = pc + u;
+                    const int slot = (int)(gi % NS);
+                    if (!spin_bar(smem_u32(&B.v_full[slot]), (gi / NS) & 1, abort_flag, true)) return false;
+                    if (!spin_bar(smem_u32(&B.p_full[x][gp & 1]), (gp >> 1) & 1, abort_flag, true)) return false;
                     tc_fence_after();
                     const uint32_t pcol = bufcol + kKeys * (gp & 1);
-                    const int stage = (int)((item0 + u) % NS);
-                    const uint64_t vd = desc_sw128(smem_u32(sStage + stage * kStage + kKBytes), kKvBox, 1024);
+                    const uint64_t vd = desc_sw128(smem_u32(sV + slot * kVBytes), kKvBox, 1024);
                     mma_f16_ts(ocol, pcol, vd, id_o, u > 0 ? 1u : 0u);
 #pragma unroll
                     for (int kk = 1; kk < 4; ++kk) mma_f16_tsc<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o);
-                    mma_commit(smem_u32(&B.stage_empty[x][stage]));
+                    mma_commit(smem_u32(&B.pv_done[x][slot]));
                     return true;
                 };
                 ok = issue_s(0);
@@ -390,7 +434,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             }
             // every product issued here completes before tensor memory is released
             mma_commit(smem_u32(&B.drain[x]));
-            if (!wait_bar(smem_u32(&B.drain[x]), 0, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+            if (!spin_bar(smem_u32(&B.drain[x]), 0, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
         }
         __syncwarp();
     } else {
@@ -400,35 +444,41 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) << 5) << 16) + x * kTmemTile;
         const float c2 = a.scale_log2;
         uint32_t sn = 0, on = 0, item = 0;
-        uint32_t ph = 0;                     // per stage: phase parity of this tile's next release
+        uint32_t ph = 0;                     // per slot: parity of this tile's next S (and of its next release)
         bool ok = true;
         Ring ring;
         while (ok) {
             const int id = ring.next(B, abort_flag, lane, true);
             if (id == -2) { give_up(SITE_FULL_WAIT); break; }
             if (id < 0) break;
-            const Task t = read_task(a, id);
-            const int trows = x ? t.rows[1] : t.rows[0];
-            const int nu = x ? t.nu[1] : t.nu[0];
+            int nu, kb, i, limit, n_units;
+            bool valid;
+            {
+                const Task t = read_task(a, id);
+                const int trows = x ? t.rows[1] : t.rows[0];
+                nu = x ? t.nu[1] : t.nu[0];
+                kb = t.kb;
+                n_units = t.n_units;
+                valid = row < trows;
+                i = t.row0 + x * kRows + (valid ? row : 0);        // token of the request
+                // last key this token sees in the split
+                limit = valid ? min(t.kend - 1, t.r.seq_len - t.r.q_len + i) : -1;
+                if (trows == 0) nu = -1;
+            }
             const uint32_t item0 = item;
-            item += t.n_units;
-            if (trows == 0) continue;
-            const bool valid = row < trows;
-            const int i = t.row0 + x * kRows + (valid ? row : 0);  // token of the request
-            // last key this token sees in the split
-            const int limit = valid ? min(t.kend - 1, t.r.seq_len - t.r.q_len + i) : -1;
+            item += n_units;
+            if (nu < 0) continue;                                  // no token of the task in this tile
             float m = -INFINITY, l = 0.f;
             for (int u = 0; u < nu; ++u) {
-                const uint32_t gi = sn;
-                const int b2 = (int)(gi & 1);
-                if (!warp_wait(smem_u32(&B.s_full[x][b2]), (gi >> 1) & 1, abort_flag, lane)) { give_up(SITE_FULL_WAIT); ok = false; break; }
+                const int b2 = (int)(sn & 1), slot = (int)((item0 + u) % NS);
+                if (!spin_warp(smem_u32(&B.s_full[x][slot]), (ph >> slot) & 1u, abort_flag)) { give_up(SITE_FULL_WAIT); ok = false; break; }
                 tc_fence_after();
                 uint32_t sr[64];
                 SKV_LD32(lane_addr + kColS + kKeys * b2, sr);
                 SKV_LD32(lane_addr + kColS + kKeys * b2 + 32, (sr + 32));
                 tc_wait_ld();
                 ++sn;
-                const int key0 = t.kb + u * kKeys;
+                const int key0 = kb + u * kKeys;
                 // warp-uniform: the tensor-memory instructions below are warp-collective
                 const bool unmasked = __all_sync(0xffffffffu, key0 + kKeys - 1 <= limit);
                 // the scale is positive, so the maximum is taken before it
@@ -444,10 +494,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 }
                 if (__any_sync(0xffffffffu, need)) {
                     if (u >= 1) {
-                        // P V of unit u - 1 has updated O once this tile released that unit's stage; the
-                        // release barrier moves on only with this softmax's next P
+                        // P V of unit u - 1 has updated O once this tile released that unit's values; that
+                        // barrier moves on only with this softmax's next P
                         const int rs = (int)((item0 + u - 1) % NS);
-                        if (!warp_wait(smem_u32(&B.stage_empty[x][rs]), ((ph >> rs) & 1u) ^ 1u, abort_flag, lane)) {
+                        if (!spin_warp(smem_u32(&B.pv_done[x][rs]), ((ph >> rs) & 1u) ^ 1u, abort_flag)) {
                             give_up(SITE_EMPTY_WAIT);
                             ok = false;
                             break;
@@ -455,13 +505,15 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                         tc_fence_after();
                     }
                     l *= scale_o;
-                    for (int c = 0; c < kLatV; c += 32) {
-                        uint32_t o[32];
-                        SKV_LD32(lane_addr + c, o);
+                    // (eight columns at a time: the unit's 64 scores stay in registers meanwhile)
+#pragma unroll 1
+                    for (int c = 0; c < kLatV; c += 8) {
+                        uint32_t o[8];
+                        SKV_LD8(lane_addr + c, o);
                         tc_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale_o);
-                        SKV_ST32(lane_addr + c, o);
+                        for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale_o);
+                        SKV_ST8(lane_addr + c, o);
                     }
                 }
                 const float base = (m == -INFINITY) ? 0.f : m;
@@ -471,21 +523,23 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&B.p_full[x][b2]));
-                ph ^= 1u << ((item0 + u) % NS);
+                ph ^= 1u << slot;
             }
             if (!ok) break;
             if (nu > 0) {
-                if (!warp_wait(smem_u32(&B.o_full[x]), on & 1, abort_flag, lane)) { give_up(SITE_FULL_WAIT); ok = false; break; }
+                if (!spin_warp(smem_u32(&B.o_full[x]), on & 1, abort_flag)) { give_up(SITE_FULL_WAIT); ok = false; break; }
                 ++on;
                 tc_fence_after();
             }
             // a token that sees no key of the split has an empty state; a sum that is not positive
             // over visible keys (NaN, or every score -inf) goes through, as in the formula
-            const bool empty_row = limit < t.kb;
+            const bool empty_row = limit < kb;
             const float inv = empty_row ? 0.f : a.v_scale / l;
             const float lse = empty_row ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-            const size_t orow = (size_t)(t.r.q_start + i) * a.heads + t.head;
-            const size_t st = (size_t)t.r.state_base + ((size_t)i * a.heads + t.head) * t.r.n_splits + t.split;
+            const LatentTask d = a.tasks[id];                      // (read again: few registers across the loop)
+            const LatentReq r = a.reqs[d.b];
+            const size_t orow = (size_t)(r.q_start + i) * a.heads + d.head;
+            const size_t st = (size_t)r.state_base + ((size_t)i * a.heads + d.head) * r.n_splits + d.split;
             const bool direct = a.o_part == nullptr;
             for (int c = 0; c < kLatV; c += 32) {
                 uint32_t o[32];
