@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional, Sequence
 
@@ -102,19 +103,10 @@ class KernelTime(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_int32), ("pad", ctypes.c_int32), ("total_ms", ctypes.c_double)]
 
 
-class KVRows(ctypes.Structure):
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_token_stride", ctypes.c_int64),
-                ("k_head_stride", ctypes.c_int64), ("v_token_stride", ctypes.c_int64),
-                ("v_head_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
-
-
-class Verify(ctypes.Structure):
-    _fields_ = [("batch", ctypes.c_int32), ("total_q", ctypes.c_int32), ("vocab", ctypes.c_int32),
-                ("reserved", ctypes.c_int32), ("qo_indptr", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
-                ("target_probs", ctypes.c_void_p), ("draft_probs", ctypes.c_void_p),
-                ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64),
-                ("accept_u", ctypes.c_void_p), ("sample_u", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
-                ("seq_lens_out", ctypes.c_void_p), ("out_tokens", ctypes.c_void_p), ("accepted", ctypes.c_void_p)]
+# splitkv_kv_rows and splitkv_verify, packed as bytes for each call (a fifth of the host time of
+# filling a ctypes.Structure)
+_KV_ROWS = struct.Struct("@PPqqqqii")
+_VERIFY = struct.Struct("@iiiiPPPPqqPPPPPP")
 
 
 class LatentLayer(ctypes.Structure):
@@ -160,8 +152,8 @@ SIGNATURES = {
     "merge_states_typed": (ctypes.c_int, [_vp, _i32, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp]),
     "splitkv_decode": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp, _vp]),
     "splitkv_decode_static": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, _vp, _vp, _vp, _vp]),
-    "splitkv_kv_append": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(KVRows), _vp, _vp]),
-    "splitkv_kv_gather": (ctypes.c_int, [ctypes.POINTER(Problem), _vp, _vp, _i32, ctypes.POINTER(KVRows), _vp, _vp]),
+    "splitkv_kv_append": (ctypes.c_int, [_vp, _vp, _vp, _vp]),                  # structs packed per call
+    "splitkv_kv_gather": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _vp]),  # (splitkv_kv_rows, splitkv_verify)
     "splitkv_latent_plan": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(ctypes.c_void_p)]),
     "splitkv_latent_plan_destroy": (None, [_vp]),
     "splitkv_latent_workspace_bytes": (ctypes.c_size_t, [_vp]),
@@ -174,7 +166,7 @@ SIGNATURES = {
     "splitkv_latent_project": (ctypes.c_int, [ctypes.POINTER(Problem), ctypes.POINTER(LatentLayer), _vp, _i32, _vp, _vp,
                                               _vp, _vp]),
     "splitkv_latent_prefers_expanded": (_i32, [ctypes.POINTER(Problem)]),
-    "splitkv_verify_drafts": (ctypes.c_int, [ctypes.POINTER(Verify), _vp, _vp]),
+    "splitkv_verify_drafts": (ctypes.c_int, [_vp, _vp, _vp]),
     "splitkv_read_device_error": (ctypes.c_int, [_vp, _vp, _i32, _ip, _vp]),
     "splitkv_read_static_device_error": (ctypes.c_int, [_i32, _ip, _vp]),
     "splitkv_last_error_message": (ctypes.c_char_p, []),
@@ -290,6 +282,7 @@ class AttentionProblem:
             qo_indptr=qo_indptr.data_ptr(), seq_lens_host=self.seq_lens_host.ctypes.data,
             qo_indptr_host=self.qo_indptr_host.ctypes.data, kv_fp8=int(self.kv_fp8),
             k_scale=self.k_scale, v_scale=self.v_scale, reserved0=0)
+        self.address = ctypes.addressof(self._s)
 
     @property
     def total_q(self) -> int:
@@ -445,7 +438,7 @@ def _kv_part(name: str, t: torch.Tensor, shape: tuple, dtype):
     return st[0] if shape[0] > 1 else 0, st[1] if len(shape) == 3 and shape[1] > 1 else 0
 
 
-def _kv_rows(problem: AttentionProblem, rows: int, k: torch.Tensor, v: Optional[torch.Tensor]) -> KVRows:
+def _kv_rows(problem: AttentionProblem, rows: int, k: torch.Tensor, v: Optional[torch.Tensor]) -> bytes:
     """The ``splitkv_kv_rows`` of row tensors: GQA [rows, Hkv, D] each; MLA [rows, 512]
     and [rows, 64], or [rows, 576] alone.  Any strides but a contiguous last axis."""
     dt = k.dtype
@@ -459,9 +452,9 @@ def _kv_rows(problem: AttentionProblem, rows: int, k: torch.Tensor, v: Optional[
         shape, vshape = (rows, problem.head_dim_v), (rows, problem.head_dim_qk - problem.head_dim_v)
     kt, kh = _kv_part("k", k, shape, dt)
     if v is None:
-        return KVRows(k.data_ptr(), None, kt, kh, 0, 0, _DTYPES[dt], 0)
+        return _KV_ROWS.pack(k.data_ptr(), 0, kt, kh, 0, 0, _DTYPES[dt], 0)
     vt, vh = _kv_part("v", v, vshape, dt)
-    return KVRows(k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, _DTYPES[dt], 0)
+    return _KV_ROWS.pack(k.data_ptr(), v.data_ptr(), kt, kh, vt, vh, _DTYPES[dt], 0)
 
 
 def kv_append(problem: AttentionProblem, k_new: torch.Tensor, v_new: Optional[torch.Tensor] = None,
@@ -472,8 +465,9 @@ def kv_append(problem: AttentionProblem, k_new: torch.Tensor, v_new: Optional[to
     columns [total_q, 512] and v_new the rotary columns [total_q, 64], or k_new
     [total_q, 576] alone.  float32 or bfloat16, any token and head strides."""
     rows = _kv_rows(problem, problem.total_q, k_new, v_new)
-    _check(load().splitkv_kv_append(ctypes.byref(problem._s), ctypes.byref(rows), _ptr(dev_error_word),
-                                    _stream_handle(stream)))
+    st = (_lib or load()).splitkv_kv_append(problem.address, rows, _ptr(dev_error_word), _stream_handle(stream))
+    if st:
+        _check(st)
 
 
 def kv_gather(problem: AttentionProblem, kv_indptr: torch.Tensor, k_out: torch.Tensor,
@@ -482,12 +476,20 @@ def kv_gather(problem: AttentionProblem, kv_indptr: torch.Tensor, k_out: torch.T
     """splitkv_kv_gather: rows kv_indptr[b] .. kv_indptr[b+1]-1 of k_out / v_out become the
     (dequantised) cached tokens kv_begin[b] (0 without it) and following of request b.
     Shapes as kv_append's, over the rows of k_out; kv_indptr, kv_begin device int32."""
-    for name, t, n in (("kv_indptr", kv_indptr, problem.batch + 1), ("kv_begin", kv_begin, problem.batch)):
-        if t is not None and (t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n):
-            raise TypeError(f"{name} must be a contiguous int32 tensor of {n} entries")
-    rows = _kv_rows(problem, int(k_out.shape[0]), k_out, v_out)
-    _check(load().splitkv_kv_gather(ctypes.byref(problem._s), _ptr(kv_indptr), _ptr(kv_begin), int(k_out.shape[0]),
-                                    ctypes.byref(rows), _ptr(dev_error_word), _stream_handle(stream)))
+    _check_array("kv_indptr", kv_indptr, problem.batch + 1, torch.int32)
+    if kv_begin is not None:
+        _check_array("kv_begin", kv_begin, problem.batch, torch.int32)
+    n = k_out.shape[0]
+    rows = _kv_rows(problem, n, k_out, v_out)
+    st = (_lib or load()).splitkv_kv_gather(problem.address, kv_indptr.data_ptr(), _ptr(kv_begin), n, rows,
+                                            _ptr(dev_error_word), _stream_handle(stream))
+    if st:
+        _check(st)
+
+
+def _check_array(name: str, t: torch.Tensor, n: int, dtype):
+    if t.dtype is not dtype or not t.is_contiguous() or t.numel() != n:
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor of {n} entries")
 
 
 class LatentPlan:
@@ -581,30 +583,47 @@ def verify_drafts(tokens: torch.Tensor, qo_indptr: torch.Tensor, target_probs: t
     proposed with certainty), accept_u [total_q], sample_u [batch].  With seq_lens the
     lengths without the refused drafts' slots go to seq_lens_out.  Returns (out_tokens,
     accepted)."""
-    total, vocab = int(tokens.shape[0]), int(target_probs.shape[-1])
-    batch = int(qo_indptr.shape[0]) - 1
-    out_tokens = torch.empty_like(tokens) if out_tokens is None else out_tokens
-    accepted = torch.empty(batch, dtype=torch.int32, device=tokens.device) if accepted is None else accepted
-    for name, t, n, dt in (("tokens", tokens, total, torch.int32), ("qo_indptr", qo_indptr, batch + 1, torch.int32),
-                           ("accept_u", accept_u, total, torch.float32), ("sample_u", sample_u, batch, torch.float32),
-                           ("out_tokens", out_tokens, total, torch.int32), ("accepted", accepted, batch, torch.int32),
-                           ("seq_lens", seq_lens, batch, torch.int32), ("seq_lens_out", seq_lens_out, batch, torch.int32)):
-        if t is not None and (t.dtype != dt or not t.is_contiguous() or t.numel() != n):
-            raise TypeError(f"{name} must be a contiguous {dt} tensor of {n} entries")
-    stride = [vocab, vocab]
-    for i, t in enumerate((target_probs, draft_probs)):
-        if t is None:
-            continue
-        if t.dtype != torch.float32 or tuple(t.shape) != (total, vocab) or (t.stride(1) != 1 and vocab > 1 and total > 0):
-            raise TypeError(f"probabilities must be float32 [{total}, {vocab}] with contiguous rows")
-        if total > 1:
-            stride[i] = t.stride(0)
-    v = Verify(batch, total, vocab, 0, qo_indptr.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(),
-               None if draft_probs is None else draft_probs.data_ptr(), stride[0], stride[1], accept_u.data_ptr(),
-               sample_u.data_ptr(), None if seq_lens is None else seq_lens.data_ptr(),
-               None if seq_lens_out is None else seq_lens_out.data_ptr(), out_tokens.data_ptr(), accepted.data_ptr())
-    _check(load().splitkv_verify_drafts(ctypes.byref(v), _ptr(dev_error_word), _stream_handle(stream)))
+    total, vocab, batch = tokens.shape[0], target_probs.shape[-1], qo_indptr.shape[0] - 1
+    i32, f32 = torch.int32, torch.float32
+    if out_tokens is None:
+        out_tokens = torch.empty_like(tokens)
+    if accepted is None:
+        accepted = torch.empty(batch, dtype=i32, device=tokens.device)
+    _check_array("tokens", tokens, total, i32)
+    _check_array("qo_indptr", qo_indptr, batch + 1, i32)
+    _check_array("accept_u", accept_u, total, f32)
+    _check_array("sample_u", sample_u, batch, f32)
+    _check_array("out_tokens", out_tokens, total, i32)
+    _check_array("accepted", accepted, batch, i32)
+    lens = lens_out = draft = 0
+    if seq_lens is not None:
+        _check_array("seq_lens", seq_lens, batch, i32)
+        lens = seq_lens.data_ptr()
+    if seq_lens_out is not None:
+        _check_array("seq_lens_out", seq_lens_out, batch, i32)
+        lens_out = seq_lens_out.data_ptr()
+    target_stride = _check_probs(target_probs, total, vocab)
+    draft_stride = vocab
+    if draft_probs is not None:
+        draft_stride = _check_probs(draft_probs, total, vocab)
+        draft = draft_probs.data_ptr()
+    v = _VERIFY.pack(batch, total, vocab, 0, qo_indptr.data_ptr(), tokens.data_ptr(), target_probs.data_ptr(), draft,
+                     target_stride, draft_stride, accept_u.data_ptr(), sample_u.data_ptr(), lens, lens_out,
+                     out_tokens.data_ptr(), accepted.data_ptr())
+    st = (_lib or load()).splitkv_verify_drafts(v, _ptr(dev_error_word), _stream_handle(stream))
+    if st:
+        _check(st)
     return out_tokens, accepted
+
+
+def _check_probs(t: torch.Tensor, total: int, vocab: int) -> int:
+    """The row stride of probabilities t, checked."""
+    if t.dtype is not torch.float32 or t.shape != (total, vocab):
+        raise TypeError(f"probabilities must be float32 [{total}, {vocab}]")
+    st = t.stride()
+    if st[1] != 1 and vocab > 1 and total > 0:
+        raise TypeError("probabilities must have contiguous rows")
+    return st[0] if total > 1 else vocab
 
 
 def read_device_error(dev_error_word: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,

@@ -110,6 +110,10 @@ class LatentAttention:
         else:
             self.q_abs = torch.empty(total, heads, 576, dtype=torch.bfloat16, device=dev)
             self.problem = make(self.q_abs)
+            if params is None:
+                # the kernel attends 128 keys (two pages) at a time: splits of less waste its products
+                units = -(-int(self.problem.seq_lens_host.max()) // 128)
+                params = _lib.plan_params(max_splits=max(1, min(64, units)))
             base = SplitKVAttention(self.problem, params, stream)
             self.plan, self.workspace, self.error_word = base.plan, base.workspace, base.error_word
             self.state_indptr = base.state_indptr

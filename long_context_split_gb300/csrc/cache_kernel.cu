@@ -290,10 +290,8 @@ bool vectors_fit(const CacheRowsArgs& a, int vec, int rows_size, int cache_size)
 
 template <typename Rows, typename Cache, int VEC, bool APPEND>
 cudaError_t launch_vec(const CacheRowsArgs& a, cudaStream_t s) {
-    int dev = 0, sms = 0;
-    cudaError_t e;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
     const int cols = a.heads * (a.part[0].width / VEC) + a.heads * (a.part[1].width / VEC);
     const int bx = std::min(kThreads, (cols + 31) / 32 * 32);
     const int by = std::max(1, kThreads / bx);

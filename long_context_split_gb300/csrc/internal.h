@@ -167,6 +167,9 @@ void set_last_error_message(const char* msg);
 // Sets the calling thread's message (printf style) and returns s.
 splitkv_status fail_with(splitkv_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 
+// SMs of the current device (0: none visible).
+int sm_count();
+
 // Host-side checks of a problem's shape and lengths (no pointers).
 splitkv_status check_problem_lengths(const splitkv_problem* prob);
 

@@ -632,9 +632,8 @@ cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s) {
         attr_err = cudaFuncSetAttribute(latent_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     });
     if (attr_err != cudaSuccess) return attr_err;
-    int dev = 0, sms = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
     {
         ProfileScope ps(SPLITKV_KERNEL_LATENT_ATTENTION, s);
         latent_attention_kernel<<<std::min(sms, a.num_tasks), kThreads, kSmemBytes, s>>>(mq, mk, mr, mv, a);

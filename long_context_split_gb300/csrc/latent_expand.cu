@@ -347,9 +347,8 @@ cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s) {
         attr_err = cudaFuncSetAttribute(latent_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     });
     if (attr_err != cudaSuccess) return attr_err;
-    int dev = 0, sms = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
     const int tiles = (a.num_blocks + kCluster - 1) / kCluster * a.heads;
     {
         ProfileScope ps(SPLITKV_KERNEL_LATENT_EXPAND, s);

@@ -3,6 +3,7 @@
 // of drafted tokens.  Argument checks and the expanded form's plan; the
 // arithmetic runs in the CUDA kernels.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -117,12 +118,8 @@ splitkv_status check_rows_ptrs(const splitkv_problem* p, const CacheRowsArgs& a,
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int device_sms() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess &&
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess && n > 0)
-        return n;
-    cudaGetLastError();
-    return 152;   // GB300, where no device is visible
+    const int n = sm_count();
+    return n > 0 ? n : 152;   // GB300, where no device is visible
 }
 
 splitkv_status check_latent_problem(const splitkv_problem* p) {
@@ -167,6 +164,24 @@ LatentArgs layer_args(const splitkv_problem* p, const splitkv_latent_layer* l, i
 int cache_kind(const splitkv_problem* p) { return p->kv_fp8 ? 2 : p->dtype == SPLITKV_BF16 ? 1 : 0; }
 
 }  // namespace
+
+namespace skv {
+int sm_count() {
+    static std::atomic<int> known[64];   // per device, a constant of the hardware
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+}  // namespace skv
 
 struct splitkv_latent_plan_s {
     int32_t batch = 0, heads = 0, page = 0, max_pages = 0, kv_fp8 = 0, total_q = 0;

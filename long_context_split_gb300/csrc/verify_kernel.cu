@@ -356,10 +356,8 @@ cudaError_t launch(const VerifyArgs& a, int cluster, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s) {
-    int dev = 0, sms = 0;
-    cudaError_t e;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
     // CTAs per request: while each still has 4096 tokens and the SMs are not full (two CTAs each)
     int cluster = 1;
     while (cluster < kMaxCluster && a.vocab > 4096 * cluster && (long long)a.batch * cluster <= sms) cluster *= 2;
