@@ -7,12 +7,13 @@
 //
 // What bounds it: bytes (128 KB of weights per head, 2 KB per state) and, for one
 // token, the chain index -> log-sum-exps -> states -> product.  So the weights' copy starts
-// first; all rows' weights are computed at once (16 lanes a row); the states are read with
-// eight 16-byte loads in flight per thread, and when there are fewer than eight tokens the
-// splits of a row are shared out over the CTA's eight groups of 128 threads.  64 tokens a CTA
-// keep a decode batch of 64 at one CTA per head (with 32: two waves of CTAs, 20 us instead
-// of XX); their operands fill 128 KB, so the weights pass through a ring of four 16 KB
-// boxes.  The product is taken transposed, D[v][token] = W_uv[v][:] . o_lat[token][:]
+// first (all 128 KB are resident); all rows' weights are computed at once (16 lanes a row); the
+// states are read with several 16-byte loads in flight per thread, and up to 16 tokens share
+// their splits out over the CTA's sixteen groups of 64 threads.  64 tokens a CTA keep a decode batch of 64 at one CTA per head.  The latent columns
+// are merged and multiplied in two halves, so that the operands of one half (64 KB) fit
+// beside the weights and the first half's product runs under the second half's merge (with
+// the weights in a ring of four boxes instead, the products waited 3 us for the second four).
+// The product is taken transposed, D[v][token] = W_uv[v][:] . o_lat[token][:]
 // (M = 128 value columns, N = 64 tokens, K = 512), so that few tokens waste little.
 //
 // o_lat stays float32 until it meets the weights, as a bf16 high part and a bf16
@@ -25,25 +26,24 @@ namespace skv {
 namespace {
 
 constexpr int kThreads = 1024;
-constexpr int kGroups = kThreads / 128;
+constexpr int kGroups = kThreads / 64;               // a group covers half of a row's 512 columns, four a thread
 constexpr int kTok = 64;                             // tokens per CTA (N of the product)
-constexpr int kRing = 4;                             // weight boxes in shared memory
-constexpr int kTable = 32;                           // splits of a row whose weights are kept
+constexpr int kTable = 64;                           // splits of a row whose weights are kept
 constexpr int kBoxes = kLatC / 64;
 constexpr int kWBox = kLatV * 128;                   // 128 weight rows x 64 columns
 constexpr int kOBox = kTok * 128;                    // 64 tokens x 64 columns
 
 struct Shared {
-    unsigned long long w_full[kRing], w_empty[kRing], done;
+    unsigned long long w_full[2], done[2];           // per half of the latent columns
     uint32_t tmem_base;
     int abort_flag;
     float lse[kTok];
     int first[kTok], count[kTok];
-    float4 part[kGroups][128];
+    float4 part[kGroups][64];
     float weight[kTok][kTable];
 };
 
-constexpr size_t kSmemBytes = 1024 + kRing * (size_t)kWBox + kBoxes * (size_t)(2 * kOBox) + sizeof(Shared);
+constexpr size_t kSmemBytes = 1024 + kBoxes * (size_t)kWBox + kBoxes / 2 * (size_t)(2 * kOBox) + sizeof(Shared);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 template <bool BF16>
@@ -63,7 +63,7 @@ __device__ __forceinline__ void fma4(float4& s, float w, const float4& v) {
     s.w = fmaf(w, v.w, s.w);
 }
 
-// the token's four columns as bf16 high parts and residuals, in the swizzled operand boxes
+// the token's four columns (of the half) as bf16 high parts and residuals, in the swizzled operand boxes
 __device__ __forceinline__ void put(unsigned char* hi, unsigned char* lo, int tok, int col4, const float4& s) {
     uint32_t h[2], l[2];
     split_bf16(s.x, s.y, h[0], l[0]);
@@ -79,23 +79,23 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
                       const int32_t* indptr) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sW = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char* sHi = sW + kRing * kWBox;
-    unsigned char* sLo = sHi + kBoxes * kOBox;
-    Shared& S = *(Shared*)(sLo + kBoxes * kOBox);
+    unsigned char* sHi = sW + kBoxes * kWBox;              // four boxes: a half of the columns
+    unsigned char* sLo = sHi + kBoxes / 2 * kOBox;
+    Shared& S = *(Shared*)(sLo + kBoxes / 2 * kOBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int head = blockIdx.x % a.heads, t0 = blockIdx.x / a.heads * kTok;
     const int n = min(kTok, a.total_q - t0);
     if (threadIdx.x == 0) {
-        for (int j = 0; j < kRing; ++j) {
-            mbar_init(smem_u32(&S.w_full[j]), 1);
-            mbar_init(smem_u32(&S.w_empty[j]), 1);
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(smem_u32(&S.w_full[h]), 1);
+            mbar_init(smem_u32(&S.done[h]), 1);
         }
-        mbar_init(smem_u32(&S.done), 1);
         S.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        for (int j = 0; j < kRing; ++j) {
-            mbar_expect_tx(smem_u32(&S.w_full[j]), kWBox);
-            tma_2d(smem_u32(sW + j * kWBox), &mw, 64 * j, head * kLatW + kLatNope, smem_u32(&S.w_full[j]));
+        for (int j = 0; j < kBoxes; ++j) {
+            const uint32_t full = smem_u32(&S.w_full[j / (kBoxes / 2)]);
+            if (j % (kBoxes / 2) == 0) mbar_expect_tx(full, kBoxes / 2 * kWBox);
+            tma_2d(smem_u32(sW + j * kWBox), &mw, 64 * j, head * kLatW + kLatNope, full);
         }
     }
     if (warp == 1) {
@@ -109,16 +109,26 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
         const bool on = t < n;
         const size_t x = (size_t)(t0 + (on ? t : 0)) * a.heads + head;
         const int s0 = indptr[x], cnt = on ? indptr[x + 1] - s0 : 0;
-        float m = -INFINITY, sum = 0.f;
-        for (int s = sub; s < cnt; s += 16) m = fmaxf(m, lse_part[s0 + s]);
+        // (the first four of a lane's states stay in registers: all of them up to 64 splits)
+        float own[4], m = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            own[k] = sub + 16 * k < cnt ? lse_part[s0 + sub + 16 * k] : -INFINITY;
+            m = fmaxf(m, own[k]);
+        }
+        for (int s = sub + 64; s < cnt; s += 16) m = fmaxf(m, lse_part[s0 + s]);
 #pragma unroll
         for (int d = 8; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        for (int s = sub; s < cnt; s += 16) sum += m == -INFINITY ? 0.f : expf(lse_part[s0 + s] - m);
+        const float base = m == -INFINITY ? 0.f : m;         // (then every weight is exp(-inf) = 0)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum += sub + 16 * k < cnt ? expf(own[k] - base) : 0.f;
+        for (int s = sub + 64; s < cnt; s += 16) sum += expf(lse_part[s0 + s] - base);
 #pragma unroll
         for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         const float lse = m == -INFINITY ? -INFINITY : m + logf(sum);
-        for (int s = sub; s < min(cnt, kTable); s += 16)
-            S.weight[t][s] = m == -INFINITY ? 0.f : expf(lse_part[s0 + s] - lse);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (sub + 16 * k < cnt) S.weight[t][sub + 16 * k] = m == -INFINITY ? 0.f : expf(own[k] - lse);
         if (on && sub == 0) {
             S.lse[t] = lse;
             S.first[t] = s0;
@@ -127,124 +137,123 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
         }
     }
     __syncthreads();
-    // ---- merge: a group of 128 threads covers a row, four columns each ----
-    const int group = threadIdx.x >> 7, col4 = threadIdx.x & 127;
+    const uint32_t tmem = S.tmem_base;
+    volatile int* abort_flag = &S.abort_flag;
     auto weight = [&](int t, int s) {
         if (s < kTable) return S.weight[t][s];
         const float l = lse_part[S.first[t] + s];
         return S.lse[t] == -INFINITY ? 0.f : expf(l - S.lse[t]);
     };
-    if (n < kGroups) {
-        // few rows: the groups take every eighth split of a row and add up through shared memory
-        for (int t = 0; t < n; ++t) {
+    const int group = threadIdx.x >> 6;
+    for (int half = 0; half < 2; ++half) {
+        // ---- merge of the half's columns ----
+        const int col4 = 64 * half + (threadIdx.x & 63), to4 = threadIdx.x & 63;
+        // the operand boxes are free once the first half's product has read them
+        auto boxes_free = [&]() {
+            if (half == 1 && !spin_warp(smem_u32(&S.done[0]), 0, abort_flag)) *abort_flag = 1;
+        };
+        if (n <= kGroups) {
+            // few rows: each row's splits are shared out over kGroups / (n rounded up to a power of two)
+            // groups, which add up through shared memory
+            const int np = n <= 1 ? 1 : 1 << (32 - __clz(n - 1));
+            const int per = kGroups / np, t = group / per, part = group % per;
             float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int cnt = S.count[t];
-            for (int s = group; s < cnt; s += 8 * kGroups) {
-                float4 v[8];
-                float w[8];
+            const int cnt = t < n ? S.count[t] : 0;
+            for (int s = part; s < cnt; s += 4 * per) {
+                float4 v[4];
+                float w[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int x = s + k * kGroups;
+                for (int k = 0; k < 4; ++k) {
+                    const int x = s + k * per;
                     w[k] = 0.f;
+                    v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (x < cnt) {
                         v[k] = load_state<BF16>(o_part, S.first[t] + x, col4);
                         w[k] = weight(t, x);
-                    } else {
-                        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) fma4(sum, w[k], v[k]);
+                for (int k = 0; k < 4; ++k) fma4(sum, w[k], v[k]);
             }
-            S.part[group][col4] = sum;
+            S.part[group][to4] = sum;
             __syncthreads();
-            if (group == 0) {
-                sum = S.part[0][col4];
-#pragma unroll
-                for (int g = 1; g < kGroups; ++g) fma4(sum, 1.f, S.part[g][col4]);
-                put(sHi, sLo, t, col4, sum);
+            if (part == 0 && t < n) {
+                for (int g = 1; g < per; ++g) fma4(sum, 1.f, S.part[group + g][to4]);
+                boxes_free();
+                put(sHi, sLo, t, to4, sum);
             }
-            __syncthreads();
-        }
-    } else {
-        // four rows of the group at a time, two splits of each in flight
-        for (int r0 = group; r0 < n; r0 += 4 * kGroups) {
-            float4 sum[4];
-            int most = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int t = r0 + j * kGroups;
-                if (t < n) most = max(most, S.count[t]);
-            }
-            for (int s = 0; s < most; s += 2) {
-                float4 v[4][2];
-                float w[4][2];
+        } else {
+            // four rows of the group at a time, two splits of each in flight
+            for (int r0 = group; r0 < n; r0 += 4 * kGroups) {
+                float4 sum[4];
+                int most = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
+                    sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
                     const int t = r0 + j * kGroups;
+                    if (t < n) most = max(most, S.count[t]);
+                }
+                for (int s = 0; s < most; s += 2) {
+                    float4 v[4][2];
+                    float w[4][2];
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        w[j][k] = 0.f;
-                        v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (t < n && s + k < S.count[t]) {
-                            v[j][k] = load_state<BF16>(o_part, S.first[t] + s + k, col4);
-                            w[j][k] = weight(t, s + k);
+                    for (int j = 0; j < 4; ++j) {
+                        const int t = r0 + j * kGroups;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            w[j][k] = 0.f;
+                            v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (t < n && s + k < S.count[t]) {
+                                v[j][k] = load_state<BF16>(o_part, S.first[t] + s + k, col4);
+                                w[j][k] = weight(t, s + k);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) fma4(sum[j], w[j][k], v[j][k]);
                 }
+                if (r0 == group) boxes_free();
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) fma4(sum[j], w[j][k], v[j][k]);
+                    if (r0 + j * kGroups < n) put(sHi, sLo, r0 + j * kGroups, to4, sum[j]);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (r0 + j * kGroups < n) put(sHi, sLo, r0 + j * kGroups, col4, sum[j]);
         }
-    }
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = S.tmem_base;
-    volatile int* abort_flag = &S.abort_flag;
-    // ---- D[v][token], box by box of 64 columns (rows past n are not written back) ----
-    if (threadIdx.x == 32) {
-        // the ring's second round of weights (also waited for by the products below)
-        for (int j = kRing; j < kBoxes; ++j) {
-            if (!wait_bar(smem_u32(&S.w_empty[j - kRing]), 0, abort_flag, true)) break;
-            mbar_expect_tx(smem_u32(&S.w_full[j - kRing]), kWBox);
-            tma_2d(smem_u32(sW + (j - kRing) * kWBox), &mw, 64 * j, head * kLatW + kLatNope, smem_u32(&S.w_full[j - kRing]));
-        }
-    }
-    if (threadIdx.x == 0) {
-        constexpr uint32_t id = idesc_bf16(kLatV, kTok, 0);
-#pragma unroll 1
-        for (int j = 0; j < kBoxes; ++j) {
-            if (!wait_bar(smem_u32(&S.w_full[j % kRing]), j / kRing, abort_flag, false)) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        // ---- D[v][token] of the half, box by box of 64 columns (rows past n are not written back) ----
+        if (threadIdx.x == 0) {
+            constexpr uint32_t id = idesc_bf16(kLatV, kTok, 0);
+            if (!spin_bar(smem_u32(&S.w_full[half]), 0, abort_flag, false)) {
                 if (a.err) set_error(a.err, ERR_TIMEOUT | SITE_FULL_WAIT);
                 *abort_flag = 1;
-                break;
-            }
-            tc_fence_after();
-            const uint64_t wd = desc_sw128(smem_u32(sW + (j % kRing) * kWBox), 16, 1024);
+            } else {
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < kBoxes / 2; ++j) {
+                    const uint64_t wd = desc_sw128(smem_u32(sW + (half * (kBoxes / 2) + j) * kWBox), 16, 1024);
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                const uint64_t od = desc_sw128(smem_u32((part ? sLo : sHi) + j * kOBox), 16, 1024);
+                    for (int part = 0; part < 2; ++part) {
+                        const uint64_t od = desc_sw128(smem_u32((part ? sLo : sHi) + j * kOBox), 16, 1024);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_f16(tmem, wd + (uint64_t)((k * 32) >> 4), od + (uint64_t)((k * 32) >> 4), id, (part | j | k) ? 1u : 0u);
+                        for (int k = 0; k < 4; ++k)
+                            mma_f16(tmem, wd + (uint64_t)((k * 32) >> 4), od + (uint64_t)((k * 32) >> 4), id,
+                                    (half | part | j | k) ? 1u : 0u);
+                    }
+                }
             }
-            if (j + kRing < kBoxes) mma_commit(smem_u32(&S.w_empty[j % kRing]));
+            mma_commit(smem_u32(&S.done[half]));
         }
-        mma_commit(smem_u32(&S.done));
+        __syncwarp();
     }
     __syncwarp();
     if (warp < 8) {
         // warps 0..3 the first 32 tokens, 4..7 the others; a thread per value column
         const int c0 = (warp >> 2) * 32, quad = warp & 3;
-        if (warp_wait(smem_u32(&S.done), 0, abort_flag, lane)) {
+        if (spin_warp(smem_u32(&S.done[1]), 0, abort_flag)) {
             tc_fence_after();
             uint32_t d[32];
             SKV_LD32(tmem + ((uint32_t)(quad * 32) << 16) + c0, d);
