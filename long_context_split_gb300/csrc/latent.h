@@ -19,6 +19,16 @@ constexpr int kLatV = 128;                         // value columns of a head
 constexpr int kLatW = kLatNope + kLatV;            // weight rows of a head (key rows, then value rows)
 constexpr int kLatPad = 128;                       // each request's rows are padded to this many
 
+// The expanded keys (bf16) and values (f16) of 64 cached tokens and one head, in the order of the
+// shared-memory operands of their products, so that a warp of the expansion stores whole lines (32
+// tokens x 32 bytes) and the attention copies 16 KB at a time: eight groups of 16 columns, a
+// group 64 rows (tokens) of 32 bytes in the 32-byte swizzle (the two 16-byte halves of a row change
+// places where bit 2 of the row is set); the keys' groups, then the values'.
+constexpr int kLatUnit = 64;
+constexpr int kLatGroup = kLatUnit * 32;           // one 16-column group: 2 KB
+constexpr int kLatSide = 8 * kLatGroup;            // keys (or values) of a unit: 16 KB
+constexpr int kLatImage = 2 * kLatSide;
+
 struct LatentReq {
     int32_t seq_len;
     int32_t q_len;
@@ -60,8 +70,7 @@ struct LatentArgs {
     const LatentTask* tasks;
     const LatentBlock* blocks;
     void* rows;                // bf16 [padded rows][576]: the requests' latent rows
-    void* keys;                // bf16 [H][padded rows][128]
-    void* vals;                // f16 [H][padded rows][128]
+    void* kv;                  // [H][padded rows / 64] images of 64 keys and values, 32 KB each (see below)
     void* out;                 // bf16 [total_q][H][128]
     float* lse_out;            // may be null
     float* o_part;             // partial states of a split batch, or null: the tasks write final rows

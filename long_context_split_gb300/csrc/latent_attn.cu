@@ -49,7 +49,7 @@ namespace {
 
 constexpr int kRows = 128;                          // query tokens per tile (tensor-memory lanes)
 constexpr int kTiles = 2;
-constexpr int kKeys = 64;                           // keys per unit
+constexpr int kKeys = kLatUnit;                     // keys per unit
 constexpr int kTR = 4;                              // task ring slots
 constexpr int kSoftWarps = 4 * kTiles;
 constexpr int kTaskConsumers = kTiles + kSoftWarps; // per tile an MMA thread and 4 softmax warps
@@ -60,13 +60,13 @@ constexpr int kTmemTile = 256;                      // tensor-memory columns per
 constexpr int kColS = 128;
 constexpr int kTmemCols = kTiles * kTmemTile;
 
-constexpr int kQBoxes = kLatQ / 64, kVBoxes = kLatV / 64;
+constexpr int kQBoxes = kLatQ / 64;
 constexpr int kQBox = kRows * 128;
-constexpr int kKvBox = kKeys * 128;
+constexpr int kRBox = kKeys * 128;                  // the unit's rotary columns
 constexpr int kQTile = kQBoxes * kQBox;
 constexpr int kQBytes = kTiles * kQTile;
-constexpr int kKBytes = kQBoxes * kKvBox;            // a unit's keys: 24 KB
-constexpr int kVBytes = kVBoxes * kKvBox;            // a unit's values: 16 KB
+constexpr int kKBytes = kLatSide + kRBox;            // a unit's keys: 24 KB
+constexpr int kVBytes = kLatSide;                    // a unit's values: 16 KB
 constexpr int NS = 3;                                // slots of the key ring, and of the value ring
 
 struct Bars {
@@ -203,6 +203,18 @@ struct Ring {
     }
 };
 
+// shared-memory operand of 32-byte rows in the 32-byte swizzle
+__device__ __forceinline__ uint64_t desc_sw32(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return (desc_sw128(addr, lbo, sbo) & ~((uint64_t)7 << 61)) | ((uint64_t)6 << 61);
+}
+
+// `bytes` contiguous bytes (a multiple of 16, both ends 16-byte aligned) into shared memory
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
 // The producer's view of one ring: which tiles attend each slot's unit (only those release it),
 // and the phase parities of the tiles' releases and of the slot's loads.
 struct SlotUse {
@@ -239,13 +251,13 @@ struct SlotUse {
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
-latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
-                        const __grid_constant__ CUtensorMap tmap_r, const __grid_constant__ CUtensorMap tmap_v, LatentArgs a) {
+latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_r,
+                        LatentArgs a) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     unsigned char* sQ = smem;                              // tile x at x * kQTile
-    unsigned char* sK = sQ + kQBytes;                      // slot: 2 key boxes, the rotary box
-    unsigned char* sV = sK + NS * kKBytes;                 // slot: 2 value boxes
+    unsigned char* sK = sQ + kQBytes;                      // slot: the keys' image, the rotary box
+    unsigned char* sV = sK + NS * kKBytes;                 // slot: the values' image
     Bars& B = *(Bars*)(sV + NS * kVBytes);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -284,7 +296,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
     tc_fence_after();
     const uint32_t tmem = B.tmem_base;
     volatile int* abort_flag = &B.abort_flag;
-    const int padded = a.num_blocks * kLatPad;
+    const int units = a.num_blocks * (kLatPad / kKeys);
     auto give_up = [&](int site) {
         if (!*abort_flag) {
             set_error(a.err, ERR_TIMEOUT | site);
@@ -324,6 +336,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                         tma_2d(smem_u32(sQ + x * kQTile + j * kQBox), &tmap_q, t.head * kLatQ + 64 * j,
                                t.r.q_start + t.row0 + x * kRows, smem_u32(&B.q_full));
                 ++qn;
+                auto image = [&](int head, int y) { return (const char*)a.kv + ((size_t)head * units + y / kKeys) * kLatImage; };
                 // Keys two units ahead of values, the order in which the tiles release them: P V of unit
                 // u - 3 (the values' slot) is issued before S of unit u - 1 (the keys' slot of u + 2)
                 auto load_keys = [&](int u) -> bool {
@@ -333,9 +346,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     const uint32_t full = smem_u32(&B.k_full[s]), to = smem_u32(sK + s * kKBytes);
                     const int y = t.r.row_base + t.kb + u * kKeys;   // row of the copies
                     mbar_expect_tx(full, kKBytes);
-                    tma_2d(to, &tmap_k, 0, t.head * padded + y, full);
-                    tma_2d(to + kKvBox, &tmap_k, 64, t.head * padded + y, full);
-                    tma_2d(to + 2 * kKvBox, &tmap_r, kLatC, y, full);
+                    bulk_copy(to, image(t.head, y), kLatSide, full);
+                    tma_2d(to + kLatSide, &tmap_r, kLatC, y, full);
                     return true;
                 };
                 auto load_values = [&](int u) -> bool {
@@ -343,10 +355,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     if (!vu.wait_free(B.pv_done, s, abort_flag)) return false;
                     vu.use(s, u < t.nu[0], u < t.nu[1]);
                     const uint32_t full = smem_u32(&B.v_full[s]), to = smem_u32(sV + s * kVBytes);
-                    const int y = t.head * padded + t.r.row_base + t.kb + u * kKeys;
                     mbar_expect_tx(full, kVBytes);
-                    tma_2d(to, &tmap_v, 0, y, full);
-                    tma_2d(to + kKvBox, &tmap_v, 64, y, full);
+                    bulk_copy(to, image(t.head, t.r.row_base + t.kb + u * kKeys) + kLatSide, kLatSide, full);
                     return true;
                 };
                 ok = load_keys(0) && (t.n_units < 2 || load_keys(1));
@@ -397,11 +407,13 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     if (!spin_bar(smem_u32(&B.k_full[slot]), (gi / NS) & 1, abort_flag, true)) return false;
                     tc_fence_after();
                     const uint32_t scol = bufcol + kKeys * ((pc + u) & 1);
-                    const uint64_t kd = desc_sw128(smem_u32(sK + slot * kKBytes), 16, 1024);
+                    const uint64_t kd = desc_sw32(smem_u32(sK + slot * kKBytes), 16, 256);
+                    const uint64_t rd = desc_sw128(smem_u32(sK + slot * kKBytes + kLatSide), 16, 1024);
 #pragma unroll
                     for (int kk = 0; kk < kLatQ / 16; ++kk) {
                         const uint64_t ad = qd + (uint64_t)((((kk >> 2) * kQBox) + (kk & 3) * 32) >> 4);
-                        const uint64_t bd = kd + (uint64_t)((((kk >> 2) * kKvBox) + (kk & 3) * 32) >> 4);
+                        const uint64_t bd = kk < kLatNope / 16 ? kd + (uint64_t)((kk * kLatGroup) >> 4)
+                                                               : rd + (uint64_t)(((kk & 3) * 32) >> 4);
                         if (kk == 0) mma_f16c<0>(scol, ad, bd, id_s);
                         else mma_f16c<1>(scol, ad, bd, id_s);
                     }
@@ -416,10 +428,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     if (!spin_bar(smem_u32(&B.p_full[x][gp & 1]), (gp >> 1) & 1, abort_flag, true)) return false;
                     tc_fence_after();
                     const uint32_t pcol = bufcol + kKeys * (gp & 1);
-                    const uint64_t vd = desc_sw128(smem_u32(sV + slot * kVBytes), kKvBox, 1024);
+                    const uint64_t vd = desc_sw32(smem_u32(sV + slot * kVBytes), kLatGroup, 256);
                     mma_f16_ts(ocol, pcol, vd, id_o, u > 0 ? 1u : 0u);
 #pragma unroll
-                    for (int kk = 1; kk < 4; ++kk) mma_f16_tsc<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o);
+                    for (int kk = 1; kk < 4; ++kk) mma_f16_tsc<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 512) >> 4), id_o);   // 16 keys: 512 bytes
                     mma_commit(smem_u32(&B.pv_done[x][slot]));
                     return true;
                 };
@@ -602,15 +614,14 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
 }
 
 // ---------------------------------------------------------------- host
-cudaError_t make_map(CUtensorMap* m, const void* base, long long cols, long long rows, long long stride_elems, int box_rows,
-                     CUtensorMapDataType dtype = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
+cudaError_t make_map(CUtensorMap* m, const void* base, long long cols, long long rows, long long stride_elems, int box_rows) {
     auto enc = encode_fn();
     if (!enc) return cudaErrorNotSupported;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)stride_elems * 2};
     cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
     cuuint32_t es[2] = {1, 1};
-    CUresult r = enc(m, dtype, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -620,12 +631,10 @@ cudaError_t make_map(CUtensorMap* m, const void* base, long long cols, long long
 cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s) {
     if (a.num_tasks <= 0) return cudaSuccess;
     const long long rows = (long long)a.num_blocks * kLatPad;
-    CUtensorMap mq, mk, mr, mv;
+    CUtensorMap mq, mr;
     cudaError_t e;
     if ((e = make_map(&mq, a.q, (long long)a.heads * kLatQ, a.total_q, a.q_stride, kRows)) != cudaSuccess) return e;
-    if ((e = make_map(&mk, a.keys, kLatNope, a.heads * rows, kLatNope, kKeys)) != cudaSuccess) return e;
     if ((e = make_map(&mr, a.rows, kLatRow, rows, kLatRow, kKeys)) != cudaSuccess) return e;
-    if ((e = make_map(&mv, a.vals, kLatV, a.heads * rows, kLatV, kKeys, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != cudaSuccess) return e;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [&]() {
@@ -636,7 +645,7 @@ cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s) {
     if (sms <= 0) return cudaErrorInvalidDevice;
     {
         ProfileScope ps(SPLITKV_KERNEL_LATENT_ATTENTION, s);
-        latent_attention_kernel<<<std::min(sms, a.num_tasks), kThreads, kSmemBytes, s>>>(mq, mk, mr, mv, a);
+        latent_attention_kernel<<<std::min(sms, a.num_tasks), kThreads, kSmemBytes, s>>>(mq, mr, a);
     }
     return cudaGetLastError();
 }

@@ -4,17 +4,19 @@
 //
 // What bounds the product: 2 * 512 * 256 operations per token and head.  Streaming both
 // operands of 128 x 256 tiles from L2 takes 384 KB a tile, and L2 gave 13 TB/s of it at
-// 57 % of the tensor rate (218 us for 7.3k tokens and 128 heads).  So
-// a CTA keeps its 128 latent rows (128 KB) in shared memory while it walks over
-// heads, and a cluster of two CTAs (two row tiles, the same heads) shares each 64-column
-// box of the head's weights: each loads half of its 256 rows and multicasts it to both
-// (128 KB a tile and CTA from L2; XX us).
+// 57 % of the tensor rate (218 us for 7.3k tokens and 128 heads).  So a CTA keeps its 128
+// latent rows while it walks over heads, as the A operand in tensor memory (256 columns),
+// and a cluster of two CTAs (two row tiles, the same heads) shares every 64-column box of
+// weights: each loads half of its 128 rows and multicasts it to both.  That leaves 192 KB of shared
+// memory for a ring of twelve boxes: with the rows in shared memory and three boxes the
+// stores' traffic delayed the copies by more than the ring covered (215 us; 150 without the
+// stores; XX now).
 //
-// Roles: warp 0 TMA producer, warp 1 MMA thread (M = 128 rows, N = 256 weight rows,
-// K = 512 in eight boxes; two accumulators in tensor memory), warps 2..5 the epilogue,
-// which rounds the accumulator once and stores 32 bytes of a row per thread and
-// instruction while the next tile accumulates.  Values get f16's three more bits: they meet the
-// probabilities in an f16 product.
+// Roles: warp 0 TMA producer, warp 1 MMA thread (M = 128 rows, N = 128: a head's keys or
+// its values, K = 512 in eight boxes; two accumulators), warps 2..5 the epilogue, which
+// rounds an accumulator once and stores whole lines of the attention's operand images while
+// the next tile accumulates, and which brings a new row tile into tensor memory.  Values
+// get f16's three more bits: they meet the probabilities in an f16 product.
 //
 // A box may be overwritten once both CTAs' products have read it: each CTA's MMA
 // thread commits to both CTAs' barriers, and neither CTA leaves before the other.
@@ -35,13 +37,16 @@ constexpr int kEpiWarps = 4;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kCluster = 2;
 constexpr int kBoxes = kLatC / 64;
+constexpr int kN = 128;                            // weight rows of a tile: W_uk's or W_uv's of a head
 constexpr int kABox = kM * 128;                    // 128 latent rows x 64 columns
-constexpr int kBBox = kLatW * 128;                 // a head's 256 weight rows x 64 columns
-constexpr int NS = 3;                              // weight boxes in shared memory
-constexpr int kTmem = 2 * kLatW;
+constexpr int kBBox = kN * 128;                    // 128 weight rows x 64 columns
+constexpr int NS = kBoxes;                         // weight boxes in shared memory: a tile's, so that slots are constants
+constexpr int kColA = 0, kColAcc = 256;            // tensor memory: the rows (256 columns), two accumulators
+constexpr int kTmem = 512;
 
 struct Bars {
-    unsigned long long a_full, a_empty;
+    unsigned long long as_full[2], as_empty[2];    // staging of the rows on their way to tensor memory
+    unsigned long long a_ready;
     unsigned long long b_full[NS], b_empty[NS];
     unsigned long long acc_full[2], acc_empty[2];
     unsigned long long drain;
@@ -49,7 +54,7 @@ struct Bars {
     int abort_flag;
 };
 
-constexpr size_t kSmemBytes = 1024 + (size_t)kBoxes * kABox + (size_t)NS * kBBox + sizeof(Bars);
+constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kABox + (size_t)NS * kBBox + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -71,40 +76,60 @@ __device__ __forceinline__ void tma_2d_both(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
-__device__ __forceinline__ void commit_both(uint32_t bar) {
+__device__ __forceinline__ void commit_both_if(uint32_t bar, uint32_t cond) {
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-        "h"((uint16_t)3)
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
+        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3), "r"(cond)
         : "memory");
 }
 
-__device__ __forceinline__ void store32(void* p, const uint32_t* w) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
-                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+// 16 packed columns, their 16-byte halves exchanged when `swap`
+__device__ __forceinline__ void store32(void* p, const uint32_t* w, int swap) {
+    uint32_t x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        x[k] = swap ? w[4 + k] : w[k];
+        x[4 + k] = swap ? w[k] : w[4 + k];
+    }
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+                 "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
                  : "memory");
 }
 
-// Tiles (row pair, head), heads innermost; cluster c takes [c n / clusters, (c + 1) n / clusters).
+// Tiles (row pair, head, keys or values); cluster c takes [c n / clusters, (c + 1) n / clusters).
+struct Tile {
+    int pair, head, side;
+};
+__device__ __forceinline__ Tile tile_of(int t, int heads) {
+    Tile x;
+    x.pair = t / (2 * heads);
+    x.head = t % (2 * heads) / 2;
+    x.side = t % 2;
+    return x;
+}
+
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, LatentArgs a,
                      int num_tiles) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sA = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char* sB = sA + kBoxes * kABox;
+    unsigned char* sB = sA + 2 * kABox;
     Bars& B = *(Bars*)(sB + NS * kBBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank(), cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster;
     const int t0 = (int)((long long)cluster * num_tiles / clusters), t1 = (int)((long long)(cluster + 1) * num_tiles / clusters);
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(&B.a_full), 1);
-        mbar_init(smem_u32(&B.a_empty), 1);
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(smem_u32(&B.as_full[k]), 1);
+            mbar_init(smem_u32(&B.as_empty[k]), kEpiWarps);
+            mbar_init(smem_u32(&B.acc_full[k]), 1);
+            mbar_init(smem_u32(&B.acc_empty[k]), kEpiWarps);
+        }
+        mbar_init(smem_u32(&B.a_ready), kEpiWarps);
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&B.b_full[s]), 1);
             mbar_init(smem_u32(&B.b_empty[s]), kCluster);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_u32(&B.acc_full[b]), 1);
-            mbar_init(smem_u32(&B.acc_empty[b]), kEpiWarps);
         }
         mbar_init(smem_u32(&B.drain), 1);
         B.abort_flag = 0;
@@ -131,30 +156,30 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
     if (warp == 0) {
         // ===================== TMA producer (lane 0) =====================
         if (lane == 0) {
-            uint32_t it = 0, an = 0;
+            uint32_t it = 0, an = 0;   // weight boxes, row boxes so far
             int pair = -1;
             bool ok = a.inject != 1;   // (test hook: load nothing)
             for (int t = t0; t < t1 && ok; ++t) {
-                if (t / a.heads != pair) {
-                    pair = t / a.heads;
-                    if (!spin_bar(smem_u32(&B.a_empty), (an & 1) ^ 1, abort_flag, true)) { give_up(SITE_EMPTY_WAIT); break; }
+                const Tile x = tile_of(t, a.heads);
+                if (x.pair != pair) {
                     // (an odd last row tile: its partner's rows are the zero fill past the tensor)
-                    mbar_expect_tx(smem_u32(&B.a_full), kBoxes * kABox);
-                    for (int j = 0; j < kBoxes; ++j)
-                        tma_2d(smem_u32(sA + j * kABox), &ma, 64 * j, (pair * kCluster + rank) * kM, smem_u32(&B.a_full));
-                    ++an;
-                }
-                const int y = (t % a.heads) * kLatW + rank * (kLatW / kCluster);
-                for (int j = 0; j < kBoxes; ++j, ++it) {
-                    const int s = (int)(it % NS);
-                    if (!spin_bar(smem_u32(&B.b_empty[s]), ((it / NS) & 1) ^ 1, abort_flag, true)) {
-                        give_up(SITE_EMPTY_WAIT);
-                        ok = false;
-                        break;
+                    pair = x.pair;
+                    for (int j = 0; j < kBoxes && ok; ++j, ++an) {
+                        ok = spin_bar(smem_u32(&B.as_empty[an & 1]), ((an >> 1) & 1) ^ 1, abort_flag, true);
+                        if (!ok) break;
+                        mbar_expect_tx(smem_u32(&B.as_full[an & 1]), kABox);
+                        tma_2d(smem_u32(sA + (an & 1) * kABox), &ma, 64 * j, (pair * kCluster + rank) * kM, smem_u32(&B.as_full[an & 1]));
                     }
+                }
+                const int y = x.head * kLatW + x.side * kN + rank * (kN / kCluster);
+                for (int j = 0; j < kBoxes && ok; ++j, ++it) {
+                    const int s = (int)(it % NS);
+                    ok = spin_bar(smem_u32(&B.b_empty[s]), ((it / NS) & 1) ^ 1, abort_flag, true);
+                    if (!ok) break;
                     mbar_expect_tx(smem_u32(&B.b_full[s]), kBBox);
                     tma_2d_both(smem_u32(sB + s * kBBox + rank * (kBBox / kCluster)), &mb, 64 * j, y, smem_u32(&B.b_full[s]));
                 }
+                if (!ok) give_up(SITE_EMPTY_WAIT);
             }
             // no copy may still be landing when the CTA leaves
             bool landed = true;
@@ -162,75 +187,110 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                 const uint32_t last = it - 1 - k;
                 landed = spin_bar(smem_u32(&B.b_full[last % NS]), (last / NS) & 1, abort_flag, false) && landed;
             }
-            if (an) landed = spin_bar(smem_u32(&B.a_full), (an - 1) & 1, abort_flag, false) && landed;
+            for (uint32_t k = 0; k < 2 && k < an; ++k) {
+                const uint32_t last = an - 1 - k;
+                landed = spin_bar(smem_u32(&B.as_full[last & 1]), (last >> 1) & 1, abort_flag, false) && landed;
+            }
             if (!landed) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ===================== MMA issuer (lane 0) =====================
-        if (lane == 0) {
-            constexpr uint32_t id = idesc_bf16(kM, kLatW, 0);
-            uint32_t it = 0, an = 0, n = 0;
-            int pair = -1;
-            bool ok = true;
-            for (int t = t0; t < t1 && ok; ++t, ++n) {
-                const uint32_t buf = n & 1, acc = tmem + buf * kLatW;
-                if (t / a.heads != pair) {
-                    pair = t / a.heads;
-                    if (!spin_bar(smem_u32(&B.a_full), an & 1, abort_flag, true)) { give_up(SITE_FULL_WAIT); break; }
-                    ++an;
-                }
-                if (!spin_bar(smem_u32(&B.acc_empty[buf]), ((n >> 1) & 1) ^ 1, abort_flag, true)) { give_up(SITE_EMPTY_WAIT); break; }
-                for (int j = 0; j < kBoxes; ++j, ++it) {
-                    const int s = (int)(it % NS);
-                    if (!spin_bar(smem_u32(&B.b_full[s]), (it / NS) & 1, abort_flag, true)) {
-                        give_up(SITE_FULL_WAIT);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t ad = desc_sw128(smem_u32(sA + j * kABox), 16, 1024);
-                    const uint64_t bd = desc_sw128(smem_u32(sB + s * kBBox), 16, 1024);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mma_f16(acc, ad + (uint64_t)((k * 32) >> 4), bd + (uint64_t)((k * 32) >> 4), id, (j | k) != 0 ? 1u : 0u);
-                    commit_both(smem_u32(&B.b_empty[s]));
-                }
-                if (!ok) break;
-                mma_commit(smem_u32(&B.acc_full[buf]));
-                if (t + 1 < t1 && (t + 1) / a.heads != pair) mma_commit(smem_u32(&B.a_empty));
+        // ===================== MMA issuer (the warp in step, one elected lane issues) =====================
+        constexpr uint32_t id = idesc_bf16(kM, kN, 0);
+        const uint32_t leader = elect_one();
+        const uint64_t bd0 = desc_sw128(smem_u32(sB), 16, 1024);
+        const uint32_t full0 = smem_u32(&B.b_full[0]), empty0 = smem_u32(&B.b_empty[0]);
+        uint32_t an = 0, n = 0;
+        int pair = -1;
+        bool ok = true;
+        for (int t = t0; t < t1 && ok; ++t, ++n) {
+            const uint32_t buf = n & 1, acc = tmem + kColAcc + buf * kN;
+            const Tile x = tile_of(t, a.heads);
+            if (x.pair != pair) {
+                pair = x.pair;
+                if (!spin_warp(smem_u32(&B.a_ready), an & 1, abort_flag)) { give_up(SITE_FULL_WAIT); break; }
+                ++an;
             }
-            mma_commit(smem_u32(&B.drain));
-            if (!spin_bar(smem_u32(&B.drain), 0, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+            if (!spin_warp(smem_u32(&B.acc_empty[buf]), ((n >> 1) & 1) ^ 1, abort_flag)) { give_up(SITE_EMPTY_WAIT); break; }
+            // (unrolled over the slots, descriptors by constant steps: one thread issues everything,
+            // and its own instructions set the pace of small products)
+#pragma unroll
+            for (int j = 0; j < kBoxes; ++j) {
+                if (ok && !spin_warp(full0 + 8 * j, n & 1, abort_flag)) ok = false;
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {   // 16 columns of the rows: 8 columns of tensor memory
+                    const uint64_t bd = bd0 + (uint64_t)((j * kBBox + k * 32) >> 4);
+                    if (j + k == 0) mma_f16_ts_if<0>(acc, tmem + kColA, bd, id, leader);
+                    else mma_f16_ts_if<1>(acc, tmem + kColA + 32 * j + 8 * k, bd, id, leader);
+                }
+                commit_both_if(empty0 + 8 * j, leader);
+            }
+            if (!ok) { give_up(SITE_FULL_WAIT); break; }
+            mma_commit_if(smem_u32(&B.acc_full[buf]), leader);
         }
+        mma_commit_if(smem_u32(&B.drain), leader);
+        if (!spin_warp_drain(smem_u32(&B.drain), 0, abort_flag) && lane == 0) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
         __syncwarp();
     } else {
-        // ===================== epilogue: a thread per row of the tile =====================
+        // ===================== rows into tensor memory; epilogue: a thread per row =====================
         const int quad = warp & 3;
-        const size_t rows = (size_t)a.num_blocks * kLatPad;
+        const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+        const int units = a.num_blocks * (kLatPad / kLatUnit);
         float vmax = 0.f;
-        uint32_t n = 0;
-        for (int t = t0; t < t1; ++t, ++n) {
+        uint32_t n = 0, an = 0;
+        int pair = -1;
+        bool ok = true;
+        for (int t = t0; t < t1 && ok; ++t, ++n) {
             const uint32_t buf = n & 1;
-            const size_t row = (size_t)(t / a.heads * kCluster + rank) * kM + 32 * quad + lane;
-            const size_t at = ((size_t)(t % a.heads) * rows + row) * kLatNope;
+            const Tile x = tile_of(t, a.heads);
+            if (x.pair != pair) {
+                // every product of the previous rows is done: this warp has seen its last tile's end
+                pair = x.pair;
+                for (int j = 0; j < kBoxes && ok; ++j, ++an) {
+                    ok = spin_warp(smem_u32(&B.as_full[an & 1]), (an >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const unsigned char* src = sA + (an & 1) * kABox + (32 * quad + lane) * 128;
+                    uint32_t v[32];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint4 w = *(const uint4*)(src + ((k ^ (lane & 7)) << 4));
+                        v[4 * k] = w.x;
+                        v[4 * k + 1] = w.y;
+                        v[4 * k + 2] = w.z;
+                        v[4 * k + 3] = w.w;
+                    }
+                    SKV_ST32(lanes + kColA + 32 * j, v);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&B.as_empty[an & 1]));
+                }
+                if (!ok) { give_up(SITE_FULL_WAIT); break; }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&B.a_ready));
+            }
+            const int row = (x.pair * kCluster + rank) * kM + 32 * quad + lane;
+            const int unit = row / kLatUnit, r = row % kLatUnit, swap = (r >> 2) & 1;
+            char* image = (char*)a.kv + ((size_t)x.head * units + unit) * kLatImage + x.side * kLatSide + r * 32;
             if (!spin_warp(smem_u32(&B.acc_full[buf]), (n >> 1) & 1, abort_flag)) {
                 give_up(SITE_FULL_WAIT);
                 break;
             }
             tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * kLatW;
+            const uint32_t acc = lanes + kColAcc + buf * kN;
 #pragma unroll 1
-            for (int c = 0; c < kLatW; c += 32) {
+            for (int c = 0; c < kN; c += 32) {
                 uint32_t v[32], w[16];
                 SKV_LD32(acc + c, v);
                 tc_wait_ld();
-                if (c + 32 == kLatW) {      // the accumulator is read: the tile after next may overwrite it
+                if (c + 32 == kN) {         // the accumulator is read: the tile after next may overwrite it
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&B.acc_empty[buf]));
                 }
-                if (c < kLatNope) {
+                if (x.side == 0) {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
@@ -246,10 +306,10 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                         if (m < INFINITY) vmax = fmaxf(vmax, m);
                     }
                 }
-                if (row < rows) {
-                    char* to = c < kLatNope ? (char*)a.keys + (at + c) * 2 : (char*)a.vals + (at + c - kLatNope) * 2;
-                    store32(to, w);
-                    store32(to + 32, w + 8);
+                if (unit < units) {         // (an odd last row tile has no partner)
+                    char* to = image + c / 16 * kLatGroup;
+                    store32(to, w, swap);
+                    store32(to + kLatGroup, w + 8, swap);
                 }
             }
         }
@@ -340,7 +400,7 @@ cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s) {
     CUtensorMap ma, mb;
     cudaError_t e;
     if ((e = make_map(&ma, a.rows, kLatRow, rows, kM)) != cudaSuccess) return e;
-    if ((e = make_map(&mb, a.w, kLatC, (long long)a.heads * kLatW, kLatW / kCluster)) != cudaSuccess) return e;
+    if ((e = make_map(&mb, a.w, kLatC, (long long)a.heads * kLatW, kN / kCluster)) != cudaSuccess) return e;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [&]() {
@@ -349,7 +409,7 @@ cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s) {
     if (attr_err != cudaSuccess) return attr_err;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const int tiles = (a.num_blocks + kCluster - 1) / kCluster * a.heads;
+    const int tiles = (a.num_blocks + kCluster - 1) / kCluster * a.heads * 2;
     {
         ProfileScope ps(SPLITKV_KERNEL_LATENT_EXPAND, s);
         latent_expand_kernel<<<kCluster * std::max(1, std::min(sms / kCluster, tiles)), kThreads, kSmemBytes, s>>>(ma, mb, a, tiles);

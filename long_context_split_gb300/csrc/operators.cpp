@@ -193,7 +193,7 @@ struct splitkv_latent_plan_s {
     int64_t num_states = 0;
     std::vector<unsigned char> image;       // control block and descriptors
     size_t off_tasks = 0, off_reqs = 0, off_blocks = 0, off_indptr = 0;
-    size_t off_rows = 0, off_keys = 0, off_vals = 0, off_opart = 0, off_lse = 0, ws_bytes = 0;
+    size_t off_rows = 0, off_kv = 0, off_opart = 0, off_lse = 0, ws_bytes = 0;
 };
 
 namespace {
@@ -291,10 +291,8 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
     put(pl->off_indptr, pl->state_indptr.data(), pl->state_indptr.size() * sizeof(int32_t));
     pl->off_rows = off;
     off = align256(off + (size_t)rows * kLatRow * 2);
-    pl->off_keys = off;
-    off = align256(off + (size_t)rows * H * kLatNope * 2);
-    pl->off_vals = off;
-    off = align256(off + (size_t)rows * H * kLatV * 2);
+    pl->off_kv = off;
+    off = align256(off + (size_t)(rows / kLatUnit) * H * kLatImage);
     pl->off_opart = off;
     off = align256(off + (size_t)pl->num_states * kLatV * 4);
     pl->off_lse = off;
@@ -388,8 +386,7 @@ splitkv_status splitkv_latent_expanded(const splitkv_problem* prob, const splitk
     a.tasks = (const LatentTask*)(base + plan->off_tasks);
     a.blocks = (const LatentBlock*)(base + plan->off_blocks);
     a.rows = base + plan->off_rows;
-    a.keys = base + plan->off_keys;
-    a.vals = base + plan->off_vals;
+    a.kv = base + plan->off_kv;
     if (plan->num_states > 0) {
         a.o_part = (float*)(base + plan->off_opart);
         a.lse_part = (float*)(base + plan->off_lse);

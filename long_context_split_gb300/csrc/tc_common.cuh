@@ -112,6 +112,14 @@ __device__ __forceinline__ bool spin_warp(uint32_t bar, uint32_t parity, volatil
     return true;
 }
 
+// the same without watching the abort flag (for draining what this CTA has in flight)
+__device__ __forceinline__ bool spin_warp_drain(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    unsigned long long t0 = 0;
+    for (uint32_t it = 0; !__all_sync(0xffffffffu, mbar_try(bar, parity)); ++it)
+        if (__any_sync(0xffffffffu, spin_over(it, t0, abort_flag, false))) return false;
+    return true;
+}
+
 __device__ __forceinline__ void set_error(int32_t* err, int32_t code) { atomicCAS(err, 0, code); }
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
@@ -181,6 +189,30 @@ __device__ __forceinline__ void mma_f16_tsc(uint32_t d, uint32_t a_tmem, uint64_
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(
             d),
         "r"(a_tmem), "l"(b), "r"(idesc), "n"(ACC));
+}
+
+// 1 in one lane of the (converged) warp, the same at every call.  Issuing from a warp in step
+// with the instruction predicated on its leader keeps descriptors and addresses in uniform
+// registers; in a branch of one lane each product first moves them there.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+
+template <int ACC>
+__device__ __forceinline__ void mma_f16_if(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t cond) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "n"(ACC), "r"(cond));
+}
+template <int ACC>
+__device__ __forceinline__ void mma_f16_ts_if(uint32_t d, uint32_t a_tmem, uint64_t b, uint32_t idesc, uint32_t cond) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b), "r"(idesc), "n"(ACC), "r"(cond));
 }
 
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
