@@ -373,81 +373,93 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
         }
         __syncwarp();
     } else if (warp == 1 || warp == kIssuerWarp1) {
-        // ===================== MMA issuer of tile x (lane 0) =====================
+        // ===================== MMA issuer of tile x (the warp in step, one elected lane issues) ==========
         const int x = warp == 1 ? 0 : 1;
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_bf16(kRows, kKeys, 0);
-            constexpr uint32_t id_o = idesc_f16(kRows, kLatV, 1);     // P and V both f16
-            const uint64_t qd = desc_sw128(smem_u32(sQ + x * kQTile), 16, 1024);
-            const uint32_t ocol = tmem + x * kTmemTile, bufcol = ocol + kColS;
-            uint32_t item = 0, qn = 0;
-            uint32_t pc = 0;      // units this tile attended so far
-            uint32_t tn = 0;      // tasks this tile finished
-            bool ok = true;
-            Ring ring;
-            while (ok) {
-                const int id = ring.next(B, abort_flag, 0, false);
-                if (id == -2) { give_up(SITE_FULL_WAIT); break; }
-                if (id < 0) break;
-                const Task t = read_task(a, id);
-                if (t.n_units == 0) continue;
-                const uint32_t item0 = item;      // slot of unit u: (item0 + u) % NS
-                item += t.n_units;
-                const int nu = x ? t.nu[1] : t.nu[0];
-                if (!spin_bar(smem_u32(&B.q_full), qn & 1, abort_flag, true)) { give_up(SITE_FULL_WAIT); break; }
-                ++qn;
-                if (nu == 0) {                    // nothing to attend: release the queries
-                    mbar_arrive(smem_u32(&B.q_empty));
-                    continue;
-                }
+        const uint32_t leader = elect_one();
+        constexpr uint32_t id_s = idesc_bf16(kRows, kKeys, 0);
+        constexpr uint32_t id_o = idesc_f16(kRows, kLatV, 1);     // P and V both f16
+        const uint64_t qd = desc_sw128(smem_u32(sQ + x * kQTile), 16, 1024);
+        const uint64_t kd0 = desc_sw32(smem_u32(sK), 16, 256), rd0 = desc_sw128(smem_u32(sK + kLatSide), 16, 1024);
+        const uint64_t vd0 = desc_sw32(smem_u32(sV), kLatGroup, 256);
+        const uint32_t ocol = tmem + x * kTmemTile, bufcol = ocol + kColS;
+        const uint32_t k_full = smem_u32(&B.k_full[0]), v_full = smem_u32(&B.v_full[0]), s_full = smem_u32(&B.s_full[x][0]),
+                       pv_done = smem_u32(&B.pv_done[x][0]), p_full = smem_u32(&B.p_full[x][0]);
+        uint32_t qn = 0;
+        uint32_t pc = 0;      // units this tile attended so far
+        uint32_t tn = 0;      // tasks this tile finished
+        // ring positions of the next S and of the next P V: slot and the parity of its loads
+        uint32_t s_slot = 0, s_par = 0, v_slot = 0, v_par = 0;
+        auto advance = [](uint32_t& slot, uint32_t& par) {
+            if (++slot == NS) {
+                slot = 0;
+                par ^= 1;
+            }
+        };
+        bool ok = true;
+        Ring ring;
+        while (ok) {
+            const int id = ring.next(B, abort_flag, lane, true);
+            if (id == -2) { give_up(SITE_FULL_WAIT); break; }
+            if (id < 0) break;
+            const Task t = read_task(a, id);
+            if (t.n_units == 0) continue;
+            const int nu = x ? t.nu[1] : t.nu[0];
+            if (!spin_warp(smem_u32(&B.q_full), qn & 1, abort_flag)) { give_up(SITE_FULL_WAIT); break; }
+            ++qn;
+            if (nu == 0 && lane == 0) mbar_arrive(smem_u32(&B.q_empty));   // nothing to attend: release the queries
+            tc_fence_after();
+            auto issue_s = [&](uint32_t n) -> bool {       // n: the tile's unit count, which picks the S buffer
+                if (!spin_warp(k_full + 8 * s_slot, s_par, abort_flag)) return false;
                 tc_fence_after();
-                auto issue_s = [&](int u) -> bool {
-                    const uint32_t gi = item0 + u;
-                    const int slot = (int)(gi % NS);
-                    if (!spin_bar(smem_u32(&B.k_full[slot]), (gi / NS) & 1, abort_flag, true)) return false;
-                    tc_fence_after();
-                    const uint32_t scol = bufcol + kKeys * ((pc + u) & 1);
-                    const uint64_t kd = desc_sw32(smem_u32(sK + slot * kKBytes), 16, 256);
-                    const uint64_t rd = desc_sw128(smem_u32(sK + slot * kKBytes + kLatSide), 16, 1024);
+                const uint32_t scol = bufcol + kKeys * (n & 1);
+                const uint64_t kd = kd0 + (uint64_t)(s_slot * (kKBytes >> 4)), rd = rd0 + (uint64_t)(s_slot * (kKBytes >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < kLatQ / 16; ++kk) {
-                        const uint64_t ad = qd + (uint64_t)((((kk >> 2) * kQBox) + (kk & 3) * 32) >> 4);
-                        const uint64_t bd = kk < kLatNope / 16 ? kd + (uint64_t)((kk * kLatGroup) >> 4)
-                                                               : rd + (uint64_t)(((kk & 3) * 32) >> 4);
-                        if (kk == 0) mma_f16c<0>(scol, ad, bd, id_s);
-                        else mma_f16c<1>(scol, ad, bd, id_s);
-                    }
-                    mma_commit(smem_u32(&B.s_full[x][slot]));
-                    return true;
-                };
-                auto issue_pv = [&](int u) -> bool {
-                    if (u == 0 && !spin_bar(smem_u32(&B.o_empty[x]), (tn & 1) ^ 1, abort_flag, true)) return false;
-                    const uint32_t gi = item0 + u, gp = pc + u;
-                    const int slot = (int)(gi % NS);
-                    if (!spin_bar(smem_u32(&B.v_full[slot]), (gi / NS) & 1, abort_flag, true)) return false;
-                    if (!spin_bar(smem_u32(&B.p_full[x][gp & 1]), (gp >> 1) & 1, abort_flag, true)) return false;
-                    tc_fence_after();
-                    const uint32_t pcol = bufcol + kKeys * (gp & 1);
-                    const uint64_t vd = desc_sw32(smem_u32(sV + slot * kVBytes), kLatGroup, 256);
-                    mma_f16_ts(ocol, pcol, vd, id_o, u > 0 ? 1u : 0u);
+                for (int kk = 0; kk < kLatQ / 16; ++kk) {
+                    const uint64_t ad = qd + (uint64_t)((((kk >> 2) * kQBox) + (kk & 3) * 32) >> 4);
+                    const uint64_t bd = kk < kLatNope / 16 ? kd + (uint64_t)((kk * kLatGroup) >> 4)
+                                                           : rd + (uint64_t)(((kk & 3) * 32) >> 4);
+                    if (kk == 0) mma_f16_if<0>(scol, ad, bd, id_s, leader);
+                    else mma_f16_if<1>(scol, ad, bd, id_s, leader);
+                }
+                mma_commit_if(s_full + 8 * s_slot, leader);
+                advance(s_slot, s_par);
+                return true;
+            };
+            auto issue_pv = [&](uint32_t n, bool first) -> bool {
+                if (first && !spin_warp(smem_u32(&B.o_empty[x]), (tn & 1) ^ 1, abort_flag)) return false;
+                if (!spin_warp(v_full + 8 * v_slot, v_par, abort_flag)) return false;
+                if (!spin_warp(p_full + 8 * (n & 1), (n >> 1) & 1, abort_flag)) return false;
+                tc_fence_after();
+                const uint32_t pcol = bufcol + kKeys * (n & 1);
+                const uint64_t vd = vd0 + (uint64_t)(v_slot * (kVBytes >> 4));
+                if (first) mma_f16_ts_if<0>(ocol, pcol, vd, id_o, leader);
+                else mma_f16_ts_if<1>(ocol, pcol, vd, id_o, leader);
 #pragma unroll
-                    for (int kk = 1; kk < 4; ++kk) mma_f16_tsc<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 512) >> 4), id_o);   // 16 keys: 512 bytes
-                    mma_commit(smem_u32(&B.pv_done[x][slot]));
-                    return true;
-                };
-                ok = issue_s(0);
-                for (int u = 0; ok && u + 1 < nu; ++u) ok = issue_s(u + 1) && issue_pv(u);
-                if (ok) mma_commit(smem_u32(&B.q_empty));   // every S of the task is issued
-                if (ok) ok = issue_pv(nu - 1);
+                for (int kk = 1; kk < 4; ++kk)     // 16 keys: 8 columns of P, 512 bytes of V
+                    mma_f16_ts_if<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 512) >> 4), id_o, leader);
+                mma_commit_if(pv_done + 8 * v_slot, leader);
+                advance(v_slot, v_par);
+                return true;
+            };
+            if (nu > 0) {
+                ok = issue_s(pc);
+                for (int u = 0; ok && u + 1 < nu; ++u) ok = issue_s(pc + u + 1) && issue_pv(pc + u, u == 0);
+                if (ok) mma_commit_if(smem_u32(&B.q_empty), leader);   // every S of the task is issued
+                if (ok) ok = issue_pv(pc + nu - 1, nu == 1);
                 if (!ok) { give_up(SITE_FULL_WAIT); break; }
-                mma_commit(smem_u32(&B.o_full[x]));
+                mma_commit_if(smem_u32(&B.o_full[x]), leader);
                 pc += nu;
                 ++tn;
             }
-            // every product issued here completes before tensor memory is released
-            mma_commit(smem_u32(&B.drain[x]));
-            if (!spin_bar(smem_u32(&B.drain[x]), 0, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+            // units that only the other tile attends pass by in the rings
+            for (int u = nu; u < t.n_units; ++u) {
+                advance(s_slot, s_par);
+                advance(v_slot, v_par);
+            }
         }
+        // every product issued here completes before tensor memory is released
+        mma_commit_if(smem_u32(&B.drain[x]), leader);
+        if (!spin_warp_drain(smem_u32(&B.drain[x]), 0, abort_flag) && lane == 0) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
         __syncwarp();
     } else {
         // ===================== softmax + epilogue (thread = query token of tile x) =====================
