@@ -307,14 +307,17 @@ mla_partial_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
         __syncwarp();
     } else if (warp == 1) {
-        // ===================== MMA thread (lane 0) =====================
+        // ===================== MMA warp (in step; one elected lane issues) =====================
         // Per unit: S (nine key boxes), then P V (the value slots) once its P is in.  Ring
         // slots are read in the producer's order.  A full unit's issue code is straight-line
         // (boxes and k-steps unrolled, operand sources and accumulate flags compile-time):
         // tcgen05 issue from one thread queues only a few MMAs, and run-time loops and branches
         // between them left the tensor pipe idle (measured: 2,507 cycles for the score
-        // product's 36 MMAs unrolled against 6,052 in a loop over boxes).
-        if (lane == 0) {
+        // product's 36 MMAs unrolled against 6,052 in a loop over boxes).  The whole warp runs
+        // it and one elected lane issues: in a branch of one lane, descriptors first move to
+        // uniform registers (64 requests, log-uniform 1k..16k tokens: 197 us so, 181 now).
+        {
+            const uint32_t leader = elect_one();
             constexpr uint32_t id_s = idesc_bf16(kHeads, kUnit, 0);
             constexpr uint32_t id_o = idesc_bf16(kHeads, kHalfV, 1);
             const uint64_t kdesc0 = desc_sw128(smem_u32(sRing), 16, 1024);     // + 1024 per slot (16 KB >> 4)
@@ -335,24 +338,24 @@ mla_partial_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     const int kk = 2 * j + ks;
                     const uint32_t hi = dcol + (uint32_t)(64 * (kk >> 2) + 8 * (kk & 3));
                     const uint64_t bd = vd + (uint64_t)((ks * 2048) >> 4);
-                    if (ks == 0) mma_f16_ts(tmem + kColO, hi, bd, id_o, first_acc);
-                    else mma_f16_tsc<1>(tmem + kColO, hi, bd, id_o);
-                    mma_f16_tsc<1>(tmem + kColO, hi + 32, bd, id_o);
+                    if (ks == 0 && !first_acc) mma_f16_ts_if<0>(tmem + kColO, hi, bd, id_o, leader);
+                    else mma_f16_ts_if<1>(tmem + kColO, hi, bd, id_o, leader);
+                    mma_f16_ts_if<1>(tmem + kColO, hi + 32, bd, id_o, leader);
                 }
             };
             auto slot_done = [&]() {
-                mma_commit(empty0 + 8u * rs);
+                mma_commit_if(empty0 + 8u * rs, leader);
                 rs = rs == kNS - 1 ? 0u : rs + 1u;
                 rph ^= rs == 0u ? 1u : 0u;
             };
             while (ok) {
-                const int item = ring.next(B, abort_flag, 0, false);
+                const int item = ring.next(B, abort_flag, lane, true);
                 if (item == -2) { give_up(SITE_FULL_WAIT); ok = false; break; }
                 if (item < 0) break;
                 const ItemInfo ti = item_info(a, item);
                 if (ti.empty) continue;
-                if (!wait_bar(smem_u32(&B.qt_full), qn & 1, abort_flag, true) ||
-                    !wait_bar(smem_u32(&B.qs_full), qn & 1, abort_flag, true)) {
+                if (!spin_warp(smem_u32(&B.qt_full), qn & 1, abort_flag) ||
+                    !spin_warp(smem_u32(&B.qs_full), qn & 1, abort_flag)) {
                     give_up(SITE_FULL_WAIT); ok = false; break;
                 }
                 ++qn;
@@ -361,41 +364,41 @@ mla_partial_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     // ---- S = Q K^T over the nine key boxes ----
 #pragma unroll
                     for (int c = 0; c < kBoxes; ++c) {
-                        if (!wait_bar(full0 + 8u * rs, rph, abort_flag, true)) { ok = false; break; }
+                        if (!spin_warp(full0 + 8u * rs, rph, abort_flag)) { ok = false; break; }
                         tc_fence_after();
                         const uint64_t kd = kdesc0 + ((uint64_t)rs << 10);
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {   // 16 latent columns per k-step: 32 bytes
                             if (c < kQTmem) {               // query columns 64 c + 16 kk ..: tensor-memory column 32 c + 8 kk
-                                if (c == 0 && kk == 0) mma_f16_tsc<0>(dcol, tmem + kColQ, kd, id_s);
-                                else mma_f16_tsc<1>(dcol, tmem + kColQ + 32 * c + 8 * kk, kd + (uint64_t)(2 * kk), id_s);
+                                if (c == 0 && kk == 0) mma_f16_ts_if<0>(dcol, tmem + kColQ, kd, id_s, leader);
+                                else mma_f16_ts_if<1>(dcol, tmem + kColQ + 32 * c + 8 * kk, kd + (uint64_t)(2 * kk), id_s, leader);
                             } else {
-                                mma_f16c<1>(dcol, qdesc0 + (uint64_t)(((c - kQTmem) * kSlot) >> 4) + (uint64_t)(2 * kk),
-                                            kd + (uint64_t)(2 * kk), id_s);
+                                mma_f16_if<1>(dcol, qdesc0 + (uint64_t)(((c - kQTmem) * kSlot) >> 4) + (uint64_t)(2 * kk),
+                                              kd + (uint64_t)(2 * kk), id_s, leader);
                             }
                         }
                         slot_done();
                     }
                     if (!ok) break;
-                    mma_commit(smem_u32(&B.s_full));
-                    mma_commit_if(smem_u32(&B.q_empty), u == ti.n_units - 1);
+                    mma_commit_if(smem_u32(&B.s_full), leader);
+                    mma_commit_if(smem_u32(&B.q_empty), u == ti.n_units - 1 ? leader : 0u);
                     // ---- O += P V once P is in ----
                     const uint32_t g = gi + u;
-                    if (u == 0 && !wait_bar(smem_u32(&B.o_empty), (tn & 1) ^ 1, abort_flag, true)) { ok = false; break; }
-                    if (!wait_bar(smem_u32(&B.p_full), g & 1, abort_flag, true)) { ok = false; break; }
+                    if (u == 0 && !spin_warp(smem_u32(&B.o_empty), (tn & 1) ^ 1, abort_flag)) { ok = false; break; }
+                    if (!spin_warp(smem_u32(&B.p_full), g & 1, abort_flag)) { ok = false; break; }
                     tc_fence_after();
                     const int nv = value_slots(unit_keys(ti, u));
                     if (nv == 4) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            if (!wait_bar(full0 + 8u * rs, rph, abort_flag, true)) { ok = false; break; }
+                            if (!spin_warp(full0 + 8u * rs, rph, abort_flag)) { ok = false; break; }
                             tc_fence_after();
                             pv_slot(j, (u > 0 || j > 0) ? 1u : 0u);
                             slot_done();
                         }
                     } else {   // the item's last unit, 1..3 value slots
                         for (int j = 0; j < nv; ++j) {
-                            if (!wait_bar(full0 + 8u * rs, rph, abort_flag, true)) { ok = false; break; }
+                            if (!spin_warp(full0 + 8u * rs, rph, abort_flag)) { ok = false; break; }
                             tc_fence_after();
                             pv_slot(j, (u > 0 || j > 0) ? 1u : 0u);
                             slot_done();
@@ -403,14 +406,14 @@ mla_partial_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     }
                 }
                 if (!ok) { give_up(SITE_FULL_WAIT); break; }
-                mma_commit(smem_u32(&B.o_full));
+                mma_commit_if(smem_u32(&B.o_full), leader);
                 gi += ti.n_units;
                 ++tn;
             }
             // every MMA issued here completes before tensor memory is released: a final
             // commit tracks all of this thread's earlier tcgen05 operations
-            mma_commit(smem_u32(&B.drain));
-            if (!wait_bar(smem_u32(&B.drain), 0, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+            mma_commit_if(smem_u32(&B.drain), leader);
+            if (!spin_warp_drain(smem_u32(&B.drain), 0, abort_flag) && lane == 0) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
         }
         __syncwarp();
     } else {
