@@ -85,23 +85,29 @@ latent_absorb_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = B.tmem_base;
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
         constexpr uint32_t id = idesc_bf16(kM, kN, 1);
+        const uint32_t leader = elect_one();
+        const uint64_t ad0 = desc_sw128(smem_u32(sA), 16, 1024), bd0 = desc_sw128(smem_u32(sB), kBBox, 1024);
 #pragma unroll
         for (int k = 0; k < kKB; ++k) {
-            if (!spin_bar(smem_u32(&B.full[k]), 0, abort_flag, false)) {
-                if (a.err) set_error(a.err, ERR_TIMEOUT | SITE_FULL_WAIT);
-                *abort_flag = 1;
+            if (!spin_warp_drain(smem_u32(&B.full[k]), 0, abort_flag)) {
+                if (lane == 0) {
+                    if (a.err) set_error(a.err, ERR_TIMEOUT | SITE_FULL_WAIT);
+                    *abort_flag = 1;
+                }
+                __syncwarp();
                 break;
             }
             tc_fence_after();
-            const uint64_t ad = desc_sw128(smem_u32(sA + k * kABox), 16, 1024);
-            const uint64_t bd = desc_sw128(smem_u32(sB + k * kBBytes), kBBox, 1024);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)     // 16 k: 32 bytes of A's rows, 16 rows of B's boxes
-                mma_f16(tmem, ad + (uint64_t)((j * 32) >> 4), bd + (uint64_t)((j * 2048) >> 4), id, (k | j) != 0 ? 1u : 0u);
+            for (int j = 0; j < 4; ++j) {   // 16 k: 32 bytes of A's rows, 16 rows of B's boxes
+                const uint64_t ad = ad0 + (uint64_t)((k * kABox + j * 32) >> 4), bd = bd0 + (uint64_t)((k * kBBytes + j * 2048) >> 4);
+                if (k + j == 0) mma_f16_if<0>(tmem, ad, bd, id, leader);
+                else mma_f16_if<1>(tmem, ad, bd, id, leader);
+            }
         }
-        mma_commit(smem_u32(&B.done));
+        mma_commit_if(smem_u32(&B.done), leader);
     }
     __syncwarp();
     const int row = m0 + 32 * warp + lane;

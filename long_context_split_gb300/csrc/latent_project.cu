@@ -145,6 +145,7 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
         return S.lse[t] == -INFINITY ? 0.f : expf(l - S.lse[t]);
     };
     const int group = threadIdx.x >> 6;
+    const uint32_t leader = elect_one();
     for (int half = 0; half < 2; ++half) {
         // ---- merge of the half's columns ----
         const int col4 = 64 * half + (threadIdx.x & 63), to4 = threadIdx.x & 63;
@@ -225,27 +226,29 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
         __syncthreads();
         tc_fence_after();
         // ---- D[v][token] of the half, box by box of 64 columns (rows past n are not written back) ----
-        if (threadIdx.x == 0) {
+        if (warp == 0) {
             constexpr uint32_t id = idesc_bf16(kLatV, kTok, 0);
-            if (!spin_bar(smem_u32(&S.w_full[half]), 0, abort_flag, false)) {
-                if (a.err) set_error(a.err, ERR_TIMEOUT | SITE_FULL_WAIT);
-                *abort_flag = 1;
+            if (!spin_warp_drain(smem_u32(&S.w_full[half]), 0, abort_flag)) {
+                if (lane == 0) {
+                    if (a.err) set_error(a.err, ERR_TIMEOUT | SITE_FULL_WAIT);
+                    *abort_flag = 1;
+                }
             } else {
                 tc_fence_after();
-#pragma unroll 1
-                for (int j = 0; j < kBoxes / 2; ++j) {
-                    const uint64_t wd = desc_sw128(smem_u32(sW + (half * (kBoxes / 2) + j) * kWBox), 16, 1024);
+                const uint64_t wd0 = desc_sw128(smem_u32(sW + half * (kBoxes / 2) * kWBox), 16, 1024);
+                const uint64_t hd0 = desc_sw128(smem_u32(sHi), 16, 1024), ld0 = desc_sw128(smem_u32(sLo), 16, 1024);
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        const uint64_t od = desc_sw128(smem_u32((part ? sLo : sHi) + j * kOBox), 16, 1024);
+                for (int j = 0; j < kBoxes / 2; ++j)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_f16(tmem, wd + (uint64_t)((k * 32) >> 4), od + (uint64_t)((k * 32) >> 4), id,
-                                    (half | part | j | k) ? 1u : 0u);
+                    for (int k = 0; k < 4; ++k) {
+                        const uint64_t wd = wd0 + (uint64_t)((j * kWBox + k * 32) >> 4), step = (uint64_t)((j * kOBox + k * 32) >> 4);
+                        if (j + k == 0 && half == 0) mma_f16_if<0>(tmem, wd, hd0 + step, id, leader);
+                        else mma_f16_if<1>(tmem, wd, hd0 + step, id, leader);
+                        mma_f16_if<1>(tmem, wd, ld0 + step, id, leader);
                     }
-                }
             }
-            mma_commit(smem_u32(&S.done[half]));
+            __syncwarp();
+            mma_commit_if(smem_u32(&S.done[half]), leader);
         }
         __syncwarp();
     }

@@ -450,8 +450,13 @@ splitkv_status splitkv_latent_project(const splitkv_problem* prob, const splitkv
 
 int32_t splitkv_latent_prefers_expanded(const splitkv_problem* prob) {
     if (check_latent_problem(prob)) return -1;
-    // operations per head: see splitkv_latent_layer; the absorbed kernel computes its scores in both
-    // halves of the output columns and its probabilities as a high part and a residual
+    // Without the tcgen05 MLA kernel (128 heads, 64-token pages) the absorbed form attends on the
+    // CUDA cores: 16 heads, one token after 4,096 took 699 us against 60, 64 tokens 3957 against 58.
+    if (!mla_tc_supports(1, 1, prob->num_q_heads, prob->head_dim_qk, prob->head_dim_v, prob->page_size)) return 1;
+    // Operations per head: see splitkv_latent_layer; the absorbed kernel computes its scores in both
+    // halves of the output columns and its probabilities as a high part and a residual.  The two meet
+    // at 71 tokens per request after a long history (128 heads, 2 x 32,768 tokens, absorbed against
+    // expanded: 32 tokens 960 us, 2266; 64 tokens 1896, 2185; 128 tokens 3358, 2135).
     double tokens = 0, pairs = 0;
     for (int b = 0; b < prob->batch; ++b) {
         const double n = prob->seq_lens_host[b], t = prob->qo_indptr_host[b + 1] - prob->qo_indptr_host[b];

@@ -287,6 +287,17 @@ def test_problems_that_are_not_latent_attention_are_refused():
         skv.latent_prefers_expanded(gqa)
 
 
+def test_the_preferred_form_follows_lengths_and_shape():
+    def prefers(seq, new, heads, page=64):
+        c = Case(seq, new, heads, page, dev="cpu")
+        return skv.latent_prefers_expanded(_problem(c))
+
+    assert not prefers([900], [1], 128) and not prefers([900] * 3, [16, 1, 32], 128)
+    assert prefers([300], [300], 128) and prefers([900], [200], 128)
+    # where the absorbed form would attend on the CUDA cores
+    assert prefers([900], [1], 16) and prefers([90], [1], 128, page=16)
+
+
 def test_layers_are_checked():
     c = Case([20], [3], 2, dev="cpu")
     p = _problem(c)
