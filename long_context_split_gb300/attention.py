@@ -127,6 +127,8 @@ class LatentAttention:
         if out is None:
             out = torch.empty(p.total_q, p.num_q_heads, 128, dtype=torch.bfloat16, device=p.k_cache.device)
         layer = _lib.latent_layer(p, q, self.w_kv_b, out, lse)
+        if p.total_q == 0:
+            return out
         if self.form == "expanded":
             _lib.latent_expanded(p, self.plan, layer, self.workspace, self.error_word, stream)
         else:

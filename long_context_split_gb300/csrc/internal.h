@@ -2,6 +2,7 @@
 // libsplitkv.  Not part of the C ABI.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -169,6 +170,10 @@ splitkv_status fail_with(splitkv_status s, const char* fmt, ...) __attribute__((
 
 // SMs of the current device (0: none visible).
 int sm_count();
+
+// Allows `kernel` `bytes` of dynamic shared memory on the current device; `done` is the kernel's own
+// record of the devices where that has been done.
+cudaError_t allow_smem(const void* kernel, size_t bytes, std::atomic<uint64_t>& done);
 
 // Host-side checks of a problem's shape and lengths (no pointers).
 splitkv_status check_problem_lengths(const splitkv_problem* prob);

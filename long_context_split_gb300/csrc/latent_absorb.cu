@@ -161,12 +161,8 @@ cudaError_t launch_latent_absorb(const LatentArgs& a, void* q_abs, cudaStream_t 
     cudaError_t e;
     if ((e = make_map(&mq, a.q, (long long)a.heads * kLatQ, a.total_q, a.q_stride, kM)) != cudaSuccess) return e;
     if ((e = make_map(&mw, a.w, kLatC, (long long)a.heads * kLatW, kLatC, 64)) != cudaSuccess) return e;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&]() {
-        attr_err = cudaFuncSetAttribute(latent_absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static std::atomic<uint64_t> allowed{0};
+    if ((e = allow_smem((const void*)latent_absorb_kernel, kSmemBytes, allowed)) != cudaSuccess) return e;
     const long long ctas = (long long)((a.total_q + kM - 1) / kM) * a.heads * 2;
     {
         ProfileScope ps(SPLITKV_KERNEL_LATENT_ABSORB, s);

@@ -647,12 +647,8 @@ cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s) {
     cudaError_t e;
     if ((e = make_map(&mq, a.q, (long long)a.heads * kLatQ, a.total_q, a.q_stride, kRows)) != cudaSuccess) return e;
     if ((e = make_map(&mr, a.rows, kLatRow, rows, kLatRow, kKeys)) != cudaSuccess) return e;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&]() {
-        attr_err = cudaFuncSetAttribute(latent_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static std::atomic<uint64_t> allowed{0};
+    if ((e = allow_smem((const void*)latent_attention_kernel, kSmemBytes, allowed)) != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     {

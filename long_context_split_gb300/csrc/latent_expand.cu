@@ -401,12 +401,8 @@ cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s) {
     cudaError_t e;
     if ((e = make_map(&ma, a.rows, kLatRow, rows, kM)) != cudaSuccess) return e;
     if ((e = make_map(&mb, a.w, kLatC, (long long)a.heads * kLatW, kN / kCluster)) != cudaSuccess) return e;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&]() {
-        attr_err = cudaFuncSetAttribute(latent_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static std::atomic<uint64_t> allowed{0};
+    if ((e = allow_smem((const void*)latent_expand_kernel, kSmemBytes, allowed)) != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int tiles = (a.num_blocks + kCluster - 1) / kCluster * a.heads * 2;

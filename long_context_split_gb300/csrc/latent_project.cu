@@ -291,14 +291,10 @@ cudaError_t launch_latent_project(const LatentArgs& a, const void* o_part, int p
     if (enc(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(a.w), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&]() {
-        attr_err = cudaFuncSetAttribute(latent_project_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        if (attr_err == cudaSuccess)
-            attr_err = cudaFuncSetAttribute(latent_project_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static std::atomic<uint64_t> allowed[2];
+    const void* kernel = part_bf16 ? (const void*)latent_project_kernel<true> : (const void*)latent_project_kernel<false>;
+    cudaError_t e = allow_smem(kernel, kSmemBytes, allowed[part_bf16 ? 1 : 0]);
+    if (e != cudaSuccess) return e;
     const int ctas = a.heads * ((a.total_q + kTok - 1) / kTok);
     ProfileScope ps(SPLITKV_KERNEL_LATENT_PROJECT, s);
     if (part_bf16) latent_project_kernel<true><<<ctas, kThreads, kSmemBytes, s>>>(mw, a, o_part, lse_part, indptr);

@@ -359,6 +359,30 @@ def test_append_then_gather_on_another_stream():
     assert same(vo, decode(encode(v, "e4m3", V_SCALE), "e4m3", V_SCALE, "bf16"))
 
 
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    # an E4M3 pool of 4.3 GB (8 heads, 64 x 128 pages): the request's pages lie at its two ends
+    heads, page, dim = 8, 64, 128
+    pages = 2 ** 32 // (heads * page * dim) + 600
+    pool = torch.zeros(pages, heads, page, dim, dtype=torch.uint8, device="cuda")
+    table = torch.tensor([[pages - 1, 0, pages - 2]], dtype=torch.int32, device="cuda")
+    T = 150
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    prob = skv.AttentionProblem(
+        q=torch.empty(T, heads, dim, dtype=torch.bfloat16, device="cuda"), k_cache=pool, v_cache=pool.clone(), page_table=table,
+        seq_lens=i32([T]), qo_indptr=i32([0, T]), num_q_heads=heads, num_kv_heads=heads, head_dim_qk=dim, head_dim_v=dim,
+        page_size=page, scale=0.1, k_scale=K_SCALE, v_scale=V_SCALE)
+    k, v = (torch.randn(T, heads, dim).bfloat16() for _ in range(2))
+    skv.kv_append(prob, k.cuda(), v.cuda())
+    want = encode(k[:64], "e4m3", K_SCALE).transpose(0, 1)
+    assert same_codes(pool[pages - 1], want)
+    ko, vo = torch.empty(T, heads, dim, dtype=torch.bfloat16, device="cuda"), torch.empty(T, heads, dim, dtype=torch.bfloat16, device="cuda")
+    skv.kv_gather(prob, i32([0, T]), ko, vo)
+    torch.cuda.synchronize()
+    assert same(ko, decode(encode(k, "e4m3", K_SCALE), "e4m3", K_SCALE, "bf16"))
+    assert same(vo, decode(encode(v, "e4m3", V_SCALE), "e4m3", V_SCALE, "bf16"))
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 def _cpu(**kw):
     return Batch([20, 20], [2, 1], dev="cpu", **kw)

@@ -157,7 +157,7 @@ def test_expanded_many_heads_and_tasks():
 @pytest.mark.parametrize("fp8", [False, True])
 def test_absorbed(heads, fp8):
     seq, new = ([200, 64, 1, 777], [1, 3, 1, 2]) if heads == 128 else ([200, 64, 1], [1, 3, 1])
-    c = Case(seq, new, heads, 64, fp8, seed=7, stale=0.0)
+    c = Case(seq, new, heads, 64, fp8, seed=7)
     _, out, lse = c.run("absorbed")
     c.check("absorbed", out, lse)
 
@@ -165,7 +165,7 @@ def test_absorbed(heads, fp8):
 @pytest.mark.gpu
 @pytest.mark.parametrize("seq,new", [([3000], [1]), ([3000, 100], [2, 1]), ([700] * 9, [1] * 9), ([300] * 20, [2] * 20)])
 def test_absorbed_merges_many_splits(seq, new):
-    c = Case(seq, new, 128, seed=17, stale=0.0)
+    c = Case(seq, new, 128, seed=17)
     for params in (skv.plan_params("uniform", uniform_splits=37), skv.plan_params("uniform", uniform_splits=3, partial_dtype=skv.BF16)):
         att, out, lse = c.run("absorbed", params=params)
         assert att.plan.splits()[0] in (37, 3)
@@ -180,7 +180,7 @@ def test_absorbed_merges_many_splits(seq, new):
 @pytest.mark.gpu
 def test_absorbed_single_token_and_more_tokens_than_a_tile():
     for seq, new in (([500], [1]), ([65] * 67, [2] * 67)):
-        c = Case(seq, new, 128 if len(seq) == 1 else 8, seed=8, stale=0.0)
+        c = Case(seq, new, 128 if len(seq) == 1 else 8, seed=8)
         _, out, _ = c.run("absorbed", lse=False)
         c.check("absorbed", out)
 
@@ -188,7 +188,7 @@ def test_absorbed_single_token_and_more_tokens_than_a_tile():
 @pytest.mark.gpu
 @pytest.mark.parametrize("form", ["expanded", "absorbed"])
 def test_queries_sliced_from_a_wider_projection(form):
-    c = Case([90, 30], [5, 2], 4, seed=9, stale=0.0)
+    c = Case([90, 30], [5, 2], 4, seed=9)
     wide = torch.full((7, 4 * 192 + 64), float("nan"), dtype=torch.bfloat16)
     wide[:, :768] = c.q.view(7, 768)
     q = wide.cuda()[:, :768].view(7, 4, 192)
@@ -199,7 +199,7 @@ def test_queries_sliced_from_a_wider_projection(form):
 
 @pytest.mark.gpu
 def test_auto_takes_the_form_that_the_lengths_make_cheaper():
-    prompt, decode = Case([900], [900], 128, seed=10), Case([900], [1], 128, seed=10, stale=0.0)
+    prompt, decode = Case([900], [900], 128, seed=10), Case([900], [1], 128, seed=10)
     for c, form in ((prompt, "expanded"), (decode, "absorbed")):
         att, out, _ = c.run("auto", lse=False)
         assert att.form == form
@@ -210,7 +210,7 @@ def test_auto_takes_the_form_that_the_lengths_make_cheaper():
 @pytest.mark.gpu
 @pytest.mark.parametrize("form", ["expanded", "absorbed"])
 def test_replays_from_a_graph(form):
-    c = Case([300, 70], [40, 1], 128, seed=11, stale=0.0)
+    c = Case([300, 70], [40, 1], 128, seed=11)
     att, out, lse = c.run(form)
     q = c.q.cuda()
     stream = torch.cuda.Stream()
@@ -226,6 +226,42 @@ def test_replays_from_a_graph(form):
         torch.cuda.synchronize()
     att.check_device_error()
     c.check(form, out, lse, q=q2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["expanded", "absorbed"])
+def test_waits_that_run_out_are_reported(form):
+    # the loads are withheld (a host-side hook): every wait ends by its limit, the error word tells,
+    # and the same object works again after its plan is uploaded
+    c = Case([300], [20], 128, seed=14)
+    att, out, lse = c.run(form)
+    q = c.q.cuda()
+    skv.debug_set_inject(1)
+    try:
+        att(q, out=out, lse=lse)
+        st, raw = skv.read_device_error(att.error_word, clear=True)
+    finally:
+        skv.debug_set_inject(0)
+    assert st == skv.ERR_TIMEOUT and raw != 0
+    if form == "expanded":
+        skv.latent_upload(att.plan, att.workspace)
+    else:
+        skv.splitkv_plan_upload(att.plan, att.workspace)
+    out.fill_(float("nan"))
+    att(q, out=out, lse=lse)
+    torch.cuda.synchronize()
+    att.check_device_error()
+    c.check(form, out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", ["expanded", "absorbed"])
+def test_a_batch_without_query_rows(form):
+    c = Case([30, 7], [0, 0], 128, seed=15)
+    att = skv.LatentAttention(form=form, **c.kw)
+    assert att(c.q.cuda()).shape == (0, 128, 128)
+    torch.cuda.synchronize()
+    att.check_device_error()
 
 
 @pytest.mark.gpu

@@ -203,6 +203,25 @@ def test_replays_from_a_graph_with_new_numbers():
         np.testing.assert_array_equal(lens.cpu().numpy(), want[2])
 
 
+@pytest.mark.gpu
+def test_rows_past_32_bit_offsets():
+    vocab, rows = 120001, 18000                      # 2.2e9 probabilities (8.6 GB)
+    p = torch.zeros(rows, vocab, device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    p[rows - 3, 7] = 1.0                             # the draft after this row is accepted
+    p[rows - 2, 100] = 0.5                           # and refused after this one: the draw
+    p[rows - 2, 120000] = 0.5
+    tokens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    tokens[rows - 2], tokens[rows - 1] = 7, 5
+    qo = i32([0, 1, rows - 3, rows])
+    u = torch.zeros(rows, device="cuda")
+    out, acc = skv.verify_drafts(tokens, qo, p, None, u, torch.tensor([0.0, 0.0, 0.75], device="cuda"))
+    torch.cuda.synchronize()
+    assert acc.tolist() == [0, 0, 1]
+    assert out[rows - 3:].tolist() == [7, 120000, -1]
+    assert out[0] == -1                              # a row without weight
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 def _host():
     i = lambda n: torch.zeros(n, dtype=torch.int32)  # noqa: E731
