@@ -175,13 +175,14 @@ KERNEL_SOURCES = {
     "chunk_tc_kernel": ["long_context_split_gb300/csrc/chunk_kernel.cu", "long_context_split_gb300/csrc/tc_common.cuh",
                         "long_context_split_gb300/csrc/internal.h"],
     "mla_partial_kernel": ["long_context_split_gb300/csrc/mla_kernel.cu", "long_context_split_gb300/csrc/tc_common.cuh",
-                           "long_context_split_gb300/csrc/internal.h"],
+                           "long_context_split_gb300/csrc/tc_issue.cuh", "long_context_split_gb300/csrc/internal.h"],
     "generic_partial_kernel": ["long_context_split_gb300/csrc/generic_kernel.cu", "long_context_split_gb300/csrc/internal.h"],
     "merge_states_kernel": ["long_context_split_gb300/csrc/merge_kernel.cu", "long_context_split_gb300/csrc/internal.h"],
     "pair_tc_kernel": ["long_context_split_gb300/csrc/pair_kernel.cu", "long_context_split_gb300/csrc/tc_common.cuh",
                        "long_context_split_gb300/csrc/internal.h"],
     "mla_latent_convert_kernel": ["long_context_split_gb300/csrc/mla_kernel.cu",
                                   "long_context_split_gb300/csrc/tc_common.cuh",
+                                  "long_context_split_gb300/csrc/tc_issue.cuh",
                                   "long_context_split_gb300/csrc/internal.h"],
     "chunk_value_convert_kernel": ["long_context_split_gb300/csrc/chunk_kernel.cu",
                                    "long_context_split_gb300/csrc/tc_common.cuh",

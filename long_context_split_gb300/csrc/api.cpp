@@ -19,6 +19,7 @@
 #include "splitkv.h"
 #include "calibration.h"
 #include "internal.h"
+#include "operators.h"
 #include "planner.h"
 
 using namespace skv;

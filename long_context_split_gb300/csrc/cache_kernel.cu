@@ -20,7 +20,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "internal.h"
+#include "operators.h"
 
 namespace skv {
 namespace {

@@ -6,7 +6,7 @@
 
 #include <cuda_runtime.h>
 
-#include "internal.h"
+#include "operators.h"
 
 namespace skv {
 

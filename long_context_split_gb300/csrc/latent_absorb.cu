@@ -13,7 +13,7 @@
 #include <algorithm>
 
 #include "latent.h"
-#include "tc_common.cuh"
+#include "tc_issue.cuh"
 
 namespace skv {
 namespace {
@@ -121,17 +121,19 @@ latent_absorb_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             uint32_t v[32];
             SKV_LD32(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
             tc_wait_ld();
-            if (row >= a.total_q) continue;
+            if (row < a.total_q) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-                uint32_t w[4];
+                for (int k = 0; k < 32; k += 8) {
+                    uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1]));
-                    w[e] = *reinterpret_cast<const uint32_t*>(&p);
+                    for (int e = 0; e < 4; ++e) {
+                        const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[k + 2 * e]), __uint_as_float(v[k + 2 * e + 1]));
+                        w[e] = *reinterpret_cast<const uint32_t*>(&p);
+                    }
+                    *(uint4*)(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                *(uint4*)(out + c + k) = make_uint4(w[0], w[1], w[2], w[3]);
             }
+            __syncwarp();   // (the tensor-memory loads are warp-collective)
         }
     }
     tc_fence_before();

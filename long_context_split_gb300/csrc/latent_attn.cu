@@ -37,7 +37,7 @@
 #include <algorithm>
 
 #include "latent.h"
-#include "tc_common.cuh"
+#include "tc_issue.cuh"
 
 #define SKV_LD8(taddr, r)                                                                                            \
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"                            \
@@ -571,31 +571,33 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     SKV_LD32(lane_addr + c, o);
                     tc_wait_ld();
                 }
-                if (!valid) continue;
-                if (nu == 0 || empty_row) {
+                if (valid) {
+                    if (nu == 0 || empty_row) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = 0u;
-                }
-                if (direct) {
-                    uint4* op = (uint4*)((__nv_bfloat16*)a.out + orow * kLatV + c);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const __nv_bfloat162 p2 = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]) * inv,
-                                                                            __uint_as_float(o[j + 2 * e + 1]) * inv);
-                            w[e] = *reinterpret_cast<const uint32_t*>(&p2);
-                        }
-                        op[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int j = 0; j < 32; ++j) o[j] = 0u;
                     }
-                } else {
+                    if (direct) {
+                        uint4* op = (uint4*)((__nv_bfloat16*)a.out + orow * kLatV + c);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *(float4*)(a.o_part + st * kLatV + c + j) =
-                            make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
-                                        __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                        for (int j = 0; j < 32; j += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const __nv_bfloat162 p2 = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]) * inv,
+                                                                                __uint_as_float(o[j + 2 * e + 1]) * inv);
+                                w[e] = *reinterpret_cast<const uint32_t*>(&p2);
+                            }
+                            op[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *(float4*)(a.o_part + st * kLatV + c + j) =
+                                make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
+                                            __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                    }
                 }
+                __syncwarp();   // (the tensor-memory loads are warp-collective)
             }
             if (valid) {
                 if (!direct) a.lse_part[st] = lse;

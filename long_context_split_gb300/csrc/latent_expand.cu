@@ -27,7 +27,7 @@
 #include <algorithm>
 
 #include "latent.h"
-#include "tc_common.cuh"
+#include "tc_issue.cuh"
 
 namespace skv {
 namespace {

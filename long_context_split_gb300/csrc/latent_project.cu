@@ -20,7 +20,7 @@
 // residual (two products with the same weights, 16 significant bits): rounding it to
 // one bf16 would cost as much as the result's own rounding.
 #include "latent.h"
-#include "tc_common.cuh"
+#include "tc_issue.cuh"
 
 namespace skv {
 namespace {

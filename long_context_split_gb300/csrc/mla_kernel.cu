@@ -41,7 +41,7 @@
 // Every wait is bounded (%globaltimer); on expiry the CTA records the error
 // word and drains its own copies and MMAs before leaving.
 #include "splitkv.h"
-#include "tc_common.cuh"
+#include "tc_issue.cuh"
 #include "partial_io.cuh"
 #include "trace.cuh"
 

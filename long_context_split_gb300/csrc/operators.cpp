@@ -13,8 +13,8 @@
 #include <cuda_runtime.h>
 
 #include "splitkv.h"
-#include "internal.h"
 #include "latent.h"
+#include "operators.h"
 
 using namespace skv;
 

@@ -21,7 +21,7 @@
 // The order of every sum is fixed.
 #include <algorithm>
 
-#include "internal.h"
+#include "operators.h"
 
 namespace skv {
 namespace {
