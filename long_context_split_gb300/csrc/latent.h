@@ -17,14 +17,13 @@ constexpr int kLatC = 512;                         // latent columns
 constexpr int kLatRow = kLatC + kLatRope;          // cache row
 constexpr int kLatV = 128;                         // value columns of a head
 constexpr int kLatW = kLatNope + kLatV;            // weight rows of a head (key rows, then value rows)
-constexpr int kLatPad = 128;                       // each request's rows are padded to this many
 
 // The expanded keys (bf16) and values (f16) of 64 cached tokens and one head, in the order of the
 // shared-memory operands of their products, so that a warp of the expansion stores whole lines (32
 // tokens x 32 bytes) and the attention copies 16 KB at a time: eight groups of 16 columns, a
 // group 64 rows (tokens) of 32 bytes in the 32-byte swizzle (the two 16-byte halves of a row change
 // places where bit 2 of the row is set); the keys' groups, then the values'.
-constexpr int kLatUnit = 64;
+constexpr int kLatUnit = 64;                       // (each request's rows are padded to whole units)
 constexpr int kLatGroup = kLatUnit * 32;           // one 16-column group: 2 KB
 constexpr int kLatSide = 8 * kLatGroup;            // keys (or values) of a unit: 16 KB
 constexpr int kLatImage = 2 * kLatSide;
@@ -46,14 +45,14 @@ struct LatentTask {
     int32_t head;
     int32_t row_begin;
     int32_t row_end;
-    int32_t key_begin;      // a multiple of 128
+    int32_t key_begin;      // a multiple of 64
     int32_t key_end;
     int32_t split;
     int32_t pad;
 };
 static_assert(sizeof(LatentTask) == 32, "LatentTask layout");
 
-// 128 rows of the copies: request, first token.
+// 64 rows of the copies: request, first token.
 struct LatentBlock {
     int32_t b;
     int32_t token;
@@ -80,7 +79,7 @@ struct LatentArgs {
     int32_t total_q;
     int32_t heads;
     int32_t num_tasks;
-    int32_t num_blocks;        // padded rows / 128
+    int32_t num_blocks;        // padded rows / 64
     int32_t page_size;
     int32_t num_pages;
     int32_t max_pages;

@@ -296,7 +296,6 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
     tc_fence_after();
     const uint32_t tmem = B.tmem_base;
     volatile int* abort_flag = &B.abort_flag;
-    const int units = a.num_blocks * (kLatPad / kKeys);
     auto give_up = [&](int site) {
         if (!*abort_flag) {
             set_error(a.err, ERR_TIMEOUT | site);
@@ -324,19 +323,20 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 if (id < 0) break;
                 const Task t = read_task(a, id);
                 if (t.n_units == 0) continue;
-                // both tiles' queries (rows past the request are other tokens, or the zero fill past
+                // the tiles' queries (rows past the request are other tokens, or the zero fill past
                 // the tensor; they are never written back)
                 if (!spin_bar(smem_u32(&B.q_empty), (qn & 1) ^ 1, abort_flag, true)) {
                     give_up(SITE_EMPTY_WAIT);
                     break;
                 }
-                mbar_expect_tx(smem_u32(&B.q_full), kQBytes);
-                for (int x = 0; x < kTiles; ++x)
+                const int tiles = t.rows[1] > 0 ? kTiles : 1;
+                mbar_expect_tx(smem_u32(&B.q_full), tiles * kQTile);
+                for (int x = 0; x < tiles; ++x)
                     for (int j = 0; j < kQBoxes; ++j)
                         tma_2d(smem_u32(sQ + x * kQTile + j * kQBox), &tmap_q, t.head * kLatQ + 64 * j,
                                t.r.q_start + t.row0 + x * kRows, smem_u32(&B.q_full));
                 ++qn;
-                auto image = [&](int head, int y) { return (const char*)a.kv + ((size_t)head * units + y / kKeys) * kLatImage; };
+                auto image = [&](int head, int y) { return (const char*)a.kv + ((size_t)head * a.num_blocks + y / kKeys) * kLatImage; };
                 // Keys two units ahead of values, the order in which the tiles release them: P V of unit
                 // u - 3 (the values' slot) is issued before S of unit u - 1 (the keys' slot of u + 2)
                 auto load_keys = [&](int u) -> bool {
@@ -644,7 +644,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, long long cols, long long
 
 cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s) {
     if (a.num_tasks <= 0) return cudaSuccess;
-    const long long rows = (long long)a.num_blocks * kLatPad;
+    const long long rows = (long long)a.num_blocks * kLatUnit;
     CUtensorMap mq, mr;
     cudaError_t e;
     if ((e = make_map(&mq, a.q, (long long)a.heads * kLatQ, a.total_q, a.q_stride, kRows)) != cudaSuccess) return e;

@@ -7,10 +7,10 @@
 // 57 % of the tensor rate (218 us for 7.3k tokens and 128 heads).  So a CTA keeps its 128
 // latent rows while it walks over heads, as the A operand in tensor memory (256 columns),
 // and a cluster of two CTAs (two row tiles, the same heads) shares every 64-column box of
-// weights: each loads half of its 128 rows and multicasts it to both.  That leaves 192 KB of shared
-// memory for a ring of twelve boxes: with the rows in shared memory and three boxes the
-// stores' traffic delayed the copies by more than the ring covered (215 us; 150 without the
-// stores; 166 us now).
+// weights: each loads half of its 128 rows and multicasts it to both (128 KB a CTA and head from
+// L2).  The weights' ring holds a whole tile, so that the issuing warp's code is straight-line
+// with constant slots: with one lane's loop over twelve slots, issue alone took 660 cycles a box
+// for 256 of products (262 us; 198 unrolled, 166 issued from the warp in step).
 //
 // Roles: warp 0 TMA producer, warp 1 MMA thread (M = 128 rows, N = 128: a head's keys or
 // its values, K = 512 in eight boxes; two accumulators), warps 2..5 the epilogue, which
@@ -41,11 +41,12 @@ constexpr int kN = 128;                            // weight rows of a tile: W_u
 constexpr int kABox = kM * 128;                    // 128 latent rows x 64 columns
 constexpr int kBBox = kN * 128;                    // 128 weight rows x 64 columns
 constexpr int NS = kBoxes;                         // weight boxes in shared memory: a tile's, so that slots are constants
+constexpr int kStages = 4;                         // row boxes in flight on their way to tensor memory
 constexpr int kColA = 0, kColAcc = 256;            // tensor memory: the rows (256 columns), two accumulators
 constexpr int kTmem = 512;
 
 struct Bars {
-    unsigned long long as_full[2], as_empty[2];    // staging of the rows on their way to tensor memory
+    unsigned long long as_full[kStages], as_empty[kStages];   // staging of the rows on their way to tensor memory
     unsigned long long a_ready;
     unsigned long long b_full[NS], b_empty[NS];
     unsigned long long acc_full[2], acc_empty[2];
@@ -54,7 +55,7 @@ struct Bars {
     int abort_flag;
 };
 
-constexpr size_t kSmemBytes = 1024 + 2 * (size_t)kABox + (size_t)NS * kBBox + sizeof(Bars);
+constexpr size_t kSmemBytes = 1024 + kStages * (size_t)kABox + (size_t)NS * kBBox + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 __device__ __forceinline__ uint32_t cluster_ctarank() {
@@ -114,15 +115,17 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                      int num_tiles) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sA = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    unsigned char* sB = sA + 2 * kABox;
+    unsigned char* sB = sA + kStages * kABox;
     Bars& B = *(Bars*)(sB + NS * kBBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank(), cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster;
     const int t0 = (int)((long long)cluster * num_tiles / clusters), t1 = (int)((long long)(cluster + 1) * num_tiles / clusters);
     if (threadIdx.x == 0) {
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < kStages; ++k) {
             mbar_init(smem_u32(&B.as_full[k]), 1);
             mbar_init(smem_u32(&B.as_empty[k]), kEpiWarps);
+        }
+        for (int k = 0; k < 2; ++k) {
             mbar_init(smem_u32(&B.acc_full[k]), 1);
             mbar_init(smem_u32(&B.acc_empty[k]), kEpiWarps);
         }
@@ -165,10 +168,11 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                     // (an odd last row tile: its partner's rows are the zero fill past the tensor)
                     pair = x.pair;
                     for (int j = 0; j < kBoxes && ok; ++j, ++an) {
-                        ok = spin_bar(smem_u32(&B.as_empty[an & 1]), ((an >> 1) & 1) ^ 1, abort_flag, true);
+                        ok = spin_bar(smem_u32(&B.as_empty[an % kStages]), ((an / kStages) & 1) ^ 1, abort_flag, true);
                         if (!ok) break;
-                        mbar_expect_tx(smem_u32(&B.as_full[an & 1]), kABox);
-                        tma_2d(smem_u32(sA + (an & 1) * kABox), &ma, 64 * j, (pair * kCluster + rank) * kM, smem_u32(&B.as_full[an & 1]));
+                        mbar_expect_tx(smem_u32(&B.as_full[an % kStages]), kABox);
+                        tma_2d(smem_u32(sA + an % kStages * kABox), &ma, 64 * j, (pair * kCluster + rank) * kM,
+                               smem_u32(&B.as_full[an % kStages]));
                     }
                 }
                 const int y = x.head * kLatW + x.side * kN + rank * (kN / kCluster);
@@ -187,9 +191,9 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                 const uint32_t last = it - 1 - k;
                 landed = spin_bar(smem_u32(&B.b_full[last % NS]), (last / NS) & 1, abort_flag, false) && landed;
             }
-            for (uint32_t k = 0; k < 2 && k < an; ++k) {
+            for (uint32_t k = 0; k < (uint32_t)kStages && k < an; ++k) {
                 const uint32_t last = an - 1 - k;
-                landed = spin_bar(smem_u32(&B.as_full[last & 1]), (last >> 1) & 1, abort_flag, false) && landed;
+                landed = spin_bar(smem_u32(&B.as_full[last % kStages]), (last / kStages) & 1, abort_flag, false) && landed;
             }
             if (!landed) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
         }
@@ -237,7 +241,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         // ===================== rows into tensor memory; epilogue: a thread per row =====================
         const int quad = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-        const int units = a.num_blocks * (kLatPad / kLatUnit);
+        const int units = a.num_blocks;
         float vmax = 0.f;
         uint32_t n = 0, an = 0;
         int pair = -1;
@@ -249,9 +253,9 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                 // every product of the previous rows is done: this warp has seen its last tile's end
                 pair = x.pair;
                 for (int j = 0; j < kBoxes && ok; ++j, ++an) {
-                    ok = spin_warp(smem_u32(&B.as_full[an & 1]), (an >> 1) & 1, abort_flag);
+                    ok = spin_warp(smem_u32(&B.as_full[an % kStages]), (an / kStages) & 1, abort_flag);
                     if (!ok) break;
-                    const unsigned char* src = sA + (an & 1) * kABox + (32 * quad + lane) * 128;
+                    const unsigned char* src = sA + an % kStages * kABox + (32 * quad + lane) * 128;
                     uint32_t v[32];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -263,7 +267,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                     }
                     SKV_ST32(lanes + kColA + 32 * j, v);
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&B.as_empty[an & 1]));
+                    if (lane == 0) mbar_arrive(smem_u32(&B.as_empty[an % kStages]));
                 }
                 if (!ok) { give_up(SITE_FULL_WAIT); break; }
                 tc_wait_st();
@@ -325,7 +329,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
 }
 
 // The batch's latent rows as bf16, request after request, each padded with zero rows to a
-// multiple of 128: E4M3 codes are exact in bf16 (their scale is folded into the softmax and the
+// multiple of 64: E4M3 codes are exact in bf16 (their scale is folded into the softmax and the
 // output), and a row past a request's last token is zero whatever its page holds.
 template <bool FP8>
 __global__ void __launch_bounds__(256) latent_rows_kernel(LatentArgs a) {
@@ -333,9 +337,9 @@ __global__ void __launch_bounds__(256) latent_rows_kernel(LatentArgs a) {
     constexpr int kPieces = kLatRow / 8;                  // 16-byte pieces of a copied row
     __shared__ long long src_row[kRowsPerCta];
     const int row0 = blockIdx.x * kRowsPerCta;
-    const LatentBlock blk = a.blocks[row0 / kLatPad];
+    const LatentBlock blk = a.blocks[row0 / kLatUnit];
     if (threadIdx.x < kRowsPerCta) {
-        const int tok = blk.token + (row0 + threadIdx.x) % kLatPad;
+        const int tok = blk.token + (row0 + threadIdx.x) % kLatUnit;
         long long w = -1;
         if (tok < a.reqs[blk.b].seq_len) {
             const int page = a.page_table[(size_t)blk.b * a.max_pages + tok / a.page_size];
@@ -387,7 +391,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, long long cols, long long
 
 cudaError_t launch_latent_rows(const LatentArgs& a, cudaStream_t s) {
     if (a.num_blocks <= 0) return cudaSuccess;
-    const int ctas = a.num_blocks * (kLatPad / 16);
+    const int ctas = a.num_blocks * (kLatUnit / 16);
     ProfileScope ps(SPLITKV_KERNEL_LATENT_ROWS, s);
     if (a.kv_fp8) latent_rows_kernel<true><<<ctas, 256, 0, s>>>(a);
     else latent_rows_kernel<false><<<ctas, 256, 0, s>>>(a);
@@ -396,7 +400,7 @@ cudaError_t launch_latent_rows(const LatentArgs& a, cudaStream_t s) {
 
 cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s) {
     if (a.num_blocks <= 0) return cudaSuccess;
-    const long long rows = (long long)a.num_blocks * kLatPad;
+    const long long rows = (long long)a.num_blocks * kLatUnit;
     CUtensorMap ma, mb;
     cudaError_t e;
     if ((e = make_map(&ma, a.rows, kLatRow, rows, kM)) != cudaSuccess) return e;
@@ -405,7 +409,7 @@ cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s) {
     if ((e = allow_smem((const void*)latent_expand_kernel, kSmemBytes, allowed)) != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const int tiles = (a.num_blocks + kCluster - 1) / kCluster * a.heads * 2;
+    const int tiles = (int)((rows + kCluster * kM - 1) / (kCluster * kM)) * a.heads * 2;
     {
         ProfileScope ps(SPLITKV_KERNEL_LATENT_EXPAND, s);
         latent_expand_kernel<<<kCluster * std::max(1, std::min(sms / kCluster, tiles)), kThreads, kSmemBytes, s>>>(ma, mb, a, tiles);

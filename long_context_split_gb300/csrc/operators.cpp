@@ -238,9 +238,9 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
         if (unsplit > 0 && unsplit < sms)
             r.n_splits = (int32_t)std::max<long long>(1, std::min<long long>((sms + unsplit - 1) / unsplit, r.seq_len / 1024));
         if (r.q_len == 0) continue;          // nothing to attend: its rows are not copied
-        const int blocks = (r.seq_len + kLatPad - 1) / kLatPad;
-        for (int k = 0; k < blocks; ++k) pl->blocks.push_back(LatentBlock{b, k * kLatPad});
-        rows += (long long)blocks * kLatPad;
+        const int blocks = (r.seq_len + kLatUnit - 1) / kLatUnit;
+        for (int k = 0; k < blocks; ++k) pl->blocks.push_back(LatentBlock{b, k * kLatUnit});
+        rows += (long long)blocks * kLatUnit;
         if (rows * H >= (1LL << 31)) return fail_with(SPLITKV_ERR_UNSUPPORTED, "num_q_heads * cached tokens exceeds 2^31");
     }
     // The tasks of a (request, head, split) read the same keys and values: together, longest first,
@@ -250,7 +250,7 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
     std::stable_sort(order.begin(), order.end(), [&](int x, int y) { return pl->reqs[x].seq_len > pl->reqs[y].seq_len; });
     for (int b : order) {
         const LatentReq& r = pl->reqs[b];
-        const int nblk = (r.seq_len + kLatPad - 1) / kLatPad, per = nblk / r.n_splits, extra = nblk % r.n_splits;
+        const int nblk = (r.seq_len + kLatUnit - 1) / kLatUnit, per = nblk / r.n_splits, extra = nblk % r.n_splits;
         for (int h = 0; h < H; ++h)
             for (int s = 0; s < r.n_splits; ++s) {
                 const int first = s * per + std::min(s, extra), count = per + (s < extra ? 1 : 0);
@@ -261,8 +261,8 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
                     t.head = h;
                     t.row_begin = row;
                     t.row_end = std::min(r.q_len, row + kTaskRows);
-                    t.key_begin = std::min(first * kLatPad, r.seq_len);
-                    t.key_end = std::min((first + count) * kLatPad, r.seq_len);
+                    t.key_begin = std::min(first * kLatUnit, r.seq_len);
+                    t.key_end = std::min((first + count) * kLatUnit, r.seq_len);
                     t.split = s;
                     pl->tasks.push_back(t);
                 }
