@@ -64,23 +64,6 @@ latent_absorb_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (half == 0) {
-        // the rotary columns pass through: 128 bytes of each token, eight loads in flight per lane
-        const int y = m0 + 32 * warp;
-        uint4 v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = y + 4 * k + (lane >> 3);
-            if (r < a.total_q)
-                v[k] = *((const uint4*)((const __nv_bfloat16*)a.q + (size_t)r * a.q_stride + head * kLatQ + kLatNope) + (lane & 7));
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int r = y + 4 * k + (lane >> 3);
-            if (r < a.total_q)
-                *((uint4*)((__nv_bfloat16*)q_abs + ((size_t)r * a.heads + head) * kLatRow + kLatC) + (lane & 7)) = v[k];
-        }
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -108,6 +91,24 @@ latent_absorb_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             }
         }
         mma_commit_if(smem_u32(&B.done), leader);
+    }
+    if (half == 0) {
+        // under the product, the rotary columns pass through: 128 bytes of each token, eight loads in
+        // flight per lane
+        const int y = m0 + 32 * warp;
+        uint4 v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = y + 4 * k + (lane >> 3);
+            if (r < a.total_q)
+                v[k] = *((const uint4*)((const __nv_bfloat16*)a.q + (size_t)r * a.q_stride + head * kLatQ + kLatNope) + (lane & 7));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int r = y + 4 * k + (lane >> 3);
+            if (r < a.total_q)
+                *((uint4*)((__nv_bfloat16*)q_abs + ((size_t)r * a.heads + head) * kLatRow + kLatC) + (lane & 7)) = v[k];
+        }
     }
     __syncwarp();
     const int row = m0 + 32 * warp + lane;
