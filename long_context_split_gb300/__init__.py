@@ -3,7 +3,10 @@
 The compute path is ``libsplitkv.so`` (hand-written sm_103a CUDA kernels
 behind the C ABI of ``include/splitkv.h``); this package is its thin Python
 binding.  Names follow the C ABI: ``splitkv_plan``, ``splitkv_partial``,
-``merge_states``, ``splitkv_decode``.
+``merge_states``, ``splitkv_decode``; and around the attention call,
+``kv_append`` and ``kv_gather`` (rows into and out of a paged cache),
+``LatentAttention`` (latent attention from the model's own queries) and
+``verify_drafts`` (acceptance of drafted tokens).
 """
 from ._lib import (  # noqa: F401
     BF16, ERR_CUDA, ERR_DEVICE_CHECK, ERR_INVALID_ARG, ERR_TIMEOUT, ERR_UNSUPPORTED, ERR_WORKSPACE, F32,
