@@ -56,7 +56,9 @@ __device__ __forceinline__ float4 load_state(const void* o_part, int state, int 
     return *((const float4*)((const float*)o_part + (size_t)state * kLatC) + col4);
 }
 
+// (a state of weight zero contributes nothing, whatever it holds)
 __device__ __forceinline__ void fma4(float4& s, float w, const float4& v) {
+    if (w == 0.f) return;
     s.x = fmaf(w, v.x, s.x);
     s.y = fmaf(w, v.y, s.y);
     s.z = fmaf(w, v.z, s.z);
@@ -125,10 +127,10 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
         for (int s = sub + 64; s < cnt; s += 16) sum += expf(lse_part[s0 + s] - base);
 #pragma unroll
         for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        const float lse = m == -INFINITY ? -INFINITY : m + logf(sum);
+        const float lse = sum == 0.f ? -INFINITY : m + logf(sum);   // (a NaN among the states makes the sum NaN)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            if (sub + 16 * k < cnt) S.weight[t][sub + 16 * k] = m == -INFINITY ? 0.f : expf(own[k] - lse);
+            if (sub + 16 * k < cnt) S.weight[t][sub + 16 * k] = sum == 0.f ? 0.f : expf(own[k] - lse);
         if (on && sub == 0) {
             S.lse[t] = lse;
             S.first[t] = s0;

@@ -296,6 +296,51 @@ def test_nan_in_a_visible_row_is_not_hidden():
     assert torch.isnan(out.float()).any(-1)[50:, 0].all()
 
 
+@pytest.mark.gpu
+def test_expanded_rows_that_see_nothing_of_a_later_split():
+    c = Case([4096, 1100], [4000, 5], 2, seed=18)
+    att, out, lse = c.run("expanded")
+    assert att.plan.splits()[0] >= 3             # rows up to 1000 see the first split only
+    c.check("expanded", out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows", [3, 40])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_projection_of_states_without_weight(rows, dtype):
+    """States of lse -inf contribute nothing, whatever they hold, a row of none but those is 0 with
+    lse -inf, and a NaN log-sum-exp is not hidden: rows r of 3 states, by r % 3."""
+    c = Case([rows], [rows], 2, seed=19)
+    p, R = _problem(c, k_cache=c.cache, q=torch.zeros(rows, 2, 576, dtype=torch.bfloat16, device="cuda"),
+                    page_table=c.kw["page_table"]), rows * 2
+    g = torch.Generator().manual_seed(1)
+    states = torch.randn(R, 3, 512, generator=g).to(dtype)
+    lse = torch.randn(R, 3, generator=g)
+    kind = torch.arange(R) // 2 % 3              # 0: one empty state, 1: all empty, 2: a NaN lse
+    lse[kind == 0, 1] = -math.inf
+    lse[kind == 1] = -math.inf
+    lse[kind == 2, 0] = float("nan")
+    lse[kind == 2, 1:] = -math.inf
+    states[lse == -math.inf] = float("nan")
+    out = torch.full((rows, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse_out = torch.zeros(rows, 2, device="cuda")
+    layer = skv.latent_layer(p, c.q.cuda(), c.kw["w_kv_b"], out, lse_out)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    skv.latent_project(p, layer, states.view(-1, 512).cuda(), lse.view(-1).cuda(),
+                       torch.arange(0, 3 * R + 1, 3, dtype=torch.int32, device="cuda"), err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    kind, got = kind.view(rows, 2), out.cpu().double()
+    assert (got[kind == 1] == 0).all() and (lse_out.cpu()[kind == 1] == -math.inf).all()
+    assert torch.isnan(got[kind == 2]).all() and torch.isnan(lse_out.cpu()[kind == 2]).all()
+    # the others: the merge in float32 (three terms), the merged output as a bf16 pair (2^-15), one bf16 rounding
+    w = torch.softmax(lse.double(), 1).view(rows, 2, 3)
+    o = torch.einsum("rhs,rhsc->rhc", w, torch.nan_to_num(states.double(), nan=0.0).view(rows, 2, 3, 512))
+    ref = torch.einsum("rhc,hvc->rhv", o, c.w.double()[:, 128:])
+    tol = torch.einsum("rhc,hvc->rhv", o.abs(), c.w.double()[:, 128:].abs()) * 2.0 ** -13 + 2.0 ** -8 * ref.abs()
+    assert ((got - ref).abs() <= tol)[kind == 0].all()
+
+
 # ------------------------------------------------------------------ refusals (no GPU needed)
 def _status(call):
     with pytest.raises(skv.SplitKVError) as e:
