@@ -499,9 +499,10 @@ splitkv_status splitkv_latent_upload(const splitkv_latent_plan_t *plan, void *wo
 
 /*
  * splitkv_latent_expanded -- out[token][head] of the expanded form; row i of a
- * request sees keys 0 .. seq_len - q_len + i.  prob->q is not read.  Keys are
- * rounded to bf16, values and probabilities to f16, scores, sums and outputs
- * are float32 until the one rounding of the result.  A finite expanded value
+ * request sees keys 0 .. seq_len - q_len + i.  prob->q is not read, and the
+ * lengths are the plan's.  Keys are rounded to bf16, values and probabilities
+ * to f16; scores, sums and outputs are float32 until the one rounding of the
+ * result.  A finite expanded value
  * beyond the f16 range reports DEVICE_CHECK.  Cache slots past a request's
  * last token do not reach the result, whatever they hold.  Calls on the same
  * workspace must be stream-ordered.
@@ -570,8 +571,8 @@ typedef struct {
  * draft, if all are accepted, from p_r: the lowest token whose cumulative
  * weight exceeds sample_u[b] times the row's total.  Tokens without weight are
  * never drawn; a row without any gives -1.  Weights that are NaN or negative count as
- * 0.  out_tokens row r of request b: the accepted drafts, then the drawn token,
- * then -1.  seq_lens_out[b] = seq_lens[b] - (q_len - 1) + accepted[b].  A
+ * 0; probabilities must otherwise be finite.  out_tokens row r of request b: the
+ * accepted drafts, then the drawn token, then -1.  seq_lens_out[b] = seq_lens[b] - (q_len - 1) + accepted[b].  A
  * request without rows gets accepted 0 and keeps its length.
  *  dev_error_word: device int32 or NULL.  A draft outside [0, vocab) is refused
  *    and reports DEVICE_CHECK, and so does a qo_indptr entry outside total_q.

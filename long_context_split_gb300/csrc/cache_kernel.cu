@@ -298,7 +298,7 @@ cudaError_t launch_vec(const CacheRowsArgs& a, cudaStream_t s) {
     // tokens per block: about 8 blocks per SM (as many as fit), so that a block waits for its chain of
     // dependent reads once for many tokens; few rows get a block per `by` tokens
     const int per = std::min(kMaxTokens, std::max(by, a.rows / (8 * sms)));
-    const int blocks = (a.rows + per - 1) / per;
+    const int blocks = (int)(((long long)a.rows + per - 1) / per);
     ProfileScope ps(APPEND ? SPLITKV_KERNEL_KV_APPEND : SPLITKV_KERNEL_KV_GATHER, s);
     cache_rows_kernel<Rows, Cache, VEC, APPEND><<<blocks, dim3(bx, by), 0, s>>>(a, per);
     return cudaGetLastError();

@@ -10,8 +10,8 @@
 // What bounds it: the tensor pipe (2 * 320 operations per visible pair and head).  S with
 // N = 64 keys reads both operands from shared memory at that memory's rate, 48 cycles a
 // k-step for 32 of arithmetic, so a unit of 64 keys takes 832 cycles per 128-row tile
-// instead of 640 (the products alone, softmax left out: 680 us where the whole takes 812,
-// 1 k + 2 k tokens after 14 k + 19 k at 32 heads).  The keys and values of a
+// instead of 640 (1 k + 2 k tokens after 14 k + 19 k at 32 heads: 692 us, 1.50
+// PFLOP/s; the products alone, softmax left out, 681).  The keys and values of a
 // (request, head) are read by all of its query tiles, which run together, so they come
 // from L2.
 //
@@ -23,7 +23,8 @@
 // per token) take the row maximum, keep a running maximum and sum (base 2; O is rescaled
 // only when a maximum grows by more than 2^8, so P stays below 2^8), and write P over S as
 // f16.  Two threads per token (eight warps a tile, maxima exchanged through shared
-// memory) measured slower, 944 us against 849 on two 3.6k-token prompts.
+// memory) measured slower on two 3.6k-token prompts (944 us against 849, before the
+// products were issued from a warp in step: 755 now).
 // P and V are f16 because their product takes one type and f16's 11 significant
 // bits keep both roundings below the output's own; Q and K stay bf16, as given.
 // Sums, maxima and O are float32.  Products run in issue order, so S of unit u + 2

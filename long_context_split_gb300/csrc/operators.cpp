@@ -7,7 +7,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <new>
 #include <vector>
 
 #include <cuda_runtime.h>
@@ -337,7 +336,7 @@ splitkv_status splitkv_latent_plan(const splitkv_problem* prob, splitkv_latent_p
             delete pl;
             return s;
         }
-    } catch (const std::bad_alloc&) {
+    } catch (...) {   // (no exception leaves a C entry)
         delete pl;
         return fail_with(SPLITKV_ERR_INVALID_ARG, "no host memory for the plan");
     }
