@@ -502,10 +502,11 @@ splitkv_status splitkv_latent_upload(const splitkv_latent_plan_t *plan, void *wo
  * request sees keys 0 .. seq_len - q_len + i.  prob->q is not read, and the
  * lengths are the plan's.  Keys are rounded to bf16, values and probabilities
  * to f16; scores, sums and outputs are float32 until the one rounding of the
- * result.  A finite expanded value
- * beyond the f16 range reports DEVICE_CHECK.  Cache slots past a request's
- * last token do not reach the result, whatever they hold.  Calls on the same
- * workspace must be stream-ordered.
+ * result.  A finite expanded value beyond the f16 range reports DEVICE_CHECK.
+ * Cache slots past a request's last token do not reach the result, whatever
+ * they hold; a token's own NaN or infinity may reach the rows before it, where
+ * the masked weight 0 meets it, as in the formula's matrix product.  Calls on
+ * the same workspace must be stream-ordered.
  */
 splitkv_status splitkv_latent_expanded(const splitkv_problem *prob, const splitkv_latent_plan_t *plan,
                                        const splitkv_latent_layer *layer, void *workspace, size_t ws_bytes,

@@ -553,12 +553,21 @@ def latent_expanded(problem: AttentionProblem, plan: LatentPlan, layer: LatentLa
 
 def latent_absorb_query(problem: AttentionProblem, layer: LatentLayer, q_abs: torch.Tensor,
                         dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    """splitkv_latent_absorb_query: q_abs [total_q, H, 576] bfloat16 from the layer's q."""
+    _check_array("q_abs", q_abs, problem.total_q * problem.num_q_heads * 576, torch.bfloat16)
     _check(load().splitkv_latent_absorb_query(ctypes.byref(problem._s), ctypes.byref(layer), _ptr(q_abs),
                                               _ptr(dev_error_word), _stream_handle(stream)))
 
 
 def latent_project(problem: AttentionProblem, layer: LatentLayer, o_part: torch.Tensor, lse_part: torch.Tensor,
                    state_indptr: torch.Tensor, dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    """splitkv_latent_project: merge o_part [num_states, 512] (float32 or bfloat16) and lse_part
+    [num_states] by state_indptr [total_q * H + 1] int32 and project the rows to the layer's out."""
+    if o_part.dtype not in _DTYPES:
+        raise TypeError(f"unsupported o_part dtype {o_part.dtype}")
+    _check_array("o_part", o_part, o_part.shape[0] * 512, o_part.dtype)
+    _check_array("lse_part", lse_part, o_part.shape[0], torch.float32)
+    _check_array("state_indptr", state_indptr, problem.total_q * problem.num_q_heads + 1, torch.int32)
     _check(load().splitkv_latent_project(ctypes.byref(problem._s), ctypes.byref(layer), _ptr(o_part), _DTYPES[o_part.dtype],
                                          _ptr(lse_part), _ptr(state_indptr), _ptr(dev_error_word), _stream_handle(stream)))
 

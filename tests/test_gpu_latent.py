@@ -400,6 +400,20 @@ def test_layers_are_checked():
     assert _status(lambda: skv.latent_project(p, layer, states, lse, ind)) == skv.ERR_INVALID_ARG
 
 
+def test_the_ends_of_the_absorbed_form_check_their_buffers():
+    c = Case([20], [3], 2, dev="cpu")
+    p = _problem(c)
+    layer = skv.latent_layer(p, c.q, c.w, torch.zeros(3, 2, 128, dtype=torch.bfloat16))
+    for q_abs in (torch.zeros(2, 2, 576, dtype=torch.bfloat16), torch.zeros(3, 2, 576), torch.zeros(3, 2, 1152, dtype=torch.bfloat16)[..., ::2]):
+        with pytest.raises(TypeError):
+            skv.latent_absorb_query(p, layer, q_abs)
+    o, lse, ind = torch.zeros(12, 512), torch.zeros(12), torch.arange(0, 14, 2, dtype=torch.int32)
+    for bad in ((o.double(), lse, ind), (o[:, :256], lse, ind), (o, lse[:11], ind), (o, lse.double(), ind), (o, lse, ind[:6]),
+                (o, lse, ind.long())):
+        with pytest.raises(TypeError):
+            skv.latent_project(p, layer, *bad)
+
+
 def test_the_expanded_call_checks_its_plan_and_workspace():
     c = Case([20, 30], [3, 2], 2, dev="cpu")
     p = _problem(c)
