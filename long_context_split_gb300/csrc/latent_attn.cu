@@ -69,11 +69,16 @@ constexpr int kQBytes = kTiles * kQTile;
 constexpr int kKBytes = kLatSide + kRBox;            // a unit's keys: 24 KB
 constexpr int kVBytes = kLatSide;                    // a unit's values: 16 KB
 constexpr int NS = 3;                                // slots of the key ring, and of the value ring
+// Loads arrive on two barriers per slot in turn.  A tile passes by units that it does not attend, and a parity
+// cannot tell "the unit before is loading" from "this one has landed": with one barrier per slot, a value load
+// passed by that took until the tile's next unit of that slot would have let it read the slot early.  With two,
+// the latest phase of the barrier that a tile waits on is over when it starts to wait.
+constexpr int NB = 2 * NS;
 
 struct Bars {
     unsigned long long task_full[kTR], task_empty[kTR];
     int task_slot[kTR];
-    unsigned long long k_full[NS], v_full[NS];
+    unsigned long long k_full[NB], v_full[NB];
     unsigned long long s_full[kTiles][NS];        // per tile and key slot: S of the slot's unit is done (for its
                                                   // softmax, and the tile's release of the keys)
     unsigned long long pv_done[kTiles][NS];       // per tile and value slot: P V of the slot's unit is done (the
@@ -220,7 +225,7 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
 // and the phase parities of the tiles' releases and of the slot's loads.
 struct SlotUse {
     uint32_t occ = 0, par = 0, next = 0;   // bit 8 x + s: tile x attends slot s; its release's parity; the next one's
-    uint32_t used = 0, loads = 0;          // bit s: the slot has been loaded; parity of its latest load
+    uint32_t used = 0, loads = 0;          // bit b: a load has used the barrier; parity of its latest one
 
     __device__ __forceinline__ bool wait_free(unsigned long long (&done)[kTiles][NS], int s, volatile int* abort_flag) {
         for (int x = 0; x < kTiles; ++x) {
@@ -229,7 +234,8 @@ struct SlotUse {
         }
         return true;
     }
-    __device__ __forceinline__ void use(int s, bool tile0, bool tile1) {
+    __device__ __forceinline__ void use(int b, bool tile0, bool tile1) {
+        const int s = b % NS;
         for (int x = 0; x < kTiles; ++x) {
             const uint32_t bit = 1u << (8 * x + s);
             if (x ? tile1 : tile0) {
@@ -240,13 +246,13 @@ struct SlotUse {
                 occ &= ~bit;
             }
         }
-        loads = (used >> s) & 1u ? loads ^ (1u << s) : loads;
-        used |= 1u << s;
+        loads = (used >> b) & 1u ? loads ^ (1u << b) : loads;
+        used |= 1u << b;
     }
-    __device__ __forceinline__ bool drain(unsigned long long (&full)[NS], volatile int* abort_flag) {
+    __device__ __forceinline__ bool drain(unsigned long long (&full)[NB], volatile int* abort_flag) {
         bool ok = true;
-        for (int s = 0; s < NS; ++s)
-            if ((used >> s) & 1u) ok = spin_bar(smem_u32(&full[s]), (loads >> s) & 1u, abort_flag, false) && ok;
+        for (int b = 0; b < NB; ++b)
+            if ((used >> b) & 1u) ok = spin_bar(smem_u32(&full[b]), (loads >> b) & 1u, abort_flag, false) && ok;
         return ok;
     }
 };
@@ -267,9 +273,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             mbar_init(smem_u32(&B.task_full[s]), 1);
             mbar_init(smem_u32(&B.task_empty[s]), kTaskConsumers);
         }
+        for (int b = 0; b < NB; ++b) {
+            mbar_init(smem_u32(&B.k_full[b]), 1);
+            mbar_init(smem_u32(&B.v_full[b]), 1);
+        }
         for (int s = 0; s < NS; ++s) {
-            mbar_init(smem_u32(&B.k_full[s]), 1);
-            mbar_init(smem_u32(&B.v_full[s]), 1);
             for (int x = 0; x < kTiles; ++x) {
                 mbar_init(smem_u32(&B.s_full[x][s]), 1);
                 mbar_init(smem_u32(&B.pv_done[x][s]), 1);
@@ -341,10 +349,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 // Keys two units ahead of values, the order in which the tiles release them: P V of unit
                 // u - 3 (the values' slot) is issued before S of unit u - 1 (the keys' slot of u + 2)
                 auto load_keys = [&](int u) -> bool {
-                    const int s = (int)((items + u) % NS);
+                    const int b = (int)((items + u) % NB), s = b % NS;
                     if (!ku.wait_free(B.s_full, s, abort_flag)) return false;
-                    ku.use(s, u < t.nu[0], u < t.nu[1]);
-                    const uint32_t full = smem_u32(&B.k_full[s]), to = smem_u32(sK + s * kKBytes);
+                    ku.use(b, u < t.nu[0], u < t.nu[1]);
+                    const uint32_t full = smem_u32(&B.k_full[b]), to = smem_u32(sK + s * kKBytes);
                     const int y = t.r.row_base + t.kb + u * kKeys;   // row of the copies
                     mbar_expect_tx(full, kKBytes);
                     bulk_copy(to, image(t.head, y), kLatSide, full);
@@ -352,10 +360,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     return true;
                 };
                 auto load_values = [&](int u) -> bool {
-                    const int s = (int)((items + u) % NS);
+                    const int b = (int)((items + u) % NB), s = b % NS;
                     if (!vu.wait_free(B.pv_done, s, abort_flag)) return false;
-                    vu.use(s, u < t.nu[0], u < t.nu[1]);
-                    const uint32_t full = smem_u32(&B.v_full[s]), to = smem_u32(sV + s * kVBytes);
+                    vu.use(b, u < t.nu[0], u < t.nu[1]);
+                    const uint32_t full = smem_u32(&B.v_full[b]), to = smem_u32(sV + s * kVBytes);
                     mbar_expect_tx(full, kVBytes);
                     bulk_copy(to, image(t.head, t.r.row_base + t.kb + u * kKeys) + kLatSide, kLatSide, full);
                     return true;
@@ -388,11 +396,12 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
         uint32_t qn = 0;
         uint32_t pc = 0;      // units this tile attended so far
         uint32_t tn = 0;      // tasks this tile finished
-        // ring positions of the next S and of the next P V: slot and the parity of its loads
-        uint32_t s_slot = 0, s_par = 0, v_slot = 0, v_par = 0;
-        auto advance = [](uint32_t& slot, uint32_t& par) {
-            if (++slot == NS) {
-                slot = 0;
+        // ring positions of the next S and of the next P V: barrier and parity of its loads
+        uint32_t s_at = 0, s_par = 0, v_at = 0, v_par = 0;
+        auto slot_of = [](uint32_t at) { return at < NS ? at : at - NS; };
+        auto advance = [](uint32_t& at, uint32_t& par) {
+            if (++at == NB) {
+                at = 0;
                 par ^= 1;
             }
         };
@@ -410,9 +419,9 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             if (nu == 0 && lane == 0) mbar_arrive(smem_u32(&B.q_empty));   // nothing to attend: release the queries
             tc_fence_after();
             auto issue_s = [&](uint32_t n) -> bool {       // n: the tile's unit count, which picks the S buffer
-                if (!spin_warp(k_full + 8 * s_slot, s_par, abort_flag)) return false;
+                if (!spin_warp(k_full + 8 * s_at, s_par, abort_flag)) return false;
                 tc_fence_after();
-                const uint32_t scol = bufcol + kKeys * (n & 1);
+                const uint32_t scol = bufcol + kKeys * (n & 1), s_slot = slot_of(s_at);
                 const uint64_t kd = kd0 + (uint64_t)(s_slot * (kKBytes >> 4)), rd = rd0 + (uint64_t)(s_slot * (kKBytes >> 4));
 #pragma unroll
                 for (int kk = 0; kk < kLatQ / 16; ++kk) {
@@ -423,15 +432,15 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     else mma_f16_if<1>(scol, ad, bd, id_s, leader);
                 }
                 mma_commit_if(s_full + 8 * s_slot, leader);
-                advance(s_slot, s_par);
+                advance(s_at, s_par);
                 return true;
             };
             auto issue_pv = [&](uint32_t n, bool first) -> bool {
                 if (first && !spin_warp(smem_u32(&B.o_empty[x]), (tn & 1) ^ 1, abort_flag)) return false;
-                if (!spin_warp(v_full + 8 * v_slot, v_par, abort_flag)) return false;
+                if (!spin_warp(v_full + 8 * v_at, v_par, abort_flag)) return false;
                 if (!spin_warp(p_full + 8 * (n & 1), (n >> 1) & 1, abort_flag)) return false;
                 tc_fence_after();
-                const uint32_t pcol = bufcol + kKeys * (n & 1);
+                const uint32_t pcol = bufcol + kKeys * (n & 1), v_slot = slot_of(v_at);
                 const uint64_t vd = vd0 + (uint64_t)(v_slot * (kVBytes >> 4));
                 if (first) mma_f16_ts_if<0>(ocol, pcol, vd, id_o, leader);
                 else mma_f16_ts_if<1>(ocol, pcol, vd, id_o, leader);
@@ -439,7 +448,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 for (int kk = 1; kk < 4; ++kk)     // 16 keys: 8 columns of P, 512 bytes of V
                     mma_f16_ts_if<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 512) >> 4), id_o, leader);
                 mma_commit_if(pv_done + 8 * v_slot, leader);
-                advance(v_slot, v_par);
+                advance(v_at, v_par);
                 return true;
             };
             if (nu > 0) {
@@ -454,8 +463,8 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             }
             // units that only the other tile attends pass by in the rings
             for (int u = nu; u < t.n_units; ++u) {
-                advance(s_slot, s_par);
-                advance(v_slot, v_par);
+                advance(s_at, s_par);
+                advance(v_at, v_par);
             }
         }
         // every product issued here completes before tensor memory is released
