@@ -185,11 +185,12 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                 }
                 if (!ok) give_up(SITE_EMPTY_WAIT);
             }
-            // no copy may still be landing when the CTA leaves
+            // no copy, and no commit of the partner's, may still be on its way here when the CTA leaves
             bool landed = true;
             for (uint32_t k = 0; k < (uint32_t)NS && k < it; ++k) {
                 const uint32_t last = it - 1 - k;
                 landed = spin_bar(smem_u32(&B.b_full[last % NS]), (last / NS) & 1, abort_flag, false) && landed;
+                landed = spin_bar(smem_u32(&B.b_empty[last % NS]), (last / NS) & 1, abort_flag, true) && landed;
             }
             for (uint32_t k = 0; k < (uint32_t)kStages && k < an; ++k) {
                 const uint32_t last = an - 1 - k;
@@ -325,7 +326,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
     __syncthreads();
     tc_fence_after();
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
-    cluster_sync();          // the partner's copies and commits into this CTA have arrived
+    cluster_sync();          // this CTA's copies and commits have arrived at the partner
 }
 
 // The batch's latent rows as bf16, request after request, each padded with zero rows to a
