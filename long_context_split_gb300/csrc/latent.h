@@ -39,7 +39,8 @@ struct LatentReq {
 };
 static_assert(sizeof(LatentReq) == 32, "LatentReq layout");
 
-// Up to 256 query tokens of one (request, head) over the keys [key_begin, key_end) of one split.
+// Up to 256 query tokens of one (request, head) over the keys [key_begin, key_end) of one split; with
+// heads == 2, all (up to 128) query tokens of two consecutive heads.
 struct LatentTask {
     int32_t b;
     int32_t head;
@@ -48,7 +49,7 @@ struct LatentTask {
     int32_t key_begin;      // a multiple of 64
     int32_t key_end;
     int32_t split;
-    int32_t pad;
+    int32_t heads;
 };
 static_assert(sizeof(LatentTask) == 32, "LatentTask layout");
 
@@ -87,6 +88,7 @@ struct LatentArgs {
     float scale_log2;          // scale * k_scale * log2 e
     float v_scale;             // k_scale: values are codes times it
     int32_t inject;
+    int32_t pairs;             // some tasks are of two heads
 };
 
 // bf16 (exact) copy of the batch's latent rows, padding rows zero

@@ -10,8 +10,8 @@
 // What bounds it: the tensor pipe (2 * 320 operations per visible pair and head).  S with
 // N = 64 keys reads both operands from shared memory at that memory's rate, 48 cycles a
 // k-step for 32 of arithmetic, so a unit of 64 keys takes 832 cycles per 128-row tile
-// instead of 640 (1 k + 2 k tokens after 14 k + 19 k at 32 heads: 692 us, 1.50
-// PFLOP/s; the products alone, softmax left out, 681).  The keys and values of a
+// instead of 640 (1 k + 2 k tokens after 14 k + 19 k at 32 heads: 680 us, 1.53
+// PFLOP/s; leaving the softmax out took 692 to 681 when it was tried).  The keys and values of a
 // (request, head) are read by all of its query tiles, which run together, so they come
 // from L2.
 //
@@ -29,6 +29,10 @@
 // bits keep both roundings below the output's own; Q and K stay bf16, as given.
 // Sums, maxima and O are float32.  Products run in issue order, so S of unit u + 2
 // replaces P of unit u only after P V of unit u has read it.
+//
+// A request of up to 128 new tokens fills one tile, and one tile's chain of product and softmax does not fill
+// the SM: where there are enough of them (the plan's rule), a task is two heads of such a request, a
+// tile per head, and the rings' units alternate between the two.
 //
 // Warp roles: warp 0 TMA producer and task claimer, warps 1 and 10 the tiles' MMA
 // threads, warps 2..5 and 6..9 their softmax and epilogue.  Waits are bounded; on
@@ -96,24 +100,27 @@ static_assert(kSmemBytes <= 232448, "shared memory budget");
 
 // what every role derives from a task
 struct Task {
-    int head, row0, split, kb, kend, n_units;
+    int head, row0, kb, kend;
+    int pair;             // 1: a tile per head; units alternate between the two
+    int n_units;          // units that pass through the rings
     int rows[kTiles];     // valid tokens of each tile
     int nu[kTiles];       // units each tile attends
     LatentReq r;
 };
 
+template <bool PAIRS>
 __device__ __forceinline__ Task read_task(const LatentArgs& a, int id) {
     Task t;
     const LatentTask d = a.tasks[id];
     t.r = a.reqs[d.b];
     t.head = d.head;
     t.row0 = d.row_begin;
-    t.split = d.split;
+    t.pair = PAIRS ? d.heads - 1 : 0;
     t.kb = t.kend = d.key_begin;
     t.n_units = 0;
 #pragma unroll
     for (int x = 0; x < kTiles; ++x) {
-        const int r0 = d.row_begin + x * kRows;
+        const int r0 = d.row_begin + (t.pair ? 0 : x * kRows);
         t.rows[x] = max(0, min(kRows, d.row_end - r0));
         t.nu[x] = 0;
         if (t.rows[x] > 0) {
@@ -126,6 +133,7 @@ __device__ __forceinline__ Task read_task(const LatentArgs& a, int id) {
             }
         }
     }
+    t.n_units <<= t.pair;
     return t;
 }
 
@@ -257,6 +265,8 @@ struct SlotUse {
     }
 };
 
+// PAIRS: some tasks are of two heads (without them, 1 to 3 % of the time of long prompts and histories)
+template <bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 1)
 latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_r,
                         LatentArgs a) {
@@ -330,7 +340,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 mbar_arrive(smem_u32(&B.task_full[slot]));
                 ++claimed;
                 if (id < 0) break;
-                const Task t = read_task(a, id);
+                const Task t = read_task<PAIRS>(a, id);
                 if (t.n_units == 0) continue;
                 // the tiles' queries (rows past the request are other tokens, or the zero fill past
                 // the tensor; they are never written back)
@@ -342,30 +352,37 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 mbar_expect_tx(smem_u32(&B.q_full), tiles * kQTile);
                 for (int x = 0; x < tiles; ++x)
                     for (int j = 0; j < kQBoxes; ++j)
-                        tma_2d(smem_u32(sQ + x * kQTile + j * kQBox), &tmap_q, t.head * kLatQ + 64 * j,
-                               t.r.q_start + t.row0 + x * kRows, smem_u32(&B.q_full));
+                        tma_2d(smem_u32(sQ + x * kQTile + j * kQBox), &tmap_q, (t.head + (t.pair ? x : 0)) * kLatQ + 64 * j,
+                               t.r.q_start + t.row0 + (t.pair ? 0 : x * kRows), smem_u32(&B.q_full));
                 ++qn;
-                auto image = [&](int head, int y) { return (const char*)a.kv + ((size_t)head * a.num_blocks + y / kKeys) * kLatImage; };
+                // unit u of the rings: its first row of the copies, its image
+                auto row_of = [&](int u) { return t.r.row_base + t.kb + (u >> t.pair) * kKeys; };
+                auto image = [&](int u) {
+                    return (const char*)a.kv + ((size_t)(t.head + (u & t.pair)) * a.num_blocks + row_of(u) / kKeys) * kLatImage;
+                };
+                auto use = [&](SlotUse& slots, int b, int u) {
+                    if (t.pair) slots.use(b, (u & 1) == 0, (u & 1) == 1);
+                    else slots.use(b, u < t.nu[0], u < t.nu[1]);
+                };
                 // Keys two units ahead of values, the order in which the tiles release them: P V of unit
                 // u - 3 (the values' slot) is issued before S of unit u - 1 (the keys' slot of u + 2)
                 auto load_keys = [&](int u) -> bool {
                     const int b = (int)((items + u) % NB), s = b % NS;
                     if (!ku.wait_free(B.s_full, s, abort_flag)) return false;
-                    ku.use(b, u < t.nu[0], u < t.nu[1]);
+                    use(ku, b, u);
                     const uint32_t full = smem_u32(&B.k_full[b]), to = smem_u32(sK + s * kKBytes);
-                    const int y = t.r.row_base + t.kb + u * kKeys;   // row of the copies
                     mbar_expect_tx(full, kKBytes);
-                    bulk_copy(to, image(t.head, y), kLatSide, full);
-                    tma_2d(to + kLatSide, &tmap_r, kLatC, y, full);
+                    bulk_copy(to, image(u), kLatSide, full);
+                    tma_2d(to + kLatSide, &tmap_r, kLatC, row_of(u), full);
                     return true;
                 };
                 auto load_values = [&](int u) -> bool {
                     const int b = (int)((items + u) % NB), s = b % NS;
                     if (!vu.wait_free(B.pv_done, s, abort_flag)) return false;
-                    vu.use(b, u < t.nu[0], u < t.nu[1]);
+                    use(vu, b, u);
                     const uint32_t full = smem_u32(&B.v_full[b]), to = smem_u32(sV + s * kVBytes);
                     mbar_expect_tx(full, kVBytes);
-                    bulk_copy(to, image(t.head, t.r.row_base + t.kb + u * kKeys) + kLatSide, kLatSide, full);
+                    bulk_copy(to, image(u) + kLatSide, kLatSide, full);
                     return true;
                 };
                 ok = load_keys(0) && (t.n_units < 2 || load_keys(1));
@@ -399,9 +416,10 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
         // ring positions of the next S and of the next P V: barrier and parity of its loads
         uint32_t s_at = 0, s_par = 0, v_at = 0, v_par = 0;
         auto slot_of = [](uint32_t at) { return at < NS ? at : at - NS; };
-        auto advance = [](uint32_t& at, uint32_t& par) {
-            if (++at == NB) {
-                at = 0;
+        auto advance = [](uint32_t& at, uint32_t& par, uint32_t step) {   // step < NB
+            at += step;
+            if (at >= NB) {
+                at -= NB;
                 par ^= 1;
             }
         };
@@ -411,13 +429,17 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             const int id = ring.next(B, abort_flag, lane, true);
             if (id == -2) { give_up(SITE_FULL_WAIT); break; }
             if (id < 0) break;
-            const Task t = read_task(a, id);
+            const Task t = read_task<PAIRS>(a, id);
             if (t.n_units == 0) continue;
             const int nu = x ? t.nu[1] : t.nu[0];
             if (!spin_warp(smem_u32(&B.q_full), qn & 1, abort_flag)) { give_up(SITE_FULL_WAIT); break; }
             ++qn;
             if (nu == 0 && lane == 0) mbar_arrive(smem_u32(&B.q_empty));   // nothing to attend: release the queries
             tc_fence_after();
+            // with two heads every second unit is this tile's: the first from the first, the second from the second
+            const uint32_t step = 1 + t.pair, own = t.pair & x;
+            advance(s_at, s_par, own);
+            advance(v_at, v_par, own);
             auto issue_s = [&](uint32_t n) -> bool {       // n: the tile's unit count, which picks the S buffer
                 if (!spin_warp(k_full + 8 * s_at, s_par, abort_flag)) return false;
                 tc_fence_after();
@@ -432,7 +454,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     else mma_f16_if<1>(scol, ad, bd, id_s, leader);
                 }
                 mma_commit_if(s_full + 8 * s_slot, leader);
-                advance(s_at, s_par);
+                advance(s_at, s_par, step);
                 return true;
             };
             auto issue_pv = [&](uint32_t n, bool first) -> bool {
@@ -448,7 +470,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 for (int kk = 1; kk < 4; ++kk)     // 16 keys: 8 columns of P, 512 bytes of V
                     mma_f16_ts_if<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 512) >> 4), id_o, leader);
                 mma_commit_if(pv_done + 8 * v_slot, leader);
-                advance(v_at, v_par);
+                advance(v_at, v_par, step);
                 return true;
             };
             if (nu > 0) {
@@ -461,10 +483,17 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 pc += nu;
                 ++tn;
             }
+            if (own) {
+                // with two heads, the second tile is one unit too far: the next task's first
+                s_par ^= s_at == 0;
+                v_par ^= v_at == 0;
+                s_at = (s_at + NB - 1) % NB;
+                v_at = (v_at + NB - 1) % NB;
+            }
             // units that only the other tile attends pass by in the rings
-            for (int u = nu; u < t.n_units; ++u) {
-                advance(s_at, s_par);
-                advance(v_at, v_par);
+            for (int u = nu; !t.pair && u < t.n_units; ++u) {
+                advance(s_at, s_par, 1);
+                advance(v_at, v_par, 1);
             }
         }
         // every product issued here completes before tensor memory is released
@@ -485,26 +514,27 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             const int id = ring.next(B, abort_flag, lane, true);
             if (id == -2) { give_up(SITE_FULL_WAIT); break; }
             if (id < 0) break;
-            int nu, kb, i, limit, n_units;
+            int nu, kb, i, limit, n_units, pair;
             bool valid;
             {
-                const Task t = read_task(a, id);
+                const Task t = read_task<PAIRS>(a, id);
                 const int trows = x ? t.rows[1] : t.rows[0];
                 nu = x ? t.nu[1] : t.nu[0];
                 kb = t.kb;
                 n_units = t.n_units;
+                pair = PAIRS ? t.pair : 0;
                 valid = row < trows;
-                i = t.row0 + x * kRows + (valid ? row : 0);        // token of the request
+                i = t.row0 + (pair ? 0 : x * kRows) + (valid ? row : 0);        // token of the request
                 // last key this token sees in the split
                 limit = valid ? min(t.kend - 1, t.r.seq_len - t.r.q_len + i) : -1;
                 if (trows == 0) nu = -1;
             }
-            const uint32_t item0 = item;
+            const uint32_t item0 = item + (pair & x);              // its units in the rings: with two heads every second one
             item += n_units;
             if (nu < 0) continue;                                  // no token of the task in this tile
             float m = -INFINITY, l = 0.f;
             for (int u = 0; u < nu; ++u) {
-                const int b2 = (int)(sn & 1), slot = (int)((item0 + u) % NS);
+                const int b2 = (int)(sn & 1), slot = (int)((item0 + (u << pair)) % NS);
                 if (!spin_warp(smem_u32(&B.s_full[x][slot]), (ph >> slot) & 1u, abort_flag)) { give_up(SITE_FULL_WAIT); ok = false; break; }
                 tc_fence_after();
                 uint32_t sr[64];
@@ -530,7 +560,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                     if (u >= 1) {
                         // P V of unit u - 1 has updated O once this tile released that unit's values; that
                         // barrier moves on only with this softmax's next P
-                        const int rs = (int)((item0 + u - 1) % NS);
+                        const int rs = (int)((item0 + ((u - 1) << pair)) % NS);
                         if (!spin_warp(smem_u32(&B.pv_done[x][rs]), ((ph >> rs) & 1u) ^ 1u, abort_flag)) {
                             give_up(SITE_EMPTY_WAIT);
                             ok = false;
@@ -572,8 +602,9 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             const float lse = empty_row ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             const LatentTask d = a.tasks[id];                      // (read again: few registers across the loop)
             const LatentReq r = a.reqs[d.b];
-            const size_t orow = (size_t)(r.q_start + i) * a.heads + d.head;
-            const size_t st = (size_t)r.state_base + ((size_t)i * a.heads + d.head) * r.n_splits + d.split;
+            const int head = d.head + (pair & x);
+            const size_t orow = (size_t)(r.q_start + i) * a.heads + head;
+            const size_t st = (size_t)r.state_base + ((size_t)i * a.heads + head) * r.n_splits + d.split;
             const bool direct = a.o_part == nullptr;
             for (int c = 0; c < kLatV; c += 32) {
                 uint32_t o[32];
@@ -659,14 +690,15 @@ cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s) {
     cudaError_t e;
     if ((e = make_map(&mq, a.q, (long long)a.heads * kLatQ, a.total_q, a.q_stride, kRows)) != cudaSuccess) return e;
     if ((e = make_map(&mr, a.rows, kLatRow, rows, kLatRow, kKeys)) != cudaSuccess) return e;
-    static std::atomic<uint64_t> allowed{0};
-    if ((e = allow_smem((const void*)latent_attention_kernel, kSmemBytes, allowed)) != cudaSuccess) return e;
+    static std::atomic<uint64_t> allowed[2];
+    const void* kernel = a.pairs ? (const void*)latent_attention_kernel<true> : (const void*)latent_attention_kernel<false>;
+    if ((e = allow_smem(kernel, kSmemBytes, allowed[a.pairs ? 1 : 0])) != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    {
-        ProfileScope ps(SPLITKV_KERNEL_LATENT_ATTENTION, s);
-        latent_attention_kernel<<<std::min(sms, a.num_tasks), kThreads, kSmemBytes, s>>>(mq, mr, a);
-    }
+    const int ctas = std::min(sms, a.num_tasks);
+    ProfileScope ps(SPLITKV_KERNEL_LATENT_ATTENTION, s);
+    if (a.pairs) latent_attention_kernel<true><<<ctas, kThreads, kSmemBytes, s>>>(mq, mr, a);
+    else latent_attention_kernel<false><<<ctas, kThreads, kSmemBytes, s>>>(mq, mr, a);
     return cudaGetLastError();
 }
 

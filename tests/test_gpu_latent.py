@@ -153,6 +153,19 @@ def test_expanded_many_heads_and_tasks():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("seq,new,heads,fp8", [
+    ([700, 64, 65, 300, 128, 1, 190], [128, 64, 1, 100, 128, 1, 127], 33, False),   # odd heads: a last task of one
+    ([500, 390, 129, 64], [300, 70, 129, 64], 64, True),                            # beside requests of two tiles
+    ([257] * 5, [3, 0, 128, 129, 17], 65, False),
+])
+def test_expanded_two_heads_per_task(seq, new, heads, fp8):
+    c = Case(seq, new, heads, 32, fp8, seed=len(seq))
+    att, out, lse = c.run("expanded")
+    assert att.plan.num_tasks == sum((-(-heads // 2) if n <= 128 else -(-n // 256) * heads) for n in new if n)
+    c.check("expanded", out, lse)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("heads", [128, 16, 1])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_absorbed(heads, fp8):
