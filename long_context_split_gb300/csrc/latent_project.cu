@@ -56,9 +56,7 @@ __device__ __forceinline__ float4 load_state(const void* o_part, int state, int 
     return *((const float4*)((const float*)o_part + (size_t)state * kLatC) + col4);
 }
 
-// (a state of weight zero contributes nothing, whatever it holds)
 __device__ __forceinline__ void fma4(float4& s, float w, const float4& v) {
-    if (w == 0.f) return;
     s.x = fmaf(w, v.x, s.x);
     s.y = fmaf(w, v.y, s.y);
     s.z = fmaf(w, v.z, s.z);
@@ -168,12 +166,9 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int x = s + k * per;
-                    w[k] = 0.f;
+                    w[k] = x < cnt ? weight(t, x) : 0.f;
                     v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (x < cnt) {
-                        v[k] = load_state<BF16>(o_part, S.first[t] + x, col4);
-                        w[k] = weight(t, x);
-                    }
+                    if (w[k] != 0.f) v[k] = load_state<BF16>(o_part, S.first[t] + x, col4);   // (an empty state may hold anything)
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) fma4(sum, w[k], v[k]);
@@ -204,12 +199,9 @@ latent_project_kernel(const __grid_constant__ CUtensorMap mw, LatentArgs a, cons
                         const int t = r0 + j * kGroups;
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            w[j][k] = 0.f;
+                            w[j][k] = t < n && s + k < S.count[t] ? weight(t, s + k) : 0.f;
                             v[j][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (t < n && s + k < S.count[t]) {
-                                v[j][k] = load_state<BF16>(o_part, S.first[t] + s + k, col4);
-                                w[j][k] = weight(t, s + k);
-                            }
+                            if (w[j][k] != 0.f) v[j][k] = load_state<BF16>(o_part, S.first[t] + s + k, col4);
                         }
                     }
 #pragma unroll
