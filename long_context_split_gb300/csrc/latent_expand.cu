@@ -6,11 +6,10 @@
 // operands of 128 x 256 tiles from L2 takes 384 KB a tile, and L2 gave 13 TB/s of it at
 // 57 % of the tensor rate (218 us for 7.3k tokens and 128 heads).  So a CTA keeps its 128
 // latent rows while it walks over heads, as the A operand in tensor memory (256 columns),
-// and a cluster of two CTAs (two row tiles, the same heads) shares every 64-column box of
-// weights: each loads half of its 128 rows and multicasts it to both (128 KB a CTA and head from
-// L2).  The weights' ring holds a whole tile, so that the issuing warp's code is straight-line
-// with constant slots: with one lane's loop over twelve slots, issue alone took 660 cycles a box
-// for 256 of products (262 us; 198 unrolled, 166 issued from the warp in step).
+// and loads the weights alone (256 KB a head from L2).  The weights' ring holds a whole tile, so
+// that the issuing warp's code is straight-line with constant slots: with one lane's loop over
+// twelve slots, issue alone took 660 cycles a box for 256 of products.  7.3k tokens and 128 heads
+// take 164 us, 1.5 PFLOP/s.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA thread (M = 128 rows, N = 128: a head's keys or
 // its values, K = 512 in eight boxes; two accumulators), warps 2..5 the epilogue, which
@@ -18,9 +17,7 @@
 // the next tile accumulates, and which brings a new row tile into tensor memory.  Values
 // get f16's three more bits: they meet the probabilities in an f16 product.
 //
-// A box may be overwritten once both CTAs' products have read it: each CTA's MMA
-// thread commits to both CTAs' barriers, and neither CTA leaves before the other.
-// Waits are bounded; on expiry a CTA records the error, and its partner's waits run out too.
+// Waits are bounded; on expiry the CTA records the error and drains its copies and products.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -35,7 +32,6 @@ namespace {
 constexpr int kM = 128;
 constexpr int kEpiWarps = 4;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-constexpr int kCluster = 2;
 constexpr int kBoxes = kLatC / 64;
 constexpr int kN = 128;                            // weight rows of a tile: W_uk's or W_uv's of a head
 constexpr int kABox = kM * 128;                    // 128 latent rows x 64 columns
@@ -58,33 +54,6 @@ struct Bars {
 constexpr size_t kSmemBytes = 1024 + kStages * (size_t)kABox + (size_t)NS * kBBox + sizeof(Bars);
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
-
-// to the same address in both CTAs of the cluster, each counting the bytes on its own barrier
-__device__ __forceinline__ void tma_2d_both(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, %3}], "
-        "[%4], %5;" ::"r"(dst),
-        "l"((uint64_t)map), "r"(x), "r"(y), "r"(bar), "h"((uint16_t)3)
-        : "memory");
-}
-
-__device__ __forceinline__ void commit_both_if(uint32_t bar, uint32_t cond) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t"
-        "@p tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"((uint16_t)3), "r"(cond)
-        : "memory");
-}
-
 // 16 packed columns, their 16-byte halves exchanged when `swap`
 __device__ __forceinline__ void store32(void* p, const uint32_t* w, int swap) {
     uint32_t x[8];
@@ -98,19 +67,19 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w, int swap) {
                  : "memory");
 }
 
-// Tiles (row pair, head, keys or values); cluster c takes [c n / clusters, (c + 1) n / clusters).
+// Tiles (128 rows, head, keys or values); CTA c takes [c n / ctas, (c + 1) n / ctas).
 struct Tile {
-    int pair, head, side;
+    int rows, head, side;
 };
 __device__ __forceinline__ Tile tile_of(int t, int heads) {
     Tile x;
-    x.pair = t / (2 * heads);
+    x.rows = t / (2 * heads);
     x.head = t % (2 * heads) / 2;
     x.side = t % 2;
     return x;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb, LatentArgs a,
                      int num_tiles) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -118,8 +87,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
     unsigned char* sB = sA + kStages * kABox;
     Bars& B = *(Bars*)(sB + NS * kBBox);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)cluster_ctarank(), cluster = blockIdx.x / kCluster, clusters = gridDim.x / kCluster;
-    const int t0 = (int)((long long)cluster * num_tiles / clusters), t1 = (int)((long long)(cluster + 1) * num_tiles / clusters);
+    const int t0 = (int)((long long)blockIdx.x * num_tiles / gridDim.x), t1 = (int)((blockIdx.x + 1LL) * num_tiles / gridDim.x);
     if (threadIdx.x == 0) {
         for (int k = 0; k < kStages; ++k) {
             mbar_init(smem_u32(&B.as_full[k]), 1);
@@ -132,7 +100,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         mbar_init(smem_u32(&B.a_ready), kEpiWarps);
         for (int s = 0; s < NS; ++s) {
             mbar_init(smem_u32(&B.b_full[s]), 1);
-            mbar_init(smem_u32(&B.b_empty[s]), kCluster);
+            mbar_init(smem_u32(&B.b_empty[s]), 1);
         }
         mbar_init(smem_u32(&B.drain), 1);
         B.abort_flag = 0;
@@ -145,7 +113,6 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync();          // both CTAs' barriers are initialised before either's copies or commits reach them
     tc_fence_after();
     const uint32_t tmem = B.tmem_base;
     volatile int* abort_flag = &B.abort_flag;
@@ -160,37 +127,35 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         // ===================== TMA producer (lane 0) =====================
         if (lane == 0) {
             uint32_t it = 0, an = 0;   // weight boxes, row boxes so far
-            int pair = -1;
+            int rows = -1;
             bool ok = a.inject != 1;   // (test hook: load nothing)
             for (int t = t0; t < t1 && ok; ++t) {
                 const Tile x = tile_of(t, a.heads);
-                if (x.pair != pair) {
-                    // (an odd last row tile: its partner's rows are the zero fill past the tensor)
-                    pair = x.pair;
+                if (x.rows != rows) {
+                    rows = x.rows;
                     for (int j = 0; j < kBoxes && ok; ++j, ++an) {
                         ok = spin_bar(smem_u32(&B.as_empty[an % kStages]), ((an / kStages) & 1) ^ 1, abort_flag, true);
                         if (!ok) break;
                         mbar_expect_tx(smem_u32(&B.as_full[an % kStages]), kABox);
-                        tma_2d(smem_u32(sA + an % kStages * kABox), &ma, 64 * j, (pair * kCluster + rank) * kM,
+                        tma_2d(smem_u32(sA + an % kStages * kABox), &ma, 64 * j, rows * kM,
                                smem_u32(&B.as_full[an % kStages]));
                     }
                 }
-                const int y = x.head * kLatW + x.side * kN + rank * (kN / kCluster);
+                const int y = x.head * kLatW + x.side * kN;
                 for (int j = 0; j < kBoxes && ok; ++j, ++it) {
                     const int s = (int)(it % NS);
                     ok = spin_bar(smem_u32(&B.b_empty[s]), ((it / NS) & 1) ^ 1, abort_flag, true);
                     if (!ok) break;
                     mbar_expect_tx(smem_u32(&B.b_full[s]), kBBox);
-                    tma_2d_both(smem_u32(sB + s * kBBox + rank * (kBBox / kCluster)), &mb, 64 * j, y, smem_u32(&B.b_full[s]));
+                    tma_2d(smem_u32(sB + s * kBBox), &mb, 64 * j, y, smem_u32(&B.b_full[s]));
                 }
                 if (!ok) give_up(SITE_EMPTY_WAIT);
             }
-            // no copy, and no commit of the partner's, may still be on its way here when the CTA leaves
+            // no copy may still be on its way when the CTA leaves
             bool landed = true;
             for (uint32_t k = 0; k < (uint32_t)NS && k < it; ++k) {
                 const uint32_t last = it - 1 - k;
                 landed = spin_bar(smem_u32(&B.b_full[last % NS]), (last / NS) & 1, abort_flag, false) && landed;
-                landed = spin_bar(smem_u32(&B.b_empty[last % NS]), (last / NS) & 1, abort_flag, true) && landed;
             }
             for (uint32_t k = 0; k < (uint32_t)kStages && k < an; ++k) {
                 const uint32_t last = an - 1 - k;
@@ -206,13 +171,13 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         const uint64_t bd0 = desc_sw128(smem_u32(sB), 16, 1024);
         const uint32_t full0 = smem_u32(&B.b_full[0]), empty0 = smem_u32(&B.b_empty[0]);
         uint32_t an = 0, n = 0;
-        int pair = -1;
+        int rows = -1;
         bool ok = true;
         for (int t = t0; t < t1 && ok; ++t, ++n) {
             const uint32_t buf = n & 1, acc = tmem + kColAcc + buf * kN;
             const Tile x = tile_of(t, a.heads);
-            if (x.pair != pair) {
-                pair = x.pair;
+            if (x.rows != rows) {
+                rows = x.rows;
                 if (!spin_warp(smem_u32(&B.a_ready), an & 1, abort_flag)) { give_up(SITE_FULL_WAIT); break; }
                 ++an;
             }
@@ -230,7 +195,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                     if (j + k == 0) mma_f16_ts_if<0>(acc, tmem + kColA, bd, id, leader);
                     else mma_f16_ts_if<1>(acc, tmem + kColA + 32 * j + 8 * k, bd, id, leader);
                 }
-                commit_both_if(empty0 + 8 * j, leader);
+                mma_commit_if(empty0 + 8 * j, leader);
             }
             if (!ok) { give_up(SITE_FULL_WAIT); break; }
             mma_commit_if(smem_u32(&B.acc_full[buf]), leader);
@@ -245,14 +210,14 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         const int units = a.num_blocks;
         float vmax = 0.f;
         uint32_t n = 0, an = 0;
-        int pair = -1;
+        int rows = -1;
         bool ok = true;
         for (int t = t0; t < t1 && ok; ++t, ++n) {
             const uint32_t buf = n & 1;
             const Tile x = tile_of(t, a.heads);
-            if (x.pair != pair) {
+            if (x.rows != rows) {
                 // every product of the previous rows is done: this warp has seen its last tile's end
-                pair = x.pair;
+                rows = x.rows;
                 for (int j = 0; j < kBoxes && ok; ++j, ++an) {
                     ok = spin_warp(smem_u32(&B.as_full[an % kStages]), (an / kStages) & 1, abort_flag);
                     if (!ok) break;
@@ -276,7 +241,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&B.a_ready));
             }
-            const int row = (x.pair * kCluster + rank) * kM + 32 * quad + lane;
+            const int row = x.rows * kM + 32 * quad + lane;
             const int unit = row / kLatUnit, r = row % kLatUnit, swap = (r >> 2) & 1;
             char* image = (char*)a.kv + ((size_t)x.head * units + unit) * kLatImage + x.side * kLatSide + r * 32;
             if (!spin_warp(smem_u32(&B.acc_full[buf]), (n >> 1) & 1, abort_flag)) {
@@ -311,7 +276,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                         if (m < INFINITY) vmax = fmaxf(vmax, m);
                     }
                 }
-                if (unit < units) {         // (an odd last row tile has no partner)
+                if (unit < units) {         // (the last 64 rows of a tile may lie past the copy)
                     char* to = image + c / 16 * kLatGroup;
                     store32(to, w, swap);
                     store32(to + kLatGroup, w + 8, swap);
@@ -326,7 +291,6 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
     __syncthreads();
     tc_fence_after();
     if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmem) : "memory");
-    cluster_sync();          // this CTA's copies and commits have arrived at the partner
 }
 
 // The batch's latent rows as bf16, request after request, each padded with zero rows to a
@@ -405,15 +369,15 @@ cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s) {
     CUtensorMap ma, mb;
     cudaError_t e;
     if ((e = make_map(&ma, a.rows, kLatRow, rows, kM)) != cudaSuccess) return e;
-    if ((e = make_map(&mb, a.w, kLatC, (long long)a.heads * kLatW, kN / kCluster)) != cudaSuccess) return e;
+    if ((e = make_map(&mb, a.w, kLatC, (long long)a.heads * kLatW, kN)) != cudaSuccess) return e;
     static std::atomic<uint64_t> allowed{0};
     if ((e = allow_smem((const void*)latent_expand_kernel, kSmemBytes, allowed)) != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const int tiles = (int)((rows + kCluster * kM - 1) / (kCluster * kM)) * a.heads * 2;
+    const int tiles = (int)((rows + kM - 1) / kM) * a.heads * 2;
     {
         ProfileScope ps(SPLITKV_KERNEL_LATENT_EXPAND, s);
-        latent_expand_kernel<<<kCluster * std::max(1, std::min(sms / kCluster, tiles)), kThreads, kSmemBytes, s>>>(ma, mb, a, tiles);
+        latent_expand_kernel<<<std::min(sms, tiles), kThreads, kSmemBytes, s>>>(ma, mb, a, tiles);
     }
     return cudaGetLastError();
 }
