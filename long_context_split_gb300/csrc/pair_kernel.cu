@@ -85,12 +85,17 @@ struct PairCfg {
     static_assert(NK >= 2 && NV >= 2, "slot rings");
 };
 
+// Value loads arrive on two barriers per slot in turn.  The shorter tile passes by units that only the other
+// attends, and a parity cannot tell "the slot's unit before is loading" from "this one has landed": the
+// next task's queries show that every score product of the last task is issued, so all its keys and
+// all but its last two units' values are in, but those two may be in flight.  With two barriers the load
+// before on the barrier that a tile waits on (2 NV units back) is over when the tile starts to wait.
 template <int NK, int NV>
 struct PairBars {
     unsigned long long task_full[kTR], task_empty[kTR];
     int task_slot[kTR];
     unsigned long long k_full[NK], k_empty[NK];
-    unsigned long long v_full[NV], v_empty[NV];
+    unsigned long long v_full[2 * NV], v_empty[NV];
     unsigned long long q_full, q_empty;
     unsigned long long s_full[kTiles][2], p_full[kTiles][2], pv_done[kTiles];   // [tile][S/P buffer]
     unsigned long long o_full[kTiles], o_empty[kTiles];
@@ -193,10 +198,8 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
             mbar_init(smem_u32(&B.k_full[s]), 1);
             mbar_init(smem_u32(&B.k_empty[s]), kTiles);
         }
-        for (int s = 0; s < NV; ++s) {
-            mbar_init(smem_u32(&B.v_full[s]), 1);
-            mbar_init(smem_u32(&B.v_empty[s]), kTiles);
-        }
+        for (int b = 0; b < 2 * NV; ++b) mbar_init(smem_u32(&B.v_full[b]), 1);
+        for (int s = 0; s < NV; ++s) mbar_init(smem_u32(&B.v_empty[s]), kTiles);
         mbar_init(smem_u32(&B.q_full), 1);
         mbar_init(smem_u32(&B.q_empty), kTiles);            // one per tile's MMA thread
         for (int t = 0; t < kTiles; ++t) {
@@ -243,18 +246,18 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
         return (phys * a.num_kv_heads + pt.t[t].kv) * a.page_size + key0 % a.page_size;
     };
     // one slot ring of the producers: load both tiles' boxes of every unit of a task
-    // (`map`: K or V), releasing nothing; `had`/`last` remember the slots' last copies
+    // (`map`: K or V), releasing nothing; `had`/`last` remember the barriers' last copies
     struct SlotRing {
         uint32_t item = 0, had = 0, last = 0;
     };
-    auto load_units = [&](SlotRing& rg, const PairTask& pt, int n_slots, unsigned long long* full,
+    auto load_units = [&](SlotRing& rg, const PairTask& pt, int n_slots, int n_full, unsigned long long* full,
                           unsigned long long* empty, unsigned char* base, const CUtensorMap* map) -> bool {
         for (int u = 0; u < pt.n_units; ++u) {
             const int s = (int)(rg.item % n_slots);
-            const uint32_t round = rg.item / n_slots;
-            if (!wait_bar(smem_u32(&empty[s]), (round & 1) ^ 1, abort_flag, true)) return false;
-            const uint32_t fb = smem_u32(&full[s]);
-            rg.last = (rg.last & ~(1u << s)) | ((round & 1u) << s);
+            const int b = (int)(rg.item % n_full);
+            if (!wait_bar(smem_u32(&empty[s]), ((rg.item / n_slots) & 1) ^ 1, abort_flag, true)) return false;
+            const uint32_t fb = smem_u32(&full[b]);
+            rg.last = (rg.last & ~(1u << b)) | (((rg.item / n_full) & 1u) << b);
             int y[kTiles];
             uint32_t bytes = 0;
 #pragma unroll
@@ -263,10 +266,10 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                 if (y[t] >= 0) bytes += C::TILE_BYTES;
             }
             if (bytes == 0) {
-                rg.had &= ~(1u << s);
+                rg.had &= ~(1u << b);
                 mbar_arrive(fb);
             } else {
-                rg.had |= 1u << s;
+                rg.had |= 1u << b;
                 mbar_expect_tx(fb, bytes);
                 unsigned char* st = base + s * C::SLOT_BYTES;
 #pragma unroll
@@ -281,9 +284,9 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
         return true;
     };
     // no copy of the ring may still be landing when the CTA leaves
-    auto drain_ring = [&](const SlotRing& rg, int n_slots, unsigned long long* full) {
-        for (int s = 0; s < n_slots; ++s)
-            if (((rg.had >> s) & 1u) && !wait_bar(smem_u32(&full[s]), (rg.last >> s) & 1u, abort_flag, false))
+    auto drain_ring = [&](const SlotRing& rg, int n_full, unsigned long long* full) {
+        for (int b = 0; b < n_full; ++b)
+            if (((rg.had >> b) & 1u) && !wait_bar(smem_u32(&full[b]), (rg.last >> b) & 1u, abort_flag, false))
                 set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
     };
 
@@ -326,7 +329,7 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                 q_tma = true;
                 q_par = qn & 1;
                 ++qn;
-                if (!load_units(kr, pt, NK, B.k_full, B.k_empty, sK, &tmap_k)) { give_up(SITE_EMPTY_WAIT); ok = false; break; }
+                if (!load_units(kr, pt, NK, NK, B.k_full, B.k_empty, sK, &tmap_k)) { give_up(SITE_EMPTY_WAIT); ok = false; break; }
             }
             drain_ring(kr, NK, B.k_full);
             if (q_tma && !wait_bar(smem_u32(&B.q_full), q_par, abort_flag, false)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
@@ -342,9 +345,9 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                 if (task == -2) { give_up(SITE_FULL_WAIT); break; }
                 if (task < 0) break;
                 const PairTask pt = pair_task(a, task);
-                if (!load_units(vr, pt, NV, B.v_full, B.v_empty, sV, &tmap_v)) { give_up(SITE_EMPTY_WAIT); break; }
+                if (!load_units(vr, pt, NV, 2 * NV, B.v_full, B.v_empty, sV, &tmap_v)) { give_up(SITE_EMPTY_WAIT); break; }
             }
-            drain_ring(vr, NV, B.v_full);
+            drain_ring(vr, 2 * NV, B.v_full);
         }
         __syncwarp();
     } else if (warp == 1 || warp == kIssuerWarp1) {
@@ -536,7 +539,7 @@ pair_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant
                 // to infinity, which the epilogue reports.
                 {
                     const uint32_t vi = item0 + u;
-                    if (!warp_wait(smem_u32(&B.v_full[vi % NV]), (vi / NV) & 1, abort_flag, lane)) {
+                    if (!warp_wait(smem_u32(&B.v_full[vi % (2 * NV)]), (vi / (2 * NV)) & 1, abort_flag, lane)) {
                         give_up(SITE_FULL_WAIT); ok = false; break;
                     }
                     unsigned char* vst = sV + (vi % NV) * C::SLOT_BYTES + t * C::TILE_BYTES;
