@@ -487,7 +487,8 @@ typedef struct splitkv_latent_plan_s splitkv_latent_plan_t;
 splitkv_status splitkv_latent_plan(const splitkv_problem *prob, splitkv_latent_plan_t **out);
 void splitkv_latent_plan_destroy(splitkv_latent_plan_t *plan);
 /* Device workspace of splitkv_latent_expanded: descriptors, the batch's latent rows (1152 bytes per
- * token) and the keys and values of every head (512 bytes per token and head), partial states.
+ * token) and the keys and values of every head (512 bytes per token and head, 8 bytes per 64 of
+ * them), partial states.
  * Must be 256-byte aligned. */
 size_t splitkv_latent_workspace_bytes(const splitkv_latent_plan_t *plan);
 int32_t splitkv_latent_plan_num_tasks(const splitkv_latent_plan_t *plan);
@@ -502,7 +503,11 @@ splitkv_status splitkv_latent_upload(const splitkv_latent_plan_t *plan, void *wo
  * request sees keys 0 .. seq_len - q_len + i.  prob->q is not read, and the
  * lengths are the plan's.  Keys are rounded to bf16, values and probabilities
  * to f16; scores, sums and outputs are float32 until the one rounding of the
- * result.  A finite expanded value beyond the f16 range reports DEVICE_CHECK.
+ * result.  The values of a head over 64 tokens (64 j .. 64 j + 63 of a request)
+ * are rounded times a power of two (up to 2^60) that brings the largest magnitude
+ * among them to 2^14: down to 2^-28 of that one they keep 11 bits, below it
+ * the error is at most 2^-39 of it.  A finite expanded value beyond
+ * 65504 reports DEVICE_CHECK.
  * Cache slots past a request's last token do not reach the result, whatever
  * they hold; a token's own NaN or infinity may reach the rows before it, where
  * the masked weight 0 meets it, as in the formula's matrix product.  Calls on

@@ -28,6 +28,16 @@ constexpr int kLatGroup = kLatUnit * 32;           // one 16-column group: 2 KB
 constexpr int kLatSide = 8 * kLatGroup;            // keys (or values) of a unit: 16 KB
 constexpr int kLatImage = 2 * kLatSide;
 
+// The power of two of a unit's values: f16 holds 2^-exp2 times them, with the largest finite magnitude of the
+// unit's 64 x 128 values in [2^14, 2^15).  Values are only scaled up (exp2 <= 0: what f16 does not hold is
+// reported) and by at most 2^60, which keeps the softmax's sum in float32.
+constexpr int kLatValueTop = 14, kLatValueUp = 60;
+struct LatentScale {
+    float exp2;
+    float back;             // 2^-exp2
+};
+static_assert(sizeof(LatentScale) == 8, "LatentScale layout");
+
 struct LatentReq {
     int32_t seq_len;
     int32_t q_len;
@@ -71,6 +81,7 @@ struct LatentArgs {
     const LatentBlock* blocks;
     void* rows;                // bf16 [padded rows][576]: the requests' latent rows
     void* kv;                  // [H][padded rows / 64] images of 64 keys and values, 32 KB each (see below)
+    LatentScale* v_exp;        // [H][padded rows / 64]: each unit's values in `kv`
     void* out;                 // bf16 [total_q][H][128]
     float* lse_out;            // may be null
     float* o_part;             // partial states of a split batch, or null: the tasks write final rows

@@ -22,7 +22,7 @@
 // tensor-memory buffers before O += P V of unit u; the tile's four softmax warps (a thread
 // per token) take the row maximum, keep a running maximum and sum (base 2; O is rescaled
 // only when a maximum grows by more than 2^8, so P stays below 2^8), and write P over S as
-// f16.  Two threads per token (eight warps a tile, maxima exchanged through shared
+// f16.  Each unit's values carry a power of two, which the maximum takes in and the sum takes back.  Two threads per token (eight warps a tile, maxima exchanged through shared
 // memory) measured slower on two 3.6k-token prompts (944 us against 849, before the
 // products were issued from a warp in step: 755 now).
 // P and V are f16 because their product takes one type and f16's 11 significant
@@ -529,11 +529,18 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 limit = valid ? min(t.kend - 1, t.r.seq_len - t.r.q_len + i) : -1;
                 if (trows == 0) nu = -1;
             }
+            // the powers of two of the units' values, read a unit ahead (one load for the whole warp)
+            const LatentScale* v_exp;
+            {
+                const LatentTask d = a.tasks[id];
+                v_exp = a.v_exp + (size_t)(d.head + (pair & x)) * a.num_blocks + (a.reqs[d.b].row_base + kb) / kKeys;
+            }
             const uint32_t item0 = item + (pair & x);              // its units in the rings: with two heads every second one
             item += n_units;
             if (nu < 0) continue;                                  // no token of the task in this tile
             float m = -INFINITY, l = 0.f;
             for (int u = 0; u < nu; ++u) {
+                const LatentScale ve = v_exp[u];
                 const int b2 = (int)(sn & 1), slot = (int)((item0 + (u << pair)) % NS);
                 if (!spin_warp(smem_u32(&B.s_full[x][slot]), (ph >> slot) & 1u, abort_flag)) { give_up(SITE_FULL_WAIT); ok = false; break; }
                 tc_fence_after();
@@ -545,8 +552,11 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 const int key0 = kb + u * kKeys;
                 // warp-uniform: the tensor-memory instructions below are warp-collective
                 const bool unmasked = __all_sync(0xffffffffu, key0 + kKeys - 1 <= limit);
-                // the scale is positive, so the maximum is taken before it
-                const float mx = (unmasked ? unit_max(sr) : row_max64<true>(sr, limit - key0 + 1)) * c2;
+                // The unit's values are stored times 2^-e (e = ve.exp2), so its weights enter the product as
+                // 2^(s + e - m) and the sum as 2^e back of that: O and l stay sums over one reference.  m is the
+                // maximum of s + e, by which the largest weighted value, not the largest weight, is
+                // at the top of P's range.  (The scale is positive: the maximum is taken before it.)
+                const float mx = fmaf(unmasked ? unit_max(sr) : row_max64<true>(sr, limit - key0 + 1), c2, ve.exp2);
                 float scale_o = 1.f;
                 bool need = false;
                 if (m == -INFINITY) {
@@ -580,9 +590,9 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                         SKV_ST8(lane_addr + c, o);
                     }
                 }
-                const float base = (m == -INFINITY) ? 0.f : m;
+                const float base = (m == -INFINITY) ? 0.f : m - ve.exp2;
                 const uint32_t pcol = lane_addr + kColS + kKeys * b2;
-                l += unmasked ? unit_p(sr, c2, base, pcol) : write_p16<true>(sr, c2, base, key0, limit, pcol);
+                l = fmaf(unmasked ? unit_p(sr, c2, base, pcol) : write_p16<true>(sr, c2, base, key0, limit, pcol), ve.back, l);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();

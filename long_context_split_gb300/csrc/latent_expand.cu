@@ -9,13 +9,17 @@
 // and loads the weights alone (256 KB a head from L2).  The weights' ring holds a whole tile, so
 // that the issuing warp's code is straight-line with constant slots: with one lane's loop over
 // twelve slots, issue alone took 660 cycles a box for 256 of products.  7.3k tokens and 128 heads
-// take 164 us, 1.5 PFLOP/s.
+// take 170 us, 1.45 PFLOP/s.
 //
 // Roles: warp 0 TMA producer, warp 1 MMA thread (M = 128 rows, N = 128: a head's keys or
 // its values, K = 512 in eight boxes; two accumulators), warps 2..5 the epilogue, which
 // rounds an accumulator once and stores whole lines of the attention's operand images while
 // the next tile accumulates, and which brings a new row tile into tensor memory.  Values
-// get f16's three more bits: they meet the probabilities in an f16 product.
+// get f16's three more bits: they meet the probabilities in an f16 product.  f16's range is narrow (2^-14 to
+// 65504 at full precision), so the values of 64 tokens and a head are stored times a power of two that brings the
+// largest to 2^14: magnitudes down to 2^-28 of it keep 11 bits, and the attention divides the power out exactly.
+// (Values below 2^-14 lost bits and those below 2^-25 were zero without it; it costs 163 -> 170 us, and the attention
+// 1 %.  Reading the accumulator twice instead of keeping its 128 columns in registers: 184 us.)
 //
 // Waits are bounded; on expiry the CTA records the error and drains its copies and products.
 #include <cuda_fp16.h>
@@ -46,9 +50,11 @@ struct Bars {
     unsigned long long a_ready;
     unsigned long long b_full[NS], b_empty[NS];
     unsigned long long acc_full[2], acc_empty[2];
+    unsigned long long unit_max[2];            // both warps of a unit have written its maximum
     unsigned long long drain;
     uint32_t tmem_base;
     int abort_flag;
+    float warp_max[2][kEpiWarps];              // largest value magnitude of a warp's 32 rows, tiles in turn
 };
 
 constexpr size_t kSmemBytes = 1024 + kStages * (size_t)kABox + (size_t)NS * kBBox + sizeof(Bars);
@@ -96,6 +102,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         for (int k = 0; k < 2; ++k) {
             mbar_init(smem_u32(&B.acc_full[k]), 1);
             mbar_init(smem_u32(&B.acc_empty[k]), kEpiWarps);
+            mbar_init(smem_u32(&B.unit_max[k]), 2);
         }
         mbar_init(smem_u32(&B.a_ready), kEpiWarps);
         for (int s = 0; s < NS; ++s) {
@@ -208,8 +215,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         const int quad = warp & 3;
         const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
         const int units = a.num_blocks;
-        float vmax = 0.f;
-        uint32_t n = 0, an = 0;
+        uint32_t n = 0, an = 0, vn = 0;         // tiles, row boxes, tiles of values so far
         int rows = -1;
         bool ok = true;
         for (int t = t0; t < t1 && ok; ++t, ++n) {
@@ -250,41 +256,59 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
             }
             tc_fence_after();
             const uint32_t acc = lanes + kColAcc + buf * kN;
-#pragma unroll 1
-            for (int c = 0; c < kN; c += 32) {
-                uint32_t v[32], w[16];
-                SKV_LD32(acc + c, v);
-                tc_wait_ld();
-                if (c + 32 == kN) {         // the accumulator is read: the tile after next may overwrite it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&B.acc_empty[buf]));
-                }
-                if (x.side == 0) {
+            uint32_t v[kN];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
-                        w[e] = *reinterpret_cast<const uint32_t*>(&p);
-                    }
-                } else {
+            for (int c = 0; c < kN; c += 32) SKV_LD32(acc + c, (v + c));
+            tc_wait_ld();
+            tc_fence_before();              // the accumulator is read: the tile after next may overwrite it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&B.acc_empty[buf]));
+            uint32_t w[kN / 2];
+            if (x.side == 0) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float lo = __uint_as_float(v[2 * e]), hi = __uint_as_float(v[2 * e + 1]);
-                        const __half2 p = __floats2half2_rn(lo, hi);
-                        w[e] = *reinterpret_cast<const uint32_t*>(&p);
-                        const float m = fmaxf(fabsf(lo), fabsf(hi));
-                        if (m < INFINITY) vmax = fmaxf(vmax, m);
-                    }
+                for (int e = 0; e < kN / 2; ++e) {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                    w[e] = *reinterpret_cast<const uint32_t*>(&p);
                 }
-                if (unit < units) {         // (the last 64 rows of a tile may lie past the copy)
-                    char* to = image + c / 16 * kLatGroup;
-                    store32(to, w, swap);
-                    store32(to + kLatGroup, w + 8, swap);
+            } else {
+                // the unit's largest finite magnitude: over this thread's row, the warp, the unit's two warps
+                float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int e = 0; e < kN; ++e) {
+                    const float y = fabsf(__uint_as_float(v[e]));
+                    m[e & 3] = fmaxf(m[e & 3], y < INFINITY ? y : 0.f);
+                }
+                const float own = __uint_as_float(
+                    __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])))));
+                const uint32_t bar = smem_u32(&B.unit_max[quad >> 1]);
+                if (lane == 0) {
+                    B.warp_max[vn & 1][quad] = own;
+                    mbar_arrive(bar);
+                }
+                __syncwarp();
+                if (!spin_warp(bar, vn & 1, abort_flag)) {
+                    give_up(SITE_FULL_WAIT);
+                    break;
+                }
+                const float most = fmaxf(own, ((volatile float*)B.warp_max[vn & 1])[quad ^ 1]);
+                ++vn;
+                // (2^14 <= most 2^up < 2^15; an unscaled finite value above the f16 range becomes infinite)
+                const int up = min(kLatValueUp, max(0, kLatValueTop + 127 - (int)(__float_as_uint(most) >> 23)));
+                const float scale = __uint_as_float((uint32_t)(127 + up) << 23);
+                if (most > 65504.f && lane == 0) set_error(a.err, ERR_DEVICE_CHECK | SITE_VALUE_RANGE);
+                if (!(quad & 1) && lane == 0 && unit < units)
+                    a.v_exp[(size_t)x.head * units + unit] = LatentScale{-(float)up, scale};
+#pragma unroll
+                for (int e = 0; e < kN / 2; ++e) {
+                    const __half2 p = __floats2half2_rn(__uint_as_float(v[2 * e]) * scale, __uint_as_float(v[2 * e + 1]) * scale);
+                    w[e] = *reinterpret_cast<const uint32_t*>(&p);
                 }
             }
+            if (unit < units) {         // (the last 64 rows of a tile may lie past the copy)
+#pragma unroll
+                for (int g = 0; g < kN / 16; ++g) store32(image + g * kLatGroup, w + 8 * g, swap);
+            }
         }
-        // finite values above the f16 range became infinities
-        if (vmax > 65504.f) set_error(a.err, ERR_DEVICE_CHECK | SITE_VALUE_RANGE);
         __syncwarp();
     }
     tc_fence_before();

@@ -204,7 +204,7 @@ struct splitkv_latent_plan_s {
     int64_t num_states = 0;
     std::vector<unsigned char> image;       // control block and descriptors
     size_t off_tasks = 0, off_reqs = 0, off_blocks = 0, off_indptr = 0;
-    size_t off_rows = 0, off_kv = 0, off_opart = 0, off_lse = 0, ws_bytes = 0;
+    size_t off_rows = 0, off_kv = 0, off_vexp = 0, off_opart = 0, off_lse = 0, ws_bytes = 0;
 };
 
 namespace {
@@ -311,6 +311,8 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
     off = align256(off + (size_t)rows * kLatRow * 2);
     pl->off_kv = off;
     off = align256(off + (size_t)(rows / kLatUnit) * H * kLatImage);
+    pl->off_vexp = off;
+    off = align256(off + (size_t)(rows / kLatUnit) * H * sizeof(LatentScale));
     pl->off_opart = off;
     off = align256(off + (size_t)pl->num_states * kLatV * 4);
     pl->off_lse = off;
@@ -405,6 +407,7 @@ splitkv_status splitkv_latent_expanded(const splitkv_problem* prob, const splitk
     a.blocks = (const LatentBlock*)(base + plan->off_blocks);
     a.rows = base + plan->off_rows;
     a.kv = base + plan->off_kv;
+    a.v_exp = (LatentScale*)(base + plan->off_vexp);
     if (plan->num_states > 0) {
         a.o_part = (float*)(base + plan->off_opart);
         a.lse_part = (float*)(base + plan->off_lse);
