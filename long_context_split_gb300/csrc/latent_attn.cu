@@ -21,8 +21,8 @@
 // unit u).  A tile's MMA thread issues S = Q K^T of unit u + 1 into one of two
 // tensor-memory buffers before O += P V of unit u; the tile's four softmax warps (a thread
 // per token) take the row maximum, keep a running maximum and sum (base 2; O is rescaled
-// only when a maximum grows by more than 2^8, so P stays below 2^8), and write P over S as
-// f16.  Each unit's values carry a power of two, which the maximum takes in and the sum takes back.  Two threads per token (eight warps a tile, maxima exchanged through shared
+// only when a maximum grows by more than 2^8), and write P over S as
+// f16, the maximum at 2^7 to 2^15.  Each unit's values carry a power of two, which the maximum takes in and the sum takes back.  Two threads per token (eight warps a tile, maxima exchanged through shared
 // memory) measured slower on two 3.6k-token prompts (944 us against 849, before the
 // products were issued from a warp in step: 755 now).
 // P and V are f16 because their product takes one type and f16's 11 significant
@@ -60,7 +60,13 @@ constexpr int kSoftWarps = 4 * kTiles;
 constexpr int kTaskConsumers = kTiles + kSoftWarps; // per tile an MMA thread and 4 softmax warps
 constexpr int kThreads = (1 + kTiles + kSoftWarps) * 32;
 constexpr int kIssuerWarp1 = 2 + kSoftWarps;
-constexpr float kRescaleThreshold = 8.0f;           // log2 units
+// P of a row's largest score lies in [2^kTop, 2^(kTop + kRescaleThreshold)], below f16's largest number: a weight
+// under 2^-14 is subnormal there, with an absolute error of 2^-25, so each weight is off by at most 2^-(25 + kTop) of
+// the row's largest.  The sum keeps what the product rounds away: of 2^20 keys that together hold
+// 2 % beside one that holds the rest, P at 1 lost all of that share.  (With a threshold of 4 and kTop 11 rescaling took
+// 1.5 % of the time of two 3.6k-token prompts, with 2 and 13 15 %; 8 and 7 cost what 8 and 0 do.)
+constexpr float kRescaleThreshold = 8.0f, kTop = 7.0f;   // log2 units
+static_assert(kRescaleThreshold + kTop <= 15.0f, "P within f16");
 constexpr int kTmemTile = 256;                      // tensor-memory columns per tile: O (128) | S/P | S/P
 constexpr int kColS = 128;
 constexpr int kTmemCols = kTiles * kTmemTile;
@@ -553,7 +559,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 // warp-uniform: the tensor-memory instructions below are warp-collective
                 const bool unmasked = __all_sync(0xffffffffu, key0 + kKeys - 1 <= limit);
                 // The unit's values are stored times 2^-e (e = ve.exp2), so its weights enter the product as
-                // 2^(s + e - m) and the sum as 2^e back of that: O and l stay sums over one reference.  m is the
+                // 2^(s + e + kTop - m) and the sum as 2^-e of that: O and l stay sums over one reference.  m is the
                 // maximum of s + e, by which the largest weighted value, not the largest weight, is
                 // at the top of P's range.  (The scale is positive: the maximum is taken before it.)
                 const float mx = fmaf(unmasked ? unit_max(sr) : row_max64<true>(sr, limit - key0 + 1), c2, ve.exp2);
@@ -590,7 +596,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                         SKV_ST8(lane_addr + c, o);
                     }
                 }
-                const float base = (m == -INFINITY) ? 0.f : m - ve.exp2;
+                const float base = (m == -INFINITY) ? 0.f : m - (ve.exp2 + kTop);
                 const uint32_t pcol = lane_addr + kColS + kKeys * b2;
                 l = fmaf(unmasked ? unit_p(sr, c2, base, pcol) : write_p16<true>(sr, c2, base, key0, limit, pcol), ve.back, l);
                 tc_wait_st();
@@ -609,7 +615,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             // over visible keys (NaN, or every score -inf) goes through, as in the formula
             const bool empty_row = limit < kb;
             const float inv = empty_row ? 0.f : a.v_scale / l;
-            const float lse = empty_row ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            const float lse = empty_row ? -INFINITY : ((m - kTop) + log2f(l)) * 0.69314718055994531f;
             const LatentTask d = a.tasks[id];                      // (read again: few registers across the loop)
             const LatentReq r = a.reqs[d.b];
             const int head = d.head + (pair & x);

@@ -1,12 +1,17 @@
-"""Expanded latent attention where magnitudes are far from 1: values that f16 alone would lose.
+"""Expanded latent attention where magnitudes are far from 1: values that f16 alone would lose, and many small
+weights.
 
 The bound on every element is test_gpu_latent's (keys' roundings through the scores, 2^-11 each for values
 and probabilities, 2^-13 for sums, 2^-8 for the result), relative to sum p|v| with nothing absolute that could
 hide a small value: results are compared times the power of two that brings them back to 1."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_latent import Case
+import long_context_split_gb300 as skv
+from tests.test_gpu_latent import SCALE, Case
 
 
 def _scale_values(c, powers):
@@ -110,3 +115,45 @@ def test_units_without_values():
     _, out, lse = c.run("expanded")
     assert (out[256:] == 0).all()
     c.check("expanded", out, lse)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1 << 17, 1 << 20])
+@pytest.mark.parametrize("at", ["first", "middle", "last"])
+def test_many_small_weights_beside_a_large_one(n, at):
+    """One key holds 98 % of a row's weight and n - 1 equal ones share the rest; the large key's values are 0, so
+    the result is the small ones' share.  Each small weight is off by at most 2^-32 of the largest (an f16
+    half step of 2^-25 under a largest of 2^7), all of them together by n 2^-32; the other bounds as
+    above.  Enough requests of one token keep the history in one task."""
+    others = 160
+    pages = n // 64
+    cache = torch.zeros(pages + 1, 64, 576, dtype=torch.bfloat16, device="cuda")
+    cache[:pages, :, 0] = 1.0
+    big = {"first": 0, "middle": n // 2 + 5, "last": n - 1}[at]
+    cache[big // 64, big % 64, 0] = 0.0
+    cache[big // 64, big % 64, 512] = 16.0
+    q_rope = 13.375 if n == 1 << 17 else 15.375          # scores of 0 and of 16 q_rope / sqrt(192)
+    q = torch.zeros(1 + others, 1, 192, dtype=torch.bfloat16, device="cuda")
+    q[0, 0, 128] = q_rope
+    w = torch.zeros(1, 256, 512, dtype=torch.bfloat16)
+    w[0, 128:, 0] = torch.rand(128, generator=torch.Generator().manual_seed(3)) * 0.5 + 0.5
+    table = torch.full((1 + others, pages), pages, dtype=torch.int32)
+    table[0] = torch.arange(pages)
+    lens, qo = [n] + [1] * others, list(range(2 + others))
+    att = skv.LatentAttention(form="expanded", k_cache=cache, w_kv_b=w.cuda(), page_table=table.cuda(),
+                              seq_lens=torch.tensor(lens, dtype=torch.int32).cuda(), scale=SCALE, seq_lens_host=np.array(lens, np.int32),
+                              qo_indptr=torch.tensor(qo, dtype=torch.int32).cuda(), qo_indptr_host=np.array(qo, np.int32))
+    assert (att.plan.splits() == 1).all()
+    lse = torch.zeros(1 + others, 1, device="cuda")
+    out = att(q, lse=lse)
+    torch.cuda.synchronize()
+    att.check_device_error()
+    small = (n - 1) * math.exp(-16 * q_rope * SCALE)
+    share, v = small / (1 + small), w[0, 128:, 0].double()
+    assert 0.0195 < share < 0.0255
+    tol = v * (n * 2.0 ** -32 + share * (2.0 ** -10 + 2.0 ** -13 + n / 64 * 2.0 ** -24 + 2.0 ** -8))
+    err = (out[0, 0].cpu().double() - share * v).abs()
+    assert (err <= tol).all(), f"{float((err / v).max()):.3e} of {share:.3e}"
+    # n / 64 float32 additions of a unit's sum to one that is already 1 / share times all the others': half a
+    # step of up to 2^-23 each, always to the same side where the addends are equal
+    assert abs(float(lse[0, 0]) - (16 * q_rope * SCALE + math.log1p(small))) < n / 64 * 2.0 ** -24 + 1e-5
