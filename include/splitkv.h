@@ -487,8 +487,8 @@ typedef struct splitkv_latent_plan_s splitkv_latent_plan_t;
 splitkv_status splitkv_latent_plan(const splitkv_problem *prob, splitkv_latent_plan_t **out);
 void splitkv_latent_plan_destroy(splitkv_latent_plan_t *plan);
 /* Device workspace of splitkv_latent_expanded: descriptors, the batch's latent rows (1152 bytes per
- * token) and the keys and values of every head (512 bytes per token and head, 8 bytes per 64 of
- * them), partial states.
+ * token) and keys and values (512 bytes per token and head, 8 bytes per 64 of them) of all heads or,
+ * where those exceed 8 GiB, of as many at a time as fit that, but at least two; partial states.
  * Must be 256-byte aligned. */
 size_t splitkv_latent_workspace_bytes(const splitkv_latent_plan_t *plan);
 int32_t splitkv_latent_plan_num_tasks(const splitkv_latent_plan_t *plan);

@@ -28,6 +28,10 @@ constexpr int kLatGroup = kLatUnit * 32;           // one 16-column group: 2 KB
 constexpr int kLatSide = 8 * kLatGroup;            // keys (or values) of a unit: 16 KB
 constexpr int kLatImage = 2 * kLatSide;
 
+// The images of all heads take 512 bytes per token and head: 66 GB for a million tokens of 128 heads.  Heads are
+// expanded and attended in equal groups whose images fit these bytes (a group has at least two heads).
+constexpr size_t kLatImageBytes = (size_t)8 << 30;
+
 // The power of two of a unit's values: f16 holds 2^-exp2 times them, with the largest finite magnitude of the
 // unit's 64 x 128 values in [2^14, 2^15).  Values are only scaled up (exp2 <= 0: what f16 does not hold is
 // reported) and by at most 2^60, which keeps the softmax's sum in float32.
@@ -80,8 +84,8 @@ struct LatentArgs {
     const LatentTask* tasks;
     const LatentBlock* blocks;
     void* rows;                // bf16 [padded rows][576]: the requests' latent rows
-    void* kv;                  // [H][padded rows / 64] images of 64 keys and values, 32 KB each (see below)
-    LatentScale* v_exp;        // [H][padded rows / 64]: each unit's values in `kv`
+    void* kv;                  // [group's heads][padded rows / 64] images of 64 keys and values, 32 KB each
+    LatentScale* v_exp;        // the same: each unit's values in `kv`
     void* out;                 // bf16 [total_q][H][128]
     float* lse_out;            // may be null
     float* o_part;             // partial states of a split batch, or null: the tasks write final rows
@@ -90,7 +94,9 @@ struct LatentArgs {
     int32_t* err;
     int32_t total_q;
     int32_t heads;
-    int32_t num_tasks;
+    int32_t head0;             // the group of heads of this launch: first, how many
+    int32_t group;
+    int32_t num_tasks;         // of the group
     int32_t num_blocks;        // padded rows / 64
     int32_t page_size;
     int32_t num_pages;
@@ -104,7 +110,7 @@ struct LatentArgs {
 
 // bf16 (exact) copy of the batch's latent rows, padding rows zero
 cudaError_t launch_latent_rows(const LatentArgs& a, cudaStream_t s);
-// keys and values of every head from the copy
+// keys and values of the group's heads from the copy
 cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s);
 cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s);
 // q_abs [total_q][H][576] = (q_nope W_uk | q_rope); a.q, a.w

@@ -364,7 +364,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
                 // unit u of the rings: its first row of the copies, its image
                 auto row_of = [&](int u) { return t.r.row_base + t.kb + (u >> t.pair) * kKeys; };
                 auto image = [&](int u) {
-                    return (const char*)a.kv + ((size_t)(t.head + (u & t.pair)) * a.num_blocks + row_of(u) / kKeys) * kLatImage;
+                    return (const char*)a.kv + ((size_t)(t.head - a.head0 + (u & t.pair)) * a.num_blocks + row_of(u) / kKeys) * kLatImage;
                 };
                 auto use = [&](SlotUse& slots, int b, int u) {
                     if (t.pair) slots.use(b, (u & 1) == 0, (u & 1) == 1);
@@ -539,7 +539,7 @@ latent_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid
             const LatentScale* v_exp;
             {
                 const LatentTask d = a.tasks[id];
-                v_exp = a.v_exp + (size_t)(d.head + (pair & x)) * a.num_blocks + (a.reqs[d.b].row_base + kb) / kKeys;
+                v_exp = a.v_exp + (size_t)(d.head - a.head0 + (pair & x)) * a.num_blocks + (a.reqs[d.b].row_base + kb) / kKeys;
             }
             const uint32_t item0 = item + (pair & x);              // its units in the rings: with two heads every second one
             item += n_units;

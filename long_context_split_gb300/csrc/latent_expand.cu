@@ -73,7 +73,7 @@ __device__ __forceinline__ void store32(void* p, const uint32_t* w, int swap) {
                  : "memory");
 }
 
-// Tiles (128 rows, head, keys or values); CTA c takes [c n / ctas, (c + 1) n / ctas).
+// Tiles (128 rows, head of the group, keys or values); CTA c takes [c n / ctas, (c + 1) n / ctas).
 struct Tile {
     int rows, head, side;
 };
@@ -137,7 +137,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
             int rows = -1;
             bool ok = a.inject != 1;   // (test hook: load nothing)
             for (int t = t0; t < t1 && ok; ++t) {
-                const Tile x = tile_of(t, a.heads);
+                const Tile x = tile_of(t, a.group);
                 if (x.rows != rows) {
                     rows = x.rows;
                     for (int j = 0; j < kBoxes && ok; ++j, ++an) {
@@ -148,7 +148,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
                                smem_u32(&B.as_full[an % kStages]));
                     }
                 }
-                const int y = x.head * kLatW + x.side * kN;
+                const int y = (a.head0 + x.head) * kLatW + x.side * kN;
                 for (int j = 0; j < kBoxes && ok; ++j, ++it) {
                     const int s = (int)(it % NS);
                     ok = spin_bar(smem_u32(&B.b_empty[s]), ((it / NS) & 1) ^ 1, abort_flag, true);
@@ -182,7 +182,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         bool ok = true;
         for (int t = t0; t < t1 && ok; ++t, ++n) {
             const uint32_t buf = n & 1, acc = tmem + kColAcc + buf * kN;
-            const Tile x = tile_of(t, a.heads);
+            const Tile x = tile_of(t, a.group);
             if (x.rows != rows) {
                 rows = x.rows;
                 if (!spin_warp(smem_u32(&B.a_ready), an & 1, abort_flag)) { give_up(SITE_FULL_WAIT); break; }
@@ -220,7 +220,7 @@ latent_expand_kernel(const __grid_constant__ CUtensorMap ma, const __grid_consta
         bool ok = true;
         for (int t = t0; t < t1 && ok; ++t, ++n) {
             const uint32_t buf = n & 1;
-            const Tile x = tile_of(t, a.heads);
+            const Tile x = tile_of(t, a.group);
             if (x.rows != rows) {
                 // every product of the previous rows is done: this warp has seen its last tile's end
                 rows = x.rows;
@@ -398,7 +398,7 @@ cudaError_t launch_latent_expand(const LatentArgs& a, cudaStream_t s) {
     if ((e = allow_smem((const void*)latent_expand_kernel, kSmemBytes, allowed)) != cudaSuccess) return e;
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
-    const int tiles = (int)((rows + kM - 1) / kM) * a.heads * 2;
+    const int tiles = (int)((rows + kM - 1) / kM) * a.group * 2;
     {
         ProfileScope ps(SPLITKV_KERNEL_LATENT_EXPAND, s);
         latent_expand_kernel<<<std::min(sms, tiles), kThreads, kSmemBytes, s>>>(ma, mb, a, tiles);

@@ -198,7 +198,9 @@ struct splitkv_latent_plan_s {
     int32_t pairs = 0;                      // some tasks are of two heads
     std::vector<int32_t> seq_len, qo;
     std::vector<LatentReq> reqs;
-    std::vector<LatentTask> tasks;
+    std::vector<LatentTask> tasks;          // group after group of heads
+    std::vector<int32_t> group_tasks;       // first task of each group, then their number
+    int32_t group = 0;                      // heads of a group (the last one may have fewer)
     std::vector<LatentBlock> blocks;
     std::vector<int32_t> state_indptr;      // empty when nothing is split
     int64_t num_states = 0;
@@ -220,9 +222,22 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
     pl->seq_len.assign(p->seq_lens_host, p->seq_lens_host + B);
     pl->qo.assign(p->qo_indptr_host, p->qo_indptr_host + B + 1);
     pl->total_q = pl->qo[B];
-    long long unsplit = 0, rows = 0;
-    for (int b = 0; b < B; ++b) unsplit += (long long)((pl->qo[b + 1] - pl->qo[b] + kTaskRows - 1) / kTaskRows) * H;
-    if (unsplit > (1 << 28)) return fail_with(SPLITKV_ERR_INVALID_ARG, "too many tasks");
+    long long per_head = 0, units = 0, rows = 0;      // tasks of a head before splits; units of 64 tokens
+    for (int b = 0; b < B; ++b) {
+        const int t = pl->qo[b + 1] - pl->qo[b];
+        per_head += (t + kTaskRows - 1) / kTaskRows;
+        if (t > 0) units += (pl->seq_len[b] + kLatUnit - 1) / kLatUnit;
+    }
+    if (per_head * H > (1 << 28)) return fail_with(SPLITKV_ERR_INVALID_ARG, "too many tasks");
+    if ((long long)pl->total_q * H >= (1LL << 31)) return fail_with(SPLITKV_ERR_UNSUPPORTED, "num_q_heads * query tokens exceeds 2^31");
+    if (units * kLatUnit >= (1LL << 31) - 256) return fail_with(SPLITKV_ERR_UNSUPPORTED, "cached tokens exceed 2^31");
+    // equal groups of an even number of heads (a task may be of two)
+    pl->group = H;
+    if (units * H > (long long)(kLatImageBytes / kLatImage)) {
+        const int most = std::max(2, (int)(kLatImageBytes / kLatImage / units) & ~1), groups = (H + most - 1) / most;
+        pl->group = std::min({H, most, ((H + groups - 1) / groups + 1) & ~1});
+    }
+    const long long unsplit = per_head * pl->group;       // tasks of a group, which run together
     const int sms = device_sms();
     pl->reqs.resize(B);
     for (int b = 0; b < B; ++b) {
@@ -241,7 +256,6 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
         const int blocks = (r.seq_len + kLatUnit - 1) / kLatUnit;
         for (int k = 0; k < blocks; ++k) pl->blocks.push_back(LatentBlock{b, k * kLatUnit});
         rows += (long long)blocks * kLatUnit;
-        if (rows * H >= (1LL << 31)) return fail_with(SPLITKV_ERR_UNSUPPORTED, "num_q_heads * cached tokens exceeds 2^31");
     }
     // The tasks of a (request, head, split) read the same keys and values: together, longest first,
     // so that those stay in L2; the request with the longest task first.
@@ -252,29 +266,34 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
     // there are more tasks than SMs anyway (attention over 128 heads: 32 prompts of 117 tokens 134 -> 108 us,
     // 64 of 60 162 -> 118, 2 x 96 tokens after 30,000 709 -> 676).
     const bool pairs = unsplit > sms;
-    for (int b : order) {
-        const LatentReq& r = pl->reqs[b];
-        const int group = pairs && r.q_len <= kTileRows ? 2 : 1;
-        const int nblk = (r.seq_len + kLatUnit - 1) / kLatUnit, per = nblk / r.n_splits, extra = nblk % r.n_splits;
-        for (int h = 0; h < H; h += group)
-            for (int s = 0; s < r.n_splits; ++s) {
-                const int first = s * per + std::min(s, extra), count = per + (s < extra ? 1 : 0);
-                for (int row = (r.q_len - 1) / kTaskRows * kTaskRows; r.q_len > 0 && row >= 0; row -= kTaskRows) {
-                    LatentTask t;
-                    std::memset(&t, 0, sizeof t);
-                    t.b = b;
-                    t.head = h;
-                    t.row_begin = row;
-                    t.row_end = std::min(r.q_len, row + kTaskRows);
-                    t.key_begin = std::min(first * kLatUnit, r.seq_len);
-                    t.key_end = std::min((first + count) * kLatUnit, r.seq_len);
-                    t.split = s;
-                    t.heads = std::min(group, H - h);
-                    pl->pairs |= t.heads - 1;
-                    pl->tasks.push_back(t);
+    for (int head0 = 0; head0 < H; head0 += pl->group) {
+        const int end = std::min(H, head0 + pl->group);
+        pl->group_tasks.push_back((int32_t)pl->tasks.size());
+        for (int b : order) {
+            const LatentReq& r = pl->reqs[b];
+            const int together = pairs && r.q_len <= kTileRows ? 2 : 1;
+            const int nblk = (r.seq_len + kLatUnit - 1) / kLatUnit, per = nblk / r.n_splits, extra = nblk % r.n_splits;
+            for (int h = head0; h < end; h += together)
+                for (int s = 0; s < r.n_splits; ++s) {
+                    const int first = s * per + std::min(s, extra), count = per + (s < extra ? 1 : 0);
+                    for (int row = (r.q_len - 1) / kTaskRows * kTaskRows; r.q_len > 0 && row >= 0; row -= kTaskRows) {
+                        LatentTask t;
+                        std::memset(&t, 0, sizeof t);
+                        t.b = b;
+                        t.head = h;
+                        t.row_begin = row;
+                        t.row_end = std::min(r.q_len, row + kTaskRows);
+                        t.key_begin = std::min(first * kLatUnit, r.seq_len);
+                        t.key_end = std::min((first + count) * kLatUnit, r.seq_len);
+                        t.split = s;
+                        t.heads = std::min(together, end - h);
+                        pl->pairs |= t.heads - 1;
+                        pl->tasks.push_back(t);
+                    }
                 }
-            }
+        }
     }
+    pl->group_tasks.push_back((int32_t)pl->tasks.size());
     // with any request split, every row of the batch goes through the merge (one state or more)
     bool split = false;
     for (const LatentReq& r : pl->reqs) split = split || (r.n_splits > 1 && r.q_len > 0);
@@ -310,9 +329,9 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
     pl->off_rows = off;
     off = align256(off + (size_t)rows * kLatRow * 2);
     pl->off_kv = off;
-    off = align256(off + (size_t)(rows / kLatUnit) * H * kLatImage);
+    off = align256(off + (size_t)(rows / kLatUnit) * pl->group * kLatImage);
     pl->off_vexp = off;
-    off = align256(off + (size_t)(rows / kLatUnit) * H * sizeof(LatentScale));
+    off = align256(off + (size_t)(rows / kLatUnit) * pl->group * sizeof(LatentScale));
     pl->off_opart = off;
     off = align256(off + (size_t)pl->num_states * kLatV * 4);
     pl->off_lse = off;
@@ -403,7 +422,6 @@ splitkv_status splitkv_latent_expanded(const splitkv_problem* prob, const splitk
     a.cache = prob->k_cache;
     a.page_table = prob->page_table;
     a.reqs = (const LatentReq*)(base + plan->off_reqs);
-    a.tasks = (const LatentTask*)(base + plan->off_tasks);
     a.blocks = (const LatentBlock*)(base + plan->off_blocks);
     a.rows = base + plan->off_rows;
     a.kv = base + plan->off_kv;
@@ -413,7 +431,6 @@ splitkv_status splitkv_latent_expanded(const splitkv_problem* prob, const splitk
         a.lse_part = (float*)(base + plan->off_lse);
     }
     a.ctrl = ctrl;
-    a.num_tasks = (int32_t)plan->tasks.size();
     a.pairs = plan->pairs;
     a.num_blocks = (int32_t)plan->blocks.size();
     a.page_size = prob->page_size;
@@ -424,8 +441,14 @@ splitkv_status splitkv_latent_expanded(const splitkv_problem* prob, const splitk
     a.scale_log2 = (float)((double)prob->scale * a.v_scale * 1.4426950408889634);
     cudaError_t e;
     if ((e = launch_latent_rows(a, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "latent rows launch");
-    if ((e = launch_latent_expand(a, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "latent expansion launch");
-    if ((e = launch_latent_attention(a, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "latent attention launch");
+    for (size_t g = 0; g + 1 < plan->group_tasks.size(); ++g) {
+        a.head0 = (int32_t)g * plan->group;
+        a.group = std::min(plan->group, plan->heads - a.head0);
+        a.tasks = (const LatentTask*)(base + plan->off_tasks) + plan->group_tasks[g];
+        a.num_tasks = plan->group_tasks[g + 1] - plan->group_tasks[g];
+        if ((e = launch_latent_expand(a, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "latent expansion launch");
+        if ((e = launch_latent_attention(a, (cudaStream_t)stream)) != cudaSuccess) return cuda_fail(e, "latent attention launch");
+    }
     if (plan->num_states > 0) {
         e = launch_merge(a.o_part, 0, a.lse_part, (const int32_t*)(base + plan->off_indptr), plan->total_q * plan->heads, kLatV,
                          layer->out, 1, layer->lse_out, (cudaStream_t)stream);
