@@ -247,11 +247,11 @@ splitkv_status build_latent_plan(const splitkv_problem* p, splitkv_latent_plan_t
         r.q_start = pl->qo[b];
         r.q_len = pl->qo[b + 1] - pl->qo[b];
         r.row_base = (int32_t)rows;
-        // fewer tasks than SMs: cut the histories so that the SMs are filled once, in splits of at
-        // least 1024 keys
+        // fewer tasks than SMs: cut the histories so that the SMs are filled once and no more, in splits of at
+        // least 1024 keys (one token after 65,536, 16 heads: 144 tasks 330 us, 160 tasks 400)
         r.n_splits = 1;
         if (unsplit > 0 && unsplit < sms)
-            r.n_splits = (int32_t)std::max<long long>(1, std::min<long long>((sms + unsplit - 1) / unsplit, r.seq_len / 1024));
+            r.n_splits = (int32_t)std::max<long long>(1, std::min<long long>(sms / unsplit, r.seq_len / 1024));
         if (r.q_len == 0) continue;          // nothing to attend: its rows are not copied
         const int blocks = (r.seq_len + kLatUnit - 1) / kLatUnit;
         for (int k = 0; k < blocks; ++k) pl->blocks.push_back(LatentBlock{b, k * kLatUnit});

@@ -45,6 +45,18 @@ def test_groups_are_used_only_where_they_are_needed():
     assert odd.num_tasks == 2 * 2 * int(odd.splits()[0]) * 11
 
 
+def test_a_batch_of_few_tasks_is_not_split_into_more_than_one_round():
+    """Tasks run one per SM: a task more than SMs would leave a second round nearly empty."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 152
+    # (lengths, tasks of a group before splits, groups)
+    for seq, new, heads, tasks, groups in (([1 << 20], [1], 16, 16, 1), ([1 << 16] * 3, [1, 200, 40], 7, 21, 1),
+                                           ([1 << 20], [512], 128, 32, 8), ([1 << 17], [1], 100, 100, 1),
+                                           ([50000, 30000], [300, 1], 32, 96, 1)):
+        p = _plan(seq, new, heads)
+        assert (p.splits() == sms // tasks).all()
+        assert p.num_tasks <= groups * sms
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("seq,new,heads,fp8", [
     ([140000, 200, 65], [70, 200, 65], 128, False),      # two heads per task in the long request's groups
