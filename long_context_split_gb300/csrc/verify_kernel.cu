@@ -120,7 +120,9 @@ __device__ __forceinline__ uint32_t cluster_ctarank() {
     return r;
 }
 
+// by every thread; each warp's lanes come back together first, as the aligned forms need
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
