@@ -132,10 +132,12 @@ __device__ __forceinline__ void encode(Raw<VEC * (int)sizeof(T)>& r, const float
     }
 }
 
-// x / scale rounded to nearest, for scales whose reciprocal and remainders stay normal numbers
-// (plain_scale): with inv the rounded reciprocal, the remainder x - y scale of y = x inv is exact
-// in a fused multiply-add, and one correction rounds correctly (P. Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990).
+// x / scale for scales whose reciprocal and remainders stay normal numbers (plain_scale): with inv the
+// rounded reciprocal, the remainder x - y scale of y = x inv in a fused multiply-add, and one correction
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev.
+// 34, 1990; there y starts within a unit of the quotient, here it may be a little further off).  What is needed is the
+// E4M3 code of the correctly rounded quotient, and that holds: for all 2^23 mantissas of the scale and every x
+// within four units of a border between two codes, the result lies on the right side of the border.
 // y itself serves where E4M3 saturates, for infinities and NaN, and where E4M3 is zero (of y's
 // sign: the correction would lose that of -0).
 __device__ __forceinline__ float quotient(float x, float scale, float inv) {
