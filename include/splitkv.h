@@ -396,9 +396,9 @@ splitkv_status splitkv_read_device_error(int32_t *dev_error_word, void *workspac
  *  MLA: k is [rows][head_dim_v], the latent columns, and v is
  *    [rows][head_dim_qk - head_dim_v], the rotary columns; or v is NULL and k is
  *    [rows][head_dim_qk], whole cache rows.  Head strides are not used.
- * 16-byte aligned pointers with strides that keep every row 16-byte aligned
- * (and widths that are multiples of 8) move in 16-byte pieces, others element
- * by element.
+ * 16-byte aligned pointers (the cache's too) with strides that keep every row
+ * 16-byte aligned, and widths that are multiples of 8, move in pieces of 16 or 32
+ * bytes, others element by element.
  */
 typedef struct {
     void *k;

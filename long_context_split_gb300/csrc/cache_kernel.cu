@@ -307,12 +307,14 @@ cudaError_t launch_vec(const CacheRowsArgs& a, cudaStream_t s) {
 }
 
 // The widest piece that every address allows: 16 elements for E4M3 caches (16 bytes of codes), 8 for
-// others, element by element for odd widths and offsets
+// others, 4 where float32 is on 16-byte boundaries only, element by element for odd widths and offsets
 template <typename Rows, typename Cache, bool APPEND>
 cudaError_t launch_rows(const CacheRowsArgs& a, cudaStream_t s) {
     if constexpr (sizeof(Cache) == 1)
         if (vectors_fit(a, 16, sizeof(Rows), 1)) return launch_vec<Rows, Cache, 16, APPEND>(a, s);
     if (vectors_fit(a, 8, sizeof(Rows), sizeof(Cache))) return launch_vec<Rows, Cache, 8, APPEND>(a, s);
+    if constexpr (sizeof(Rows) == 4 || sizeof(Cache) == 4)
+        if (vectors_fit(a, 4, sizeof(Rows), sizeof(Cache))) return launch_vec<Rows, Cache, 4, APPEND>(a, s);
     return launch_vec<Rows, Cache, 1, APPEND>(a, s);
 }
 
