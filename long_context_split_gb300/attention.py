@@ -72,7 +72,8 @@ class LatentAttention:
 
     ``form``: "expanded" computes every head's keys and values first (prompts,
     chunks), "absorbed" attends the latent rows themselves (decode), "auto" takes
-    the one that the lengths make cheaper.  ``params`` plans the absorbed form.
+    the one that the lengths make cheaper: one form for the whole batch, so prompts and
+    decoding requests go into batches of their own.  ``params`` plans the absorbed form.
     The plan and workspace are reusable for every layer that shares the lengths;
     ``w_kv_b`` may be replaced between calls (attribute of the same name).  Calls
     of one object share its buffers: order them on one stream.

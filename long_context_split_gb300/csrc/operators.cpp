@@ -495,8 +495,12 @@ splitkv_status splitkv_latent_project(const splitkv_problem* prob, const splitkv
 
 int32_t splitkv_latent_prefers_expanded(const splitkv_problem* prob) {
     if (check_latent_problem(prob)) return -1;
-    // Without the tcgen05 MLA kernel (128 heads, 64-token pages) the absorbed form attends on the
-    // CUDA cores: 16 heads, one token after 4,096 took 699 us against 60, 64 tokens 3957 against 58.
+    // Without the tcgen05 MLA kernel (128 heads, 64-token pages) the absorbed form attends on the CUDA cores, and
+    // the expanded one is faster at every length: in us, expanded against absorbed, one token per
+    // request, 8 / 16 / 64 heads: after 4,096 tokens 49 / 53 / 114 against 290 / 508 / 509; after 512k (8 and 16 heads)
+    // 1279 / 2840 against 4348 / 7754; 64 requests of 300 tokens 78 / 123 / 380 against 188 / 318 / 611, of 1k to
+    // 16k 985 / 1475 / 5676 against 3744 / 6669 / 16,241 (16 new tokens each: 989 / 1483 / 5741 against 21,092 /
+    // 36,719 / 137,451); 128 heads on 16-token pages, the same 64 requests, 11,263 against 21,083.
     if (!mla_tc_supports(1, 1, prob->num_q_heads, prob->head_dim_qk, prob->head_dim_v, prob->page_size)) return 1;
     // Operations per head: see splitkv_latent_layer; the absorbed kernel computes its scores in both
     // halves of the output columns and its probabilities as a high part and a residual.  The two meet

@@ -84,7 +84,7 @@ __device__ __forceinline__ void accumulate(Pair& s, Pair w) {
     s.lo = __fadd_rn(s.lo, __fadd_rn(e, w.lo));
 }
 
-// p and q of VEC tokens (q 0 without a draft row; the excluded token's q is its p)
+// p and q of VEC tokens (q 0 without a draft row; p 0 past the end and for the excluded token)
 template <int VEC>
 struct Tokens {
     float p[VEC], q[VEC];
