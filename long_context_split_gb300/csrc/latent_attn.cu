@@ -10,7 +10,7 @@
 // What bounds it: the tensor pipe (2 * 320 operations per visible pair and head).  S with
 // N = 64 keys reads both operands from shared memory at that memory's rate, 48 cycles a
 // k-step for 32 of arithmetic, so a unit of 64 keys takes 832 cycles per 128-row tile
-// instead of 640 (1 k + 2 k tokens after 14 k + 19 k at 32 heads: 680 us, 1.53
+// instead of 640 (1 k + 2 k tokens after 14 k + 19 k at 32 heads: 686 us, 1.52
 // PFLOP/s; leaving the softmax out took 692 to 681 when it was tried).  The keys and values of a
 // (request, head) are read by all of its query tiles, which run together, so they come
 // from L2.
@@ -24,7 +24,7 @@
 // only when a maximum grows by more than 2^8), and write P over S as
 // f16, the maximum at 2^7 to 2^15.  Each unit's values carry a power of two, which the maximum takes in and the sum takes back.  Two threads per token (eight warps a tile, maxima exchanged through shared
 // memory) measured slower on two 3.6k-token prompts (944 us against 849, before the
-// products were issued from a warp in step: 755 now).
+// products were issued from a warp in step: 757 now).
 // P and V are f16 because their product takes one type and f16's 11 significant
 // bits keep both roundings below the output's own; Q and K stay bf16, as given.
 // Sums, maxima and O are float32.  Products run in issue order, so S of unit u + 2
