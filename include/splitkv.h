@@ -506,10 +506,11 @@ splitkv_status splitkv_latent_upload(const splitkv_latent_plan_t *plan, void *wo
  * result.  The values of a head over 64 tokens (64 j .. 64 j + 63 of a request)
  * are rounded times a power of two (up to 2^60) that brings the largest magnitude
  * among them to 2^14: down to 2^-28 of that one they keep 11 bits, below it
- * the error is at most 2^-39 of it.  A finite expanded value beyond
- * 65504 reports DEVICE_CHECK.  A weight smaller than 2^-21 of the row's largest (both
- * times their units' powers) enters the product with an absolute error of up to 2^-32 of that
- * one: of a million such keys together, at most 2^-12.
+ * the error is at most 2^-39 of it.  A finite expanded value beyond 65504 (of an
+ * E4M3 cache: before k_scale) reports DEVICE_CHECK.  A weight smaller than 2^-21
+ * of the row's largest (both times their units' powers) enters the product with
+ * an absolute error of up to 2^-32 of that one: of a million such keys together,
+ * at most 2^-12.
  * Cache slots past a request's last token do not reach the result, whatever
  * they hold; a token's own NaN or infinity may reach the rows before it, where
  * the masked weight 0 meets it, as in the formula's matrix product.  Calls on
