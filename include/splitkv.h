@@ -126,10 +126,23 @@ typedef struct {
                                         page of the batch.  Other shapes with head_dim_qk a
                                         multiple of 16 and head_dim_v 64, 128 or 512 run on the
                                         CUDA-core path in float32.  Other problems with
-                                        kv_fp8 = 1 are UNSUPPORTED. */
-    float k_scale;                   /* kv_fp8: finite, > 0 */
-    float v_scale;                   /* kv_fp8: finite, > 0 */
+                                        kv_fp8 = 1 are UNSUPPORTED.
+                                        2: E4M3 codes with a scale for each block of scale_block
+                                        tokens and KV head (the fields below), GQA only; what
+                                        else kv_fp8 = 1 asks for holds here too. */
+    float k_scale;                   /* kv_fp8 1: finite, > 0 */
+    float v_scale;                   /* kv_fp8 1: finite, > 0 */
     int32_t reserved0;               /* 0 */
+    /* Read only when kv_fp8 is 2 (a caller without these fields passes 0 or 1).  The value of a
+       code in slot s of page p and KV head h is e4m3(code) * scales[p][h][s / scale_block].
+       Scales are 0 or from 2^-100 to 2^100; those of blocks that no visible token
+       lies in may be anything.  Scores take a key's scale in float32; a weight meets its value's
+       scale in float32 and is rounded to f16 relative to the largest such product of its row
+       (of the keys that one warp has met), so that blocks of very different scales keep their bits. */
+    const float *k_block_scales;     /* device [num_pages][num_kv_heads][page_size / scale_block] */
+    const float *v_block_scales;     /* the same */
+    int32_t scale_block;             /* 16, 32, 64 or 128; divides page_size */
+    int32_t reserved1;               /* 0 */
 } splitkv_problem;
 
 typedef enum { SPLITKV_PLAN_UNIFORM = 0, SPLITKV_PLAN_CRITICAL_WAVE = 1 } splitkv_plan_mode;
@@ -423,6 +436,14 @@ typedef struct {
  *    nearest even, E4M3 caches the code of sat(x / k_scale) (or v_scale; MLA
  *    rows take k_scale): the quotient in float32, rounded to nearest even,
  *    magnitudes above 448 (infinities too) to 448, NaN to the NaN code.
+ *  Block scales (kv_fp8 2) are written too.  A block whose first slot is among the new
+ *    tokens gets the smallest power of two (from 2^-126) whose 448-fold reaches its
+ *    tokens' largest finite magnitude.  A block that holds older tokens of the request
+ *    keeps its scale while 448 times it reaches the new tokens' largest magnitude;
+ *    otherwise it gets the power of two of those, and the older codes become those
+ *    of sat(e4m3(code) * old / new).  Powers of two divide exactly, so that a code
+ *    changes only where it falls below E4M3's smallest normal.  No other request may
+ *    read or append to such a block's slots meanwhile (requests share whole blocks only).
  *  Positions come from the device arrays seq_lens and qo_indptr, so a captured
  *    call follows lengths updated in place; the host arrays give the number of
  *    rows and the argument checks.  Rows behind the device qo_indptr's last
@@ -442,8 +463,8 @@ splitkv_status splitkv_kv_append(const splitkv_problem *prob, const splitkv_kv_r
  *    kv_begin[b] + i of request b, which must lie below seq_lens[b].
  *  num_rows: rows that `rows` holds, >= kv_indptr[batch]; rows behind
  *    kv_indptr[batch] are left as they were.
- *  Values: E4M3 codes times k_scale / v_scale in float32, rounded once to the
- *    row type; other entries are converted to it.
+ *  Values: E4M3 codes times k_scale / v_scale, or their block's scale, in float32,
+ *    rounded once to the row type; other entries are converted to it.
  *  dev_error_word: as splitkv_kv_append; a refused row is written as zeros.
  */
 splitkv_status splitkv_kv_gather(const splitkv_problem *prob, const int32_t *kv_indptr, const int32_t *kv_begin,
@@ -588,6 +609,86 @@ typedef struct {
  */
 splitkv_status splitkv_verify_drafts(const splitkv_verify *v, int32_t *dev_error_word, splitkv_stream stream);
 
+/*
+ * The pages of a batch's requests, and where they come from.  All pointers device.
+ */
+typedef struct {
+    int32_t batch;                   /* 1 .. 8192 */
+    int32_t page_size;
+    int32_t max_pages_per_req;       /* row stride of page_table */
+    int32_t capacity;                /* entries of free_pages (a pool's pages all fit where it is num_pages) */
+    int32_t *page_table;             /* [batch][max_pages_per_req]: entries 0 .. held[b] - 1 of row b are request b's */
+    const int32_t *held;             /* [batch]: pages that each request holds */
+    int32_t *held_out;               /* [batch], after the call (may be held itself) */
+    const int32_t *seq_lens;         /* [batch]: tokens that each request is to have room for; 0: it has ended */
+    int32_t *free_pages;             /* [capacity]: the ids of the free pages, the next one to be taken last */
+    const int32_t *free_count;       /* [1]: how many there are */
+    int32_t *free_count_out;         /* [1], after the call (may be free_count itself) */
+    const int32_t *qo_indptr;        /* [batch + 1], or NULL without slots */
+    int64_t *slots;                  /* [num_slots], or NULL: the cache slot, page * page_size + offset, of every new token:
+                                        entry qo_indptr[b] + i is that of token seq_lens[b] - q_len + i */
+    int32_t num_slots;               /* entries of slots; those from qo_indptr[batch] on are left as they were */
+    int32_t reserved;                /* 0 */
+} splitkv_pages;
+
+/*
+ * splitkv_assign_pages -- give every request the ceil(seq_lens[b] / page_size) pages
+ * that its length needs, on the GPU: the page table that the other calls read, from
+ * lengths alone (a captured call follows lengths updated in place).
+ *  Requests that hold more (ended ones, refused drafts) give the surplus back first:
+ *    page_table[b][need .. held - 1] go onto the free list, request after request, in
+ *    order.  Those that hold too few then take ids from the list's end, in order.  Table
+ *    entries behind a request's pages are left as they were.
+ *  dev_error_word: device int32 or NULL.  A request that needs more than
+ *    max_pages_per_req, or whose pages together with those of the growing requests before it exceed
+ *    the free ones, gets none (it keeps what it holds) and reports DEVICE_CHECK; a
+ *    negative length counts as 0 and reports it too, as do a held or free count out of
+ *    range (taken as the nearest one in range) and pages given back beyond `capacity`
+ *    (dropped).  Slots of tokens without a page are -1, so are all those of a request whose
+ *    qo_indptr entries decrease, leave num_slots or exceed its length (reported).
+ */
+splitkv_status splitkv_assign_pages(const splitkv_pages *p, int32_t *dev_error_word, splitkv_stream stream);
+
+/*
+ * Logits of the next tokens and each row's settings.  All pointers device; a NULL setting is off
+ * for every row.
+ */
+typedef struct {
+    int32_t rows;
+    int32_t vocab;                   /* 1 .. 2^19 */
+    int32_t dtype;                   /* splitkv_dtype of logits */
+    int32_t reserved;                /* 0 */
+    const void *logits;              /* [rows][vocab], row stride logits_stride */
+    int64_t logits_stride;           /* elements, >= vocab */
+    const float *temperature;        /* [rows], >= 0; 0: the most likely token */
+    const int32_t *top_k;            /* [rows]; <= 0: off */
+    const float *top_p;              /* [rows]; >= 1 (and NaN): off; <= 0: the most likely token */
+    const float *min_p;              /* [rows]; <= 0 (and NaN): off; above 1 counts as 1 */
+    const float *sample_u;           /* [rows] random numbers in [0, 1); NULL without out_tokens */
+    int32_t *out_tokens;             /* [rows] or NULL */
+    float *probs;                    /* [rows][vocab] or NULL: the distributions drawn from */
+    int64_t probs_stride;            /* elements, >= vocab */
+} splitkv_sample;
+
+/*
+ * splitkv_sample_tokens -- draw a token from each row of logits x, and / or write the
+ * distributions that splitkv_verify_drafts takes.  With m the row's largest logit and T its
+ * temperature, the weight of token i is exp((x_i - m) / T).  In turn, each on what the ones before
+ * have left: min_p keeps tokens of (x_i - m) / T >= log(min_p); top_k the k largest; top_p
+ * the fewest of the largest whose weights reach top_p times the weight that is left.  Equal logits
+ * rank in the order of their tokens.  The token drawn is the lowest whose cumulative
+ * weight exceeds sample_u times the total; probs are weights over the total, 0 for tokens not kept.
+ *  Logits that are NaN or -infinity have no weight; a row without any other gives token -1 and
+ *    probabilities of 0.  Infinite logits share all the weight.  T = 0 is the largest logit's
+ *    lowest token, whatever the other settings.
+ *    Random numbers of 1 and more draw the last token with weight, negative ones and NaN the first.
+ *  Weights are whole multiples of 2^-44 of the largest, computed to 2^-40 of themselves, so that their sums do
+ *    not depend on any order; probs are float32.
+ *  dev_error_word: device int32 or NULL.  A negative or NaN temperature reports
+ *    DEVICE_CHECK and gives token -1 and probabilities of 0.
+ */
+splitkv_status splitkv_sample_tokens(const splitkv_sample *s, int32_t *dev_error_word, splitkv_stream stream);
+
 /* Message for the last error returned on the calling thread. */
 const char *splitkv_last_error_message(void);
 const char *splitkv_status_string(splitkv_status s);
@@ -724,7 +825,9 @@ typedef enum {
     SPLITKV_KERNEL_LATENT_ATTENTION = 13,  /* expanded latent attention */
     SPLITKV_KERNEL_LATENT_ABSORB = 14,     /* queries times W_uk */
     SPLITKV_KERNEL_LATENT_PROJECT = 15,    /* merge of latent outputs, times W_uv^T */
-    SPLITKV_KERNEL_COUNT = 16
+    SPLITKV_KERNEL_ASSIGN_PAGES = 16,      /* page tables and slots from lengths */
+    SPLITKV_KERNEL_SAMPLE = 17,            /* the next tokens from logits */
+    SPLITKV_KERNEL_COUNT = 18
 } splitkv_kernel;
 
 typedef struct {

@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libsplitkv.so")
 SOURCES = ["api.cpp", "planner.cpp", "merge_kernel.cu", "generic_kernel.cu", "gqa_engine.cu", "mla_kernel.cu",
            "chunk_kernel.cu", "pair_kernel.cu", "static_scratch.cu", "profile.cpp",
            "cache_kernel.cu", "verify_kernel.cu", "latent_absorb.cu", "latent_expand.cu", "latent_attn.cu",
-           "latent_project.cu", "operators.cpp"]
+           "latent_project.cu", "operators.cpp", "block_append_kernel.cu", "pages_kernel.cu", "sample_kernel.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -11,7 +11,7 @@ import ctypes
 import os
 import struct
 import threading
-from typing import Optional, Sequence
+from typing import Optional, Sequence, Union
 
 import numpy as np
 import torch
@@ -51,6 +51,8 @@ class Problem(ctypes.Structure):
         ("qo_indptr_host", ctypes.c_void_p),
         ("kv_fp8", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
         ("reserved0", ctypes.c_int32),
+        ("k_block_scales", ctypes.c_void_p), ("v_block_scales", ctypes.c_void_p),
+        ("scale_block", ctypes.c_int32), ("reserved1", ctypes.c_int32),
     ]
 
 
@@ -103,10 +105,12 @@ class KernelTime(ctypes.Structure):
     _fields_ = [("launches", ctypes.c_int32), ("pad", ctypes.c_int32), ("total_ms", ctypes.c_double)]
 
 
-# splitkv_kv_rows and splitkv_verify, packed as bytes for each call (a fifth of the host time of
-# filling a ctypes.Structure)
+# splitkv_kv_rows, splitkv_verify, splitkv_pages and splitkv_sample, packed as bytes for each call (a
+# fifth of the host time of filling a ctypes.Structure)
 _KV_ROWS = struct.Struct("@PPqqqqii")
 _VERIFY = struct.Struct("@iiiiPPPPqqPPPPPP")
+_PAGES = struct.Struct("@iiiiPPPPPPPPPii")
+_SAMPLE = struct.Struct("@iiiiPqPPPPPPPq")
 
 
 class LatentLayer(ctypes.Structure):
@@ -118,7 +122,8 @@ class LatentLayer(ctypes.Structure):
 KERNEL_NAMES = ["generic_partial_kernel", "gqa_engine_kernel", "mla_partial_kernel", "chunk_tc_kernel",
                 "merge_states_kernel", "chunk_value_convert_kernel", "pair_tc_kernel", "mla_latent_convert_kernel",
                 "kv_append_kernel", "kv_gather_kernel", "verify_drafts_kernel", "latent_rows_kernel", "latent_expand_kernel",
-                "latent_attention_kernel", "latent_absorb_kernel", "latent_project_kernel"]
+                "latent_attention_kernel", "latent_absorb_kernel", "latent_project_kernel", "assign_pages_kernel",
+                "sample_tokens_kernel"]
 
 # name -> (restype, argtypes); this list mirrors include/splitkv.h
 _vp, _i32, _i64, _dp = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_double)
@@ -167,6 +172,8 @@ SIGNATURES = {
                                               _vp, _vp]),
     "splitkv_latent_prefers_expanded": (_i32, [ctypes.POINTER(Problem)]),
     "splitkv_verify_drafts": (ctypes.c_int, [_vp, _vp, _vp]),
+    "splitkv_assign_pages": (ctypes.c_int, [_vp, _vp, _vp]),
+    "splitkv_sample_tokens": (ctypes.c_int, [_vp, _vp, _vp]),
     "splitkv_read_device_error": (ctypes.c_int, [_vp, _vp, _i32, _ip, _vp]),
     "splitkv_read_static_device_error": (ctypes.c_int, [_i32, _ip, _vp]),
     "splitkv_last_error_message": (ctypes.c_char_p, []),
@@ -236,7 +243,10 @@ class AttentionProblem:
     ``v_cache=None``; ``page_table`` int32 [B, max_pages]; ``seq_lens`` int32
     [B]; ``qo_indptr`` int32 [B+1].  Host copies of the lengths are taken once
     here (or passed in) for the planner.  K/V caches of dtype uint8 hold E4M3
-    codes (an FP8 KV cache) whose values are code * ``k_scale`` / ``v_scale``.
+    codes (an FP8 KV cache) whose values are code * ``k_scale`` / ``v_scale``:
+    one number per tensor, or (GQA) float32 tensors [num_pages, Hkv, P / S] with
+    one for each block of S = 16, 32, 64 or 128 tokens and head, which
+    ``kv_append`` writes.
     """
 
     def __init__(self, *, q: torch.Tensor, k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
@@ -245,7 +255,7 @@ class AttentionProblem:
                  page_size: int, scale: float, kind: str = "gqa",
                  seq_lens_host: Optional[Sequence[int]] = None,
                  qo_indptr_host: Optional[Sequence[int]] = None,
-                 k_scale: Optional[float] = None, v_scale: Optional[float] = None):
+                 k_scale: Union[float, torch.Tensor, None] = None, v_scale: Union[float, torch.Tensor, None] = None):
         self.q, self.k_cache, self.v_cache = q, k_cache, v_cache
         self.page_table, self.seq_lens, self.qo_indptr = page_table, seq_lens, qo_indptr
         for name, t in (("page_table", page_table), ("seq_lens", seq_lens), ("qo_indptr", qo_indptr)):
@@ -259,8 +269,25 @@ class AttentionProblem:
         self.kv_fp8 = k_cache.dtype == torch.uint8
         if self.kv_fp8 != (k_scale is not None and v_scale is not None):
             raise TypeError("uint8 (E4M3) K/V caches come with k_scale and v_scale, other caches without")
-        self.k_scale = float(k_scale) if self.kv_fp8 else 1.0
-        self.v_scale = float(v_scale) if self.kv_fp8 else 1.0
+        blocks = isinstance(k_scale, torch.Tensor) and k_scale.dim() > 0
+        if blocks != (isinstance(v_scale, torch.Tensor) and v_scale.dim() > 0):
+            raise TypeError("k_scale and v_scale are both numbers or both block scales")
+        self.scale_block = 0
+        if blocks:
+            if kind != "gqa":
+                raise TypeError("block scales are for GQA caches")
+            if k_scale.dim() != 3 or k_scale.shape[2] < 1 or page_size % k_scale.shape[2]:
+                raise TypeError("block scales must be [num_pages, num_kv_heads, blocks of a page]")
+            self.scale_block = page_size // int(k_scale.shape[2])
+            for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t.dtype != torch.float32 or not t.is_contiguous() or t.shape != (k_cache.shape[0], num_kv_heads,
+                                                                                   page_size // self.scale_block):
+                    raise TypeError(f"{name} must be contiguous float32 [num_pages, num_kv_heads, page_size // block], "
+                                    "the same for keys and values")
+            self.k_scale, self.v_scale = k_scale, v_scale
+        else:
+            self.k_scale = float(k_scale) if self.kv_fp8 else 1.0
+            self.v_scale = float(v_scale) if self.kv_fp8 else 1.0
         self.seq_lens_host = np.ascontiguousarray(
             seq_lens.cpu().numpy() if seq_lens_host is None else seq_lens_host, dtype=np.int32)
         self.qo_indptr_host = np.ascontiguousarray(
@@ -280,8 +307,10 @@ class AttentionProblem:
             v_cache=(v_cache.data_ptr() if v_cache is not None else None),
             page_table=page_table.data_ptr(), seq_lens=seq_lens.data_ptr(),
             qo_indptr=qo_indptr.data_ptr(), seq_lens_host=self.seq_lens_host.ctypes.data,
-            qo_indptr_host=self.qo_indptr_host.ctypes.data, kv_fp8=int(self.kv_fp8),
-            k_scale=self.k_scale, v_scale=self.v_scale, reserved0=0)
+            qo_indptr_host=self.qo_indptr_host.ctypes.data, kv_fp8=2 if blocks else int(self.kv_fp8),
+            k_scale=1.0 if blocks else self.k_scale, v_scale=1.0 if blocks else self.v_scale, reserved0=0,
+            k_block_scales=k_scale.data_ptr() if blocks else None, v_block_scales=v_scale.data_ptr() if blocks else None,
+            scale_block=self.scale_block, reserved1=0)
         self.address = ctypes.addressof(self._s)
 
     @property
@@ -623,6 +652,100 @@ def verify_drafts(tokens: torch.Tensor, qo_indptr: torch.Tensor, target_probs: t
     if st:
         _check(st)
     return out_tokens, accepted
+
+
+def assign_pages(page_table: torch.Tensor, held: torch.Tensor, seq_lens: torch.Tensor, free_pages: torch.Tensor,
+                 free_count: torch.Tensor, *, page_size: int, held_out: Optional[torch.Tensor] = None,
+                 free_count_out: Optional[torch.Tensor] = None, qo_indptr: Optional[torch.Tensor] = None,
+                 slots: Optional[torch.Tensor] = None, dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    """splitkv_assign_pages: give every request the pages that its length needs.  page_table
+    [B, max_pages] int32 (the rows' first held[b] entries are in use), held [B], seq_lens [B],
+    free_pages [capacity] int32 with free_count [1] ids in it: requests that hold more than
+    ceil(seq_lens / page_size) pages give the surplus back, those that hold fewer take from the
+    end of free_pages.  held and free_count are updated in place, or into held_out and
+    free_count_out.  With qo_indptr [B + 1], slots int64 [rows] gets the cache slot (page *
+    page_size + offset) of every new token."""
+    i32 = torch.int32
+    batch = held.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != batch:
+        raise TypeError(f"page_table must be [{batch}, max_pages]")
+    _check_array("page_table", page_table, page_table.numel(), i32)
+    _check_array("held", held, batch, i32)
+    _check_array("seq_lens", seq_lens, batch, i32)
+    _check_array("free_pages", free_pages, free_pages.numel(), i32)
+    _check_array("free_count", free_count, 1, i32)
+    if held_out is None:
+        held_out = held
+    else:
+        _check_array("held_out", held_out, batch, i32)
+    if free_count_out is None:
+        free_count_out = free_count
+    else:
+        _check_array("free_count_out", free_count_out, 1, i32)
+    if (qo_indptr is None) != (slots is None):
+        raise TypeError("qo_indptr and slots come together")
+    qo = at = n = 0
+    if slots is not None:
+        _check_array("qo_indptr", qo_indptr, batch + 1, i32)
+        _check_array("slots", slots, slots.numel(), torch.int64)
+        qo, at, n = qo_indptr.data_ptr(), slots.data_ptr(), slots.numel()
+    p = _PAGES.pack(batch, page_size, page_table.shape[1], free_pages.numel(), page_table.data_ptr(), held.data_ptr(),
+                    held_out.data_ptr(), seq_lens.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                    free_count_out.data_ptr(), qo, at, n, 0)
+    st = (_lib or load()).splitkv_assign_pages(p, _ptr(dev_error_word), _stream_handle(stream))
+    if st:
+        _check(st)
+
+
+def sample_tokens(logits: torch.Tensor, sample_u: Optional[torch.Tensor], *, temperature: Optional[torch.Tensor] = None,
+                  top_k: Optional[torch.Tensor] = None, top_p: Optional[torch.Tensor] = None,
+                  min_p: Optional[torch.Tensor] = None, out_tokens: Optional[torch.Tensor] = None,
+                  probs_out: Optional[torch.Tensor] = None, dev_error_word: Optional[torch.Tensor] = None, stream=None):
+    """splitkv_sample_tokens: draw a token from each row of logits [rows, vocab] (float32 or
+    bfloat16, any row stride) by sample_u [rows]; temperature, top_p, min_p float32 [rows] and
+    top_k int32 [rows] (None: off; min_p, then top_k, then top_p).  probs_out float32 [rows,
+    vocab], when given, gets the distributions drawn from (the target_probs of verify_drafts);
+    with sample_u None only those are written.  Returns out_tokens int32 [rows] (None without
+    sample_u)."""
+    rows, vocab = logits.shape
+    if logits.dtype not in _DTYPES:
+        raise TypeError(f"unsupported logits dtype {logits.dtype}")
+    if logits.stride(1) != 1 and vocab > 1 and rows > 0:
+        raise TypeError("logits must have contiguous rows")
+    f32 = torch.float32
+    t = k = p = m = u = out = probs = 0
+    if temperature is not None:
+        _check_array("temperature", temperature, rows, f32)
+        t = temperature.data_ptr()
+    if top_k is not None:
+        _check_array("top_k", top_k, rows, torch.int32)
+        k = top_k.data_ptr()
+    if top_p is not None:
+        _check_array("top_p", top_p, rows, f32)
+        p = top_p.data_ptr()
+    if min_p is not None:
+        _check_array("min_p", min_p, rows, f32)
+        m = min_p.data_ptr()
+    if sample_u is not None:
+        _check_array("sample_u", sample_u, rows, f32)
+        u = sample_u.data_ptr()
+        if out_tokens is None:
+            out_tokens = torch.empty(rows, dtype=torch.int32, device=logits.device)
+        else:
+            _check_array("out_tokens", out_tokens, rows, torch.int32)
+        out = out_tokens.data_ptr()
+    elif out_tokens is not None or probs_out is None:
+        raise TypeError("without sample_u there are no tokens to write, only probs_out")
+    probs_stride = vocab
+    if probs_out is not None:
+        probs_stride = _check_probs(probs_out, rows, vocab)
+        probs = probs_out.data_ptr()
+    s = _SAMPLE.pack(rows, vocab, _DTYPES[logits.dtype], 0, logits.data_ptr(), logits.stride(0) if rows > 1 else vocab,
+                     t, k, p, m, u, out, probs, probs_stride)
+    st = (_lib or load()).splitkv_sample_tokens(s, _ptr(dev_error_word), _stream_handle(stream))
+    if st:
+        _check(st)
+    return out_tokens
 
 
 def _check_probs(t: torch.Tensor, total: int, vocab: int) -> int:

@@ -108,6 +108,7 @@ struct splitkv_plan_s {
     int32_t trace = 0;                 // the workspace holds trace records (splitkv_plan_params.trace)
     size_t off_trace = 0;
     size_t off_vhp = 0, off_vh = 0;    // f16 value copy: its slot list (in the image) and its pages
+    size_t off_kh = 0, off_units = 0;  // block scales: the copies' key pages and the scales of 16 tokens each
     int32_t n_trace = 0, trace_red0 = 0, trace_chunk0 = 0, trace_pair0 = 0;   // records; first reduction /
                                                                               // chunk / paired-tile record
     int32_t rows_per_task = kRowsPerTask;
@@ -154,9 +155,17 @@ splitkv_status check_problem_shape(const splitkv_problem* p) {
             return fail(SPLITKV_ERR_INVALID_ARG, "MLA needs head_dim_v <= head_dim_qk");
     }
     if (!std::isfinite(p->scale)) return fail(SPLITKV_ERR_INVALID_ARG, "scale is not finite");
-    if (p->kv_fp8 != 0 && p->kv_fp8 != 1) return fail(SPLITKV_ERR_INVALID_ARG, "kv_fp8 %d", p->kv_fp8);
+    if (p->kv_fp8 < 0 || p->kv_fp8 > 2) return fail(SPLITKV_ERR_INVALID_ARG, "kv_fp8 %d", p->kv_fp8);
     if (p->reserved0 != 0) return fail(SPLITKV_ERR_INVALID_ARG, "reserved0 must be 0");
-    if (p->kv_fp8 && !(std::isfinite(p->k_scale) && std::isfinite(p->v_scale) && p->k_scale > 0.f &&
+    if (p->kv_fp8 == 2) {
+        if (p->kind != SPLITKV_GQA) return fail(SPLITKV_ERR_UNSUPPORTED, "block scales are for GQA caches");
+        if (p->scale_block != 16 && p->scale_block != 32 && p->scale_block != 64 && p->scale_block != 128)
+            return fail(SPLITKV_ERR_INVALID_ARG, "scale_block %d is not 16, 32, 64 or 128", p->scale_block);
+        if (p->page_size % p->scale_block)
+            return fail(SPLITKV_ERR_INVALID_ARG, "scale_block %d does not divide page_size %d", p->scale_block, p->page_size);
+        if (p->reserved1 != 0) return fail(SPLITKV_ERR_INVALID_ARG, "reserved1 must be 0");
+    }
+    if (p->kv_fp8 == 1 && !(std::isfinite(p->k_scale) && std::isfinite(p->v_scale) && p->k_scale > 0.f &&
                        p->v_scale > 0.f))
         return fail(SPLITKV_ERR_INVALID_ARG, "k_scale and v_scale must be finite and > 0");
     if (!p->seq_lens_host || !p->qo_indptr_host)
@@ -290,6 +299,12 @@ splitkv_status check_problem_ptrs(const splitkv_problem* p) {
     } else if (p->v_cache) {
         return fail(SPLITKV_ERR_INVALID_ARG, "MLA takes values from k_cache; v_cache must be NULL");
     }
+    if (p->kv_fp8 == 2) {
+        if (((uintptr_t)p->k_block_scales | (uintptr_t)p->v_block_scales) & 3)
+            return fail(SPLITKV_ERR_INVALID_ARG, "block scales are not aligned to their elements");
+        if ((s = check_device_ptr(p->k_block_scales, "k_block_scales", false))) return s;
+        if ((s = check_device_ptr(p->v_block_scales, "v_block_scales", false))) return s;
+    }
     if ((s = check_device_ptr(p->page_table, "page_table", false))) return s;
     if ((s = check_device_ptr(p->seq_lens, "seq_lens", false))) return s;
     if ((s = check_device_ptr(p->qo_indptr, "qo_indptr", false))) return s;
@@ -354,11 +369,19 @@ KernelArgs kernel_args(const splitkv_problem* p, const splitkv_plan_t* pl, void*
     a.mla = p->kind == SPLITKV_MLA ? 1 : 0;
     // E4M3 caches: the key scale folds into the score scale, the value scale multiplies the
     // normalised partial output
-    a.scale_log2 = (float)((double)p->scale * (p->kv_fp8 ? (double)p->k_scale : 1.0) * 1.4426950408889634);
+    a.scale_log2 = (float)((double)p->scale * (p->kv_fp8 == 1 ? (double)p->k_scale : 1.0) * 1.4426950408889634);
     a.kv_fp8 = p->kv_fp8;
-    a.v_scale = p->kv_fp8 ? (p->kind == SPLITKV_MLA ? p->k_scale : p->v_scale) : 1.f;   // MLA values are latent rows
+    if (p->kv_fp8 == 2) {
+        a.k_scales = p->k_block_scales;
+        a.v_scales = p->v_block_scales;
+        while ((1 << a.scale_shift) < p->scale_block) ++a.scale_shift;
+    }
+    a.v_scale = p->kv_fp8 == 1 ? (p->kind == SPLITKV_MLA ? p->k_scale : p->v_scale) : 1.f;   // MLA values are latent rows
     a.part_bf16 = pl->part_bf16;
     a.v_half = base + pl->off_vh;
+    a.k_half = base + pl->off_kh;
+    a.k_unit = (const float*)(base + pl->off_units);
+    a.v_unit = a.k_unit + pl->vh_pages.size() * (size_t)p->num_kv_heads * (p->page_size / 16);
     a.vh_pages = (const VhPage*)(base + pl->off_vhp);
     a.num_vh_pages = (int32_t)pl->vh_pages.size();
     a.lat_copy = pl->lat_copy;
@@ -386,7 +409,8 @@ cudaError_t launch_chunk_tiles(const KernelArgs& a, const splitkv_problem* p, co
     if (a.trace) c.trace = a.trace + pl->trace_chunk0;
     c.trace_red = nullptr;
     c.num_tasks = (int32_t)pl->ctasks.size();
-    cudaError_t e = launch_chunk_value_convert(c, (cudaStream_t)stream);
+    cudaError_t e = a.kv_fp8 == 2 ? launch_chunk_block_convert(c, (cudaStream_t)stream)
+                                  : launch_chunk_value_convert(c, (cudaStream_t)stream);
     if (e != cudaSuccess) return e;
     return launch_chunk_partial(c, pl->qo[pl->batch], p->num_pages, (cudaStream_t)stream);
 }
@@ -568,7 +592,7 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
     // paired-tile kernel) for 33..128 rows; otherwise 64 rows (the engine's wide prefill
     // mode) above 16; all heads of one token on the MLA path
     // (the tile kernels fold the scale into the exponent after the row max: scale > 0)
-    const bool chunk_ok = pl->path == 1 && prob->scale > 0.f && !pl->interleave && !prob->kv_fp8 &&
+    const bool chunk_ok = pl->path == 1 && prob->scale > 0.f && !pl->interleave && prob->kv_fp8 != 1 &&
                           chunk_tc_supports(prob->dtype == SPLITKV_BF16, prob->head_dim_qk, P, g);
     const bool pair_ok = pl->path == 1 && prob->scale > 0.f && !pl->interleave && !prob->kv_fp8 &&
                          pair_tc_supports(prob->dtype == SPLITKV_BF16, prob->head_dim_qk, P, g);
@@ -579,7 +603,8 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
         long long rows = (long long)pl->q_len[b] * g;
         rpt[b] = pl->rows_per_task;
         if (pl->path == 1 && P >= 64 && rows > 16) rpt[b] = 64;
-        if (chunk_ok && rows > 128) {
+        // (block scales: no paired tiles)
+        if (chunk_ok && rows > (prob->kv_fp8 == 2 ? 64 : 128)) {
             rpt[b] = 256;
             is_chunk[b] = 1;
         } else if (pair_ok && rows > 32) {
@@ -872,6 +897,12 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
     pl->off_vh = off;
     off = align256(off + pl->vh_pages.size() * (size_t)P *
                              (pl->lat_copy ? (size_t)prob->head_dim_qk : (size_t)prob->num_kv_heads * prob->head_dim_v) * 2);
+    if (prob->kv_fp8 == 2 && !pl->vh_pages.empty()) {
+        pl->off_kh = off;
+        off = align256(off + pl->vh_pages.size() * (size_t)P * prob->num_kv_heads * prob->head_dim_qk * 2);
+        pl->off_units = off;
+        off = align256(off + pl->vh_pages.size() * (size_t)prob->num_kv_heads * (P / 16) * 2 * sizeof(float));
+    }
     pl->ws_bytes = off;
     pl->image.assign(pl->image_bytes, 0);
     std::memcpy(pl->image.data() + pl->off_tasks, pl->tasks.data(), pl->tasks.size() * sizeof(TaskDesc));

@@ -31,6 +31,9 @@ constexpr int kMaxTokens = 64;    // tokens per block
 struct E4M3 {
     uint8_t code;
 };
+struct E4M3Blocks {   // with block scales (gather; such a cache is written by block_append_kernel)
+    uint8_t code;
+};
 
 // BYTES consecutive bytes in registers
 template <int BYTES>
@@ -206,6 +209,7 @@ template <typename Rows, typename Cache, int VEC, bool APPEND>
 __global__ void __launch_bounds__(kThreads, APPEND ? 5 : 4) cache_rows_kernel(CacheRowsArgs a, int tokens_per_block) {
     using Src = std::conditional_t<APPEND, Rows, Cache>;
     using Dst = std::conditional_t<APPEND, Cache, Rows>;
+    constexpr bool kBlocks = std::is_same_v<Cache, E4M3Blocks>;
     constexpr int kSrc = VEC * (int)sizeof(Src), kDst = VEC * (int)sizeof(Dst);
     constexpr int kUnroll = VEC == 1 ? 4 : std::min(8, std::max(2, (APPEND ? 64 : 128) / kSrc));
     __shared__ long long where[kMaxTokens];
@@ -226,6 +230,7 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 5 : 4) cache_rows_kernel(Ca
         const bool plain = plain_scale(scale);
         for (int t0 = threadIdx.y; t0 < n || !located; t0 += kUnroll * blockDim.y) {
             Raw<kSrc> src[kUnroll];
+            float block_scale[kBlocks ? kUnroll : 1];
             if (APPEND) {
 #pragma unroll
                 for (int k = 0; k < kUnroll; ++k)
@@ -244,6 +249,8 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 5 : 4) cache_rows_kernel(Ca
 #pragma unroll
                     for (int j = 0; j < (kSrc + 3) / 4; ++j) src[k].w[j] = 0u;   // a refused row reads as zeros
                     if (w >= 0) load_raw<kSrc>(src[k], cache + w * p.row_width);
+                    if constexpr (kBlocks)
+                        block_scale[k] = w >= 0 ? __ldg(p.scales + ((w + (long long)h * a.page_size) >> a.scale_shift)) : 0.f;
                 }
             }
 #pragma unroll
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, APPEND ? 5 : 4) cache_rows_kernel(Ca
                     if constexpr (sizeof(Cache) == 1) {
                         if (!APPEND) {
 #pragma unroll
-                            for (int j = 0; j < VEC; ++j) x[j] *= scale;
+                            for (int j = 0; j < VEC; ++j) x[j] *= kBlocks ? block_scale[kBlocks ? k : 0] : scale;
                         } else if (plain) {
 #pragma unroll
                             for (int j = 0; j < VEC; ++j) x[j] = quotient(x[j], scale, inv);
@@ -338,6 +345,10 @@ cudaError_t launch_kv_append(const CacheRowsArgs& a, int cache_kind, int rows_f3
 }
 
 cudaError_t launch_kv_gather(const CacheRowsArgs& a, int cache_kind, int rows_f32, cudaStream_t s) {
+    if (cache_kind == 3) {
+        if (a.rows <= 0) return cudaSuccess;
+        return rows_f32 ? launch_rows<float, E4M3Blocks, false>(a, s) : launch_rows<__nv_bfloat16, E4M3Blocks, false>(a, s);
+    }
     return launch_any<false>(a, cache_kind, rows_f32, s);
 }
 

@@ -218,7 +218,118 @@ __global__ void __launch_bounds__(256) chunk_value_convert_kernel(KernelArgs a) 
     if (bad_page) set_error(a.err, ERR_DEVICE_CHECK | SITE_PAGE_RANGE);
 }
 
-template <int D>
+// two E4M3 codes in the low 16 bits -> f16 pair (low code in the low half); exact
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(w));
+    return d;
+}
+
+// The same for E4M3 caches with block scales: bf16 key codes (every E4M3 value is a bf16 and an
+// f16 number, so no product is rounded before its scale), f16 value codes, and a scale
+// for every 16 tokens and head, of keys times the score scale.  Slots past a request's last key hold zeros,
+// and so do the scales of 16 such slots.  Bound by HBM: 2 bytes read, 4 written per key-value pair of elements.
+__global__ void __launch_bounds__(256) chunk_block_convert_kernel(KernelArgs a) {
+    constexpr int U = 2;
+    const int P = a.page_size, H = a.num_kv_heads;
+    const int c16 = a.head_dim_v / 16;                                 // pieces of 16 codes per row
+    const int per_page = H * P * c16, units = H * (P / 16);
+    bool bad_page = false;
+    for (int slot = blockIdx.x; slot < a.num_vh_pages; slot += gridDim.x) {
+        const VhPage vp = a.vh_pages[slot];
+        const ReqDesc r = a.reqs[vp.b];
+        const int rows = r.seq_len - vp.j * P;                         // keys of the page in use
+        const int phys = a.page_table[r.page_row + vp.j];
+        const bool ok = phys >= 0 && phys < a.num_pages;
+        if (!ok && rows > 0) bad_page = true;
+        const size_t from = (size_t)(ok ? phys : 0) * per_page, to = (size_t)slot * per_page;
+        for (int i = threadIdx.x; i < units; i += blockDim.x) {
+            const int t = i % (P / 16) * 16;                           // first slot of the unit
+            const size_t at = (((size_t)(ok ? phys : 0) * H + i / (P / 16)) * P + t) >> a.scale_shift;
+            const bool used = ok && t < rows;
+            const_cast<float*>(a.k_unit)[(size_t)slot * units + i] = used ? a.k_scales[at] * a.scale_log2 : 0.f;
+            const_cast<float*>(a.v_unit)[(size_t)slot * units + i] = used ? a.v_scales[at] : 0.f;
+        }
+        for (int i0 = threadIdx.x; i0 < per_page; i0 += U * blockDim.x) {
+            uint4 k[U], v[U];
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                const int idx = i0 + x * blockDim.x;
+                k[x] = v[x] = make_uint4(0u, 0u, 0u, 0u);
+                if (idx < per_page && ok && (idx / c16) % P < rows) {
+                    k[x] = __ldcs((const uint4*)a.k_cache + from + idx);
+                    v[x] = __ldcs((const uint4*)a.v_cache + from + idx);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < U; ++x) {
+                const int idx = i0 + x * blockDim.x;
+                if (idx >= per_page) continue;
+                const uint32_t kw[4] = {k[x].x, k[x].y, k[x].z, k[x].w}, vw[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                uint32_t kb[8], vh[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t kh = e4m3x2_to_f16x2(kw[j / 2] >> (16 * (j & 1)));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&kh));
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+                    kb[j] = *reinterpret_cast<const uint32_t*>(&b);
+                    vh[j] = e4m3x2_to_f16x2(vw[j / 2] >> (16 * (j & 1)));
+                }
+                uint4* kd = (uint4*)a.k_half + 2 * (to + idx);
+                uint4* vd = (uint4*)a.v_half + 2 * (to + idx);
+                kd[0] = make_uint4(kb[0], kb[1], kb[2], kb[3]);
+                kd[1] = make_uint4(kb[4], kb[5], kb[6], kb[7]);
+                vd[0] = make_uint4(vh[0], vh[1], vh[2], vh[3]);
+                vd[1] = make_uint4(vh[4], vh[5], vh[6], vh[7]);
+            }
+        }
+    }
+    if (bad_page) set_error(a.err, ERR_DEVICE_CHECK | SITE_PAGE_RANGE);
+}
+
+// the largest raw score of each 16 of a unit's 64 keys (keys j < valid when MASK)
+template <bool MASK>
+__device__ __forceinline__ void row_max16(const uint32_t (&sr)[64], int valid, float (&mx)[4]) {
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        mx[h] = -INFINITY;
+#pragma unroll
+        for (int j = 16 * h; j < 16 * h + 16; ++j)
+            if (!MASK || j < valid) mx[h] = fmaxf(mx[h], __uint_as_float(sr[j]));
+    }
+}
+
+// write_p16 with block scales: P = 2^(s c[h] - base) is summed, P f[h] is written
+template <bool MASK>
+__device__ __forceinline__ float write_p16_blocks(const uint32_t (&sr)[64], const float (&c)[4], const float (&f)[4], float base,
+                                                  int key0, int limit, uint32_t pcol) {
+    float part[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        uint32_t pk[8];
+        part[h] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int j = 16 * h + 2 * e;
+            float x0 = ex2_ftz(fmaf(__uint_as_float(sr[j]), c[h], -base));
+            float x1 = ex2_ftz(fmaf(__uint_as_float(sr[j + 1]), c[h], -base));
+            if (MASK) {
+                if (key0 + j > limit) x0 = 0.f;
+                if (key0 + j + 1 > limit) x1 = 0.f;
+            }
+            part[h] += x0 + x1;
+            __half2 p2 = __floats2half2_rn(x0 * f[h], x1 * f[h]);
+            pk[e] = *reinterpret_cast<uint32_t*>(&p2);
+        }
+        SKV_ST8(pcol + 8 * h, pk);
+    }
+    return (part[0] + part[1]) + (part[2] + part[3]);
+}
+
+// BS: block scales.  Keys and values are the copies' codes; a score takes its key's scale in place
+// of the score scale, a weight its value's scale before it is rounded to f16, under a
+// running maximum of its own as in the decode engine (mv, the units of O; raised lazily, as m is).
+template <int D, bool BS>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                 const __grid_constant__ CUtensorMap tmap_v, KernelArgs a) {
@@ -338,7 +449,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         }
                     }
                     const int key0 = ct.kb + u * kKeys;
-                    const int phys = a.page_table[ct.r.page_row + key0 / a.page_size];
+                    // (block scales: both operands are the copies', whose pages were checked)
+                    const int phys = BS ? 0 : a.page_table[ct.r.page_row + key0 / a.page_size];
                     const uint32_t full = smem_u32(&B.stage_full[s]);
                     last_par = (last_par & ~(1u << s)) | ((round & 1u) << s);
                     if (phys < 0 || phys >= a.num_pages) {
@@ -354,7 +466,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                                        key0 % a.page_size;
                         unsigned char* st = sStage + s * C::STAGE_BYTES;
                         for (int j = 0; j < C::BOXES; ++j) {
-                            tma_2d(smem_u32(st + j * C::KV_BOX), &tmap_k, 64 * j, y, full);
+                            tma_2d(smem_u32(st + j * C::KV_BOX), &tmap_k, 64 * j, BS ? yv : y, full);
                             tma_2d(smem_u32(st + C::TILE_BYTES + j * C::KV_BOX), &tmap_v, 64 * j, yv, full);
                         }
                     }
@@ -496,7 +608,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             const size_t st = (size_t)ct.r.state_base + ((size_t)i * a.num_q_heads + h) * ct.r.n_splits + ct.split;
             const bool direct = fused && ct.r.n_splits == 1;   // write the final output
             float m = -INFINITY, l = 0.f;
+            [[maybe_unused]] float mv = -INFINITY;
+            // block scales of unit u, read a unit ahead
+            [[maybe_unused]] float4 kn = make_float4(0.f, 0.f, 0.f, 0.f), vn = kn;
+            auto read_scales = [&](int u) {
+                if constexpr (BS) {
+                    const int key0 = ct.kb + u * kKeys, per = a.page_size / 16;
+                    const size_t at = ((size_t)(ct.r.vh_base + key0 / a.page_size) * a.num_kv_heads + ct.kv) * per +
+                                      key0 % a.page_size / 16;
+                    kn = *(const float4*)(a.k_unit + at);
+                    vn = *(const float4*)(a.v_unit + at);
+                }
+            };
+            if (nu > 0) read_scales(0);
             for (int u = 0; u < nu; ++u) {
+                [[maybe_unused]] const float kc[4] = {kn.x, kn.y, kn.z, kn.w}, vc[4] = {vn.x, vn.y, vn.z, vn.w};
+                if (BS && u + 1 < nu) read_scales(u + 1);
                 const uint32_t gi = sn;       // this tile's unit index: S/P buffer gi & 1
                 const int b2 = (int)(gi & 1);
                 if (!warp_wait(smem_u32(&B.s_full[t][b2]), (gi >> 1) & 1, abort_flag, lane)) { give_up(SITE_FULL_WAIT); ok = false; break; }
@@ -511,8 +638,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 // the P stores below are warp-collective tensor-memory instructions
                 const bool unmasked = __all_sync(0xffffffffu, key0 + kKeys - 1 <= limit);
                 // row max of the raw scores (the scale, > 0 on this path, is applied after)
-                const float mxr = unmasked ? row_max64<false>(sr, 64) : row_max64<true>(sr, limit - key0 + 1);
-                const float mx = mxr * c2;
+                float mx, my = -INFINITY;
+                if constexpr (BS) {
+                    float mxr[4];
+                    if (unmasked) row_max16<false>(sr, 64, mxr); else row_max16<true>(sr, limit - key0 + 1, mxr);
+                    mx = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float x = mxr[h] * kc[h];   // (-inf * 0, no key: NaN, which fmaxf passes over)
+                        mx = fmaxf(mx, x);
+                        my = fmaxf(my, x + (float)((int)(__float_as_uint(vc[h]) >> 23) - 126));   // 2^.. > v
+                    }
+                } else {
+                    const float mxr = unmasked ? row_max64<false>(sr, 64) : row_max64<true>(sr, limit - key0 + 1);
+                    mx = mxr * c2;
+                }
                 // lazy rescale: a row whose max grew by more than 2^8 rescales its O and l.
                 // The tensor-memory loads and stores are warp-collective, so the whole warp
                 // takes the branch when any of its rows needs it (scale 1 for the others),
@@ -522,6 +662,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 bool need = false;
                 if (m == -INFINITY) {
                     m = mx;
+                    mv = my;
+                } else if (BS) {
+                    if (mx > m + kRescaleThreshold) {
+                        l *= exp2f(m - mx);
+                        m = mx;
+                    }
+                    if (my > mv + kRescaleThreshold) {
+                        scale_o = exp2f(mv - my);
+                        mv = my;
+                        need = true;
+                    }
                 } else if (mx > m + kRescaleThreshold) {
                     scale_o = exp2f(m - mx);
                     m = mx;
@@ -539,7 +690,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         }
                         tc_fence_after();
                     }
-                    l *= scale_o;
+                    if (!BS) l *= scale_o;
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         SKV_LD32(lane_addr + c, o);
@@ -553,8 +704,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 // issued before S of this unit and so already done
                 const float base = (m == -INFINITY) ? 0.f : m;
                 const uint32_t pcol = lane_addr + kColS + kKeys * b2;
-                l += unmasked ? write_p16<false>(sr, c2, base, key0, limit, pcol)
-                              : write_p16<true>(sr, c2, base, key0, limit, pcol);
+                if constexpr (BS) {
+                    // from units of 2^m to 2^mv (at most 2^107 apart where a value's scale is not 0)
+                    const float to = exp2f(fminf(base - (mv == -INFINITY ? 0.f : mv), 126.f));
+                    const float f[4] = {vc[0] * to, vc[1] * to, vc[2] * to, vc[3] * to};
+                    l += unmasked ? write_p16_blocks<false>(sr, kc, f, base, key0, limit, pcol)
+                                  : write_p16_blocks<true>(sr, kc, f, base, key0, limit, pcol);
+                } else {
+                    l += unmasked ? write_p16<false>(sr, c2, base, key0, limit, pcol)
+                                  : write_p16<true>(sr, c2, base, key0, limit, pcol);
+                }
                 tc_wait_st();
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 tc_fence_before();
@@ -571,7 +730,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 tc_fence_after();
             }
             const bool empty_row = !(l > 0.f);
-            const float inv = empty_row ? 0.f : 1.f / l;
+            const float inv = empty_row ? 0.f : BS ? exp2f(mv - m) / l : 1.f / l;
             const float lse = empty_row ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -669,7 +828,7 @@ cudaError_t make_map(CUtensorMap* m, const void* base, int rank, const cuuint64_
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D>
+template <int D, bool BS>
 cudaError_t launch_d(const KernelArgs& a, long long total_q, int num_pages_total, cudaStream_t s) {
     const int g = a.group;
     // Q as [total_q][Hq][D]: one box = 128 / g tokens x the g heads of a KV head x 64 columns
@@ -677,14 +836,14 @@ cudaError_t launch_d(const KernelArgs& a, long long total_q, int num_pages_total
     cuuint64_t qs[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.num_q_heads * D * 2};
     cuuint32_t qb[3] = {64, (cuuint32_t)g, (cuuint32_t)(kRows / g)};
     // K, V as [num_pages * Hkv * P][D]: one box = 64 keys x 64 columns
-    const long long kvrows = (long long)num_pages_total * a.num_kv_heads * a.page_size;
+    const long long kvrows = (long long)(BS ? a.num_vh_pages : num_pages_total) * a.num_kv_heads * a.page_size;
     cuuint64_t kd[2] = {(cuuint64_t)D, (cuuint64_t)kvrows};
     cuuint64_t ks[1] = {(cuuint64_t)D * 2};
     cuuint32_t kb[2] = {64, (cuuint32_t)kKeys};
     CUtensorMap mq, mk, mv;
     cudaError_t e = make_map(&mq, a.q, 3, qd, qs, qb);
     if (e != cudaSuccess) return e;
-    if ((e = make_map(&mk, a.k_cache, 2, kd, ks, kb)) != cudaSuccess) return e;
+    if ((e = make_map(&mk, BS ? a.k_half : a.k_cache, 2, kd, ks, kb)) != cudaSuccess) return e;
     // V: the f16 copy, [slot * Hkv * P][D]
     cuuint64_t vd[2] = {(cuuint64_t)D, (cuuint64_t)a.num_vh_pages * a.num_kv_heads * a.page_size};
     if ((e = make_map(&mv, a.v_half, 2, vd, ks, kb, CU_TENSOR_MAP_DATA_TYPE_FLOAT16)) != cudaSuccess) return e;
@@ -692,7 +851,7 @@ cudaError_t launch_d(const KernelArgs& a, long long total_q, int num_pages_total
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [&]() {
-        attr_err = cudaFuncSetAttribute(chunk_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        attr_err = cudaFuncSetAttribute(chunk_tc_kernel<D, BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     });
     if (attr_err != cudaSuccess) return attr_err;
     int dev = 0, sms = 0;
@@ -701,7 +860,7 @@ cudaError_t launch_d(const KernelArgs& a, long long total_q, int num_pages_total
     const int grid = std::min(a.max_ctas > 0 ? std::min(sms, a.max_ctas) : sms, a.num_tasks);
     {
         ProfileScope ps(SPLITKV_KERNEL_CHUNK, s);
-        chunk_tc_kernel<D><<<grid, kThreads, smem, s>>>(mq, mk, mv, a);
+        chunk_tc_kernel<D, BS><<<grid, kThreads, smem, s>>>(mq, mk, mv, a);
     }
     return cudaGetLastError();
 }
@@ -729,6 +888,22 @@ cudaError_t launch_chunk_value_convert(const KernelArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+cudaError_t launch_chunk_block_convert(const KernelArgs& a, cudaStream_t s) {
+    if (a.num_vh_pages <= 0) return cudaSuccess;
+    if ((((uintptr_t)a.k_cache) & 15) || (((uintptr_t)a.v_cache) & 15) || (a.head_dim_v % 16) || (a.page_size % 64))
+        return cudaErrorMisalignedAddress;
+    int dev = 0, sms = 0;
+    cudaError_t e;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    const int blocks = std::min(sms * 8, a.num_vh_pages);   // one slot per CTA at a time
+    {
+        ProfileScope ps(SPLITKV_KERNEL_CHUNK_VCONV, s);
+        chunk_block_convert_kernel<<<blocks, 256, 0, s>>>(a);
+    }
+    return cudaGetLastError();
+}
+
 cudaError_t launch_chunk_partial(const KernelArgs& a, long long total_q, int num_pages_total, cudaStream_t s) {
     if (a.num_tasks <= 0) return cudaSuccess;
     if (!a.v_half || a.num_vh_pages <= 0) return cudaErrorInvalidValue;
@@ -736,8 +911,13 @@ cudaError_t launch_chunk_partial(const KernelArgs& a, long long total_q, int num
         return cudaErrorMisalignedAddress;
     if ((long long)num_pages_total * a.num_kv_heads * a.page_size >= (1LL << 31) || total_q >= (1LL << 31))
         return cudaErrorInvalidValue;
-    if (a.head_dim_qk == 128) return launch_d<128>(a, total_q, num_pages_total, s);
-    if (a.head_dim_qk == 64) return launch_d<64>(a, total_q, num_pages_total, s);
+    if ((long long)a.num_vh_pages * a.num_kv_heads * a.page_size >= (1LL << 31)) return cudaErrorInvalidValue;
+    if (a.kv_fp8 == 2) {
+        if (a.head_dim_qk != 128) return cudaErrorNotSupported;
+        return launch_d<128, true>(a, total_q, num_pages_total, s);
+    }
+    if (a.head_dim_qk == 128) return launch_d<128, false>(a, total_q, num_pages_total, s);
+    if (a.head_dim_qk == 64) return launch_d<64, false>(a, total_q, num_pages_total, s);
     return cudaErrorNotSupported;
 }
 

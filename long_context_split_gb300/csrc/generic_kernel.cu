@@ -285,6 +285,7 @@ generic_partial_kernel(KernelArgs a, int max_keys) {
             float s = -INFINITY;
             // element offset of key j's value row (STAGED: the dense slot's row in shared memory)
             size_t row_off = 0;
+            float v_scale = 1.f;   // of the key's block (block scales; one per tensor: folded in at the end)
             if (has_key(c0)) {
                 if (page < 0 || page >= a.num_pages) {
                     set_error(a.err, ERR_DEVICE_CHECK | SITE_PAGE_RANGE);
@@ -298,6 +299,13 @@ generic_partial_kernel(KernelArgs a, int max_keys) {
                                     : (((size_t)page * a.num_kv_heads + t.kv_head) * P + off) * Dqk;
                     s = dot_row(q_s, kc + row_off, Dqk) * a.scale_log2;
                 }
+                if constexpr (sizeof(TKV) == 1) {
+                    if (a.k_scales && page >= 0 && page < a.num_pages) {
+                        const size_t at = (((size_t)page * a.num_kv_heads + t.kv_head) * P + j % P) >> a.scale_shift;
+                        s *= a.k_scales[at];
+                        v_scale = a.v_scales[at];
+                    }
+                }
             }
             const float cmax = warp_max(s);
             const float m_new = fmaxf(m, cmax);
@@ -305,6 +313,7 @@ generic_partial_kernel(KernelArgs a, int max_keys) {
             const float alpha = exp2f(m - base);
             const float p = exp2f(s - base);
             l = l * alpha + warp_sum(p);
+            const float pv = sizeof(TKV) == 1 ? p * v_scale : p;   // (v_scale 1 for a key of weight 0)
 #pragma unroll
             for (int c = 0; c < DVL; ++c) acc[c] *= alpha;
             // p_j v_j over the chunk's keys, U keys at a time so that their value loads are in
@@ -319,7 +328,7 @@ generic_partial_kernel(KernelArgs a, int max_keys) {
                 float pj[U], vv[U][DVL];
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
-                    pj[k] = __shfl_sync(0xffffffffu, p, jj + k);
+                    pj[k] = __shfl_sync(0xffffffffu, pv, jj + k);
                     const size_t vo = __shfl_sync(0xffffffffu, row_off, jj + k);
 #pragma unroll
                     for (int c = 0; c < DVL; ++c) vv[k][c] = pj[k] != 0.f ? load_elem(vbase, vo + lane + 32 * c) : 0.f;
@@ -330,7 +339,7 @@ generic_partial_kernel(KernelArgs a, int max_keys) {
                     for (int c = 0; c < DVL; ++c) acc[c] = fmaf(pj[k], vv[k][c], acc[c]);
             }
             for (; jj < cnt; ++jj) {
-                const float pj = __shfl_sync(0xffffffffu, p, jj);
+                const float pj = __shfl_sync(0xffffffffu, pv, jj);
                 const size_t vo = __shfl_sync(0xffffffffu, row_off, jj);
                 if (pj != 0.f) {
 #pragma unroll

@@ -47,6 +47,14 @@
 // tile, put back in order when a warp hands its output over.  P enters the
 // f16 product whole (11 significant bits; the bf16 path needs a residual).  The key scale is
 // folded into the score scale, the value scale into the final normalisation.
+// Block scales (Cfg::BS; a scale for each block of 16 to 128 tokens and KV head):
+// the producer's lanes copy the stage's scales beside its codes (4-byte cp.async that
+// arrive on the same barrier).  A score takes its key's scale where it took the score
+// scale.  A weight p = 2^(s - m) meets its value's scale v in float32; since scales may
+// differ by any factor, the product is kept relative to a maximum of its own, mv =
+// max(s + e) with 2^e the power of two above v: w = p v 2^(m - mv) <= 1 is what is rounded
+// to f16, and the output accumulates in units of 2^mv (taken back to 2^m where the
+// warps' states are combined), while the sum of weights stays in units of 2^m.
 // Every wait is bounded (globaltimer); on expiry the kernel records an error
 // word, stops, waits for its own copies in flight and returns.
 #include <cuda.h>
@@ -232,13 +240,14 @@ __device__ __forceinline__ void set_error(int32_t* err, int32_t code) { atomicCA
 // ---------------------------------------------------------------------------
 constexpr size_t kSmemLimit = 232448;                    // 227 KB per CTA on sm_103
 
-template <int D_, int P_, int S_, bool F8_ = false, bool T8_ = false>
+template <int D_, int P_, int S_, bool F8_ = false, bool T8_ = false, bool BS_ = false>
 struct Cfg {
     static constexpr int D = D_;
     static constexpr int P = P_;
     static constexpr int S = S_;                         // pages per stage
     static constexpr bool F8 = F8_;                      // E4M3 K/V codes
     static constexpr bool T8 = T8_;                      // every task holds at most 8 rows: transposed products
+    static constexpr bool BS = BS_;                      // E4M3 codes under block scales
     static constexpr int EB = F8 ? 1 : 2;                // bytes per cached element
     static constexpr int T = P * S;                      // keys per stage
     static constexpr int NWC = (P == 16) ? 1 : 4;        // consumer warps
@@ -253,7 +262,10 @@ struct Cfg {
     static constexpr int KT = D / 16;                    // QK k-steps
     static constexpr size_t COMB_BYTES = (size_t)NWC * 16 * D * 4;
     // as many stages as shared memory holds (each also needs a header and two barriers)
-    static constexpr int NSTAGE_FIT = (int)((kSmemLimit - 1024 - COMB_BYTES - 1024) / (STAGE_BYTES + 112));
+    static constexpr int BLOCKS = BS ? T / 16 : 1;       // block scales of a stage, keys and values each
+    static constexpr int FULL_COUNT = BS ? 33 : 1;       // arrivals of a full stage: the copies', and each lane's scales
+    static constexpr int NSTAGE_FIT =
+        (int)((kSmemLimit - 1024 - COMB_BYTES - 1024) / (STAGE_BYTES + 112 + (BS ? 8 * BLOCKS : 0)));
     static constexpr int NSTAGE = NSTAGE_FIT < 16 ? NSTAGE_FIT : 16;
     static constexpr size_t STAGES_BYTES = (size_t)NSTAGE * STAGE_BYTES;
     // roles: warp 0 producer, 1..NWC consumers, NWC+1 scheduler, NWC+2 finaliser
@@ -267,6 +279,7 @@ struct Cfg {
     static_assert(32 % S == 0, "stages do not straddle the producer's 32-page id chunks");
     static_assert(!F8 || (D == 128 && KPW % 32 == 0), "E4M3 path: one 128-byte row per key, 32-key groups per warp");
     static_assert(!(T8 && F8), "transposed products: bf16 caches");
+    static_assert(!BS || (F8 && S * (P / 16) <= 16), "block scales: E4M3 codes, a scale of keys and of values per lane pair");
     static_assert(NSTAGE >= 2, "stage ring");
 };
 
@@ -306,6 +319,8 @@ struct SmemExtra {
     int fin_task;                                // its queue index
     float comb_m[C::NWC][16];
     float comb_l[C::NWC][16];
+    float comb_mv[C::NWC][C::BS ? 16 : 1];       // block scales: the outputs' own units
+    float scales[C::BS ? C::NSTAGE : 1][2][C::BLOCKS];   // a stage's key and value scales, in key order
     int fin_end;
     int exit_last;
     int abort_flag;
@@ -672,6 +687,139 @@ __device__ __forceinline__ void attend_keys_f8(uint32_t kbase, int kw0, int key_
     }
 }
 
+// The same with block scales: ks, vs hold the scales of the warp's 16-key groups, mv0 and mv1
+// are the units of o (see the file comment).
+template <class C, bool MASK>
+__device__ __forceinline__ void attend_keys_bs(uint32_t kbase, int kw0, int key_page, int key_end, int lim0, int lim1,
+                                               float scale_log2, const float* ks, const float* vs, int first, int shift,
+                                               const uint32_t (&qa)[C::KT][4], float (&o)[C::DT][4], float& m0, float& m1,
+                                               float& mv0, float& mv1, float& l0, float& l1, int lane) {
+    constexpr int NB = C::KPW / 16;
+    const uint32_t vbase = kbase + C::TILE_BYTES;
+    const int qc = (lane & 3) * 2;
+    float s[C::NT][4];
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < C::KT; ++kk) {
+#pragma unroll
+        for (int g = 0; g < C::KPW / 32; ++g) {
+            const int key = kw0 + 32 * g + 8 * (lane >> 3) + (lane & 7);
+            uint32_t r[4];
+            ldsm_x4(kbase + key * 128 + ((kk ^ (key & 7)) << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                mma_f16h(s[4 * g + n], qa[kk], e4m3x2_lo_to_f16x2(r[n]), e4m3x2_hi_to_f16x2(r[n]));
+        }
+    }
+    const int key0 = key_page + kw0;
+    float mx0 = -INFINITY, mx1 = -INFINITY, my0 = -INFINITY, my1 = -INFINITY;
+    float vsc[NB];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        const float f = ks[(first + 16 * j) >> shift] * scale_log2;
+        vsc[j] = vs[(first + 16 * j) >> shift];
+        float b0 = -INFINITY, b1 = -INFINITY;
+#pragma unroll
+        for (int n = 2 * j; n < 2 * j + 2; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v0 = s[n][e] * f;
+                float v1 = s[n][2 + e] * f;
+                if (MASK) {
+                    const int kidx = key0 + n * 8 + qc + e;
+                    if (kidx > lim0 || kidx >= key_end) v0 = -INFINITY;
+                    if (kidx > lim1 || kidx >= key_end) v1 = -INFINITY;
+                }
+                s[n][e] = v0;
+                s[n][2 + e] = v1;
+                b0 = fmaxf(b0, v0);
+                b1 = fmaxf(b1, v1);
+            }
+        }
+        // a block that no visible key lies in may have any scale
+        if (MASK && key0 + 16 * j >= key_end) vsc[j] = 0.f;
+        const float up = (float)((int)((__float_as_uint(vsc[j]) >> 23) & 255u) - 126);   // 2^up > |v|
+        mx0 = fmaxf(mx0, b0);
+        mx1 = fmaxf(mx1, b1);
+        my0 = fmaxf(my0, b0 + up);
+        my1 = fmaxf(my1, b1 + up);
+    }
+#pragma unroll
+    for (int x = 1; x < 4; x <<= 1) {
+        mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
+        mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
+        my0 = fmaxf(my0, __shfl_xor_sync(0xffffffffu, my0, x));
+        my1 = fmaxf(my1, __shfl_xor_sync(0xffffffffu, my1, x));
+    }
+    const float mn0 = fmaxf(m0, mx0), mn1 = fmaxf(m1, mx1);
+    const float nv0 = fmaxf(mv0, my0), nv1 = fmaxf(mv1, my1);
+    const float b0s = (mn0 == -INFINITY) ? 0.f : mn0;
+    const float b1s = (mn1 == -INFINITY) ? 0.f : mn1;
+    const float c0s = (nv0 == -INFINITY) ? 0.f : nv0;
+    const float c1s = (nv1 == -INFINITY) ? 0.f : nv1;
+    const float al0 = exp2f(m0 - b0s), al1 = exp2f(m1 - b1s);
+    const float av0 = exp2f(mv0 - c0s), av1 = exp2f(mv1 - c1s);
+    const float to0 = exp2f(b0s - c0s), to1 = exp2f(b1s - c1s);   // from units of 2^m to 2^mv
+    float ps0 = 0.f, ps1 = 0.f;
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) {
+        s[n][0] = ex2_approx(s[n][0] - b0s);
+        s[n][1] = ex2_approx(s[n][1] - b0s);
+        s[n][2] = ex2_approx(s[n][2] - b1s);
+        s[n][3] = ex2_approx(s[n][3] - b1s);
+        ps0 += s[n][0] + s[n][1];
+        ps1 += s[n][2] + s[n][3];
+    }
+    l0 = l0 * al0 + ps0;
+    l1 = l1 * al1 + ps1;
+    m0 = mn0;
+    m1 = mn1;
+    mv0 = nv0;
+    mv1 = nv1;
+#pragma unroll
+    for (int n = 0; n < C::DT; ++n) {
+        o[n][0] *= av0;
+        o[n][1] *= av0;
+        o[n][2] *= av1;
+        o[n][3] *= av1;
+    }
+#pragma unroll
+    for (int j = 0; j < C::KSTEP_PV; ++j) {
+        const float f0 = vsc[j] * to0, f1 = vsc[j] * to1;
+        uint32_t ph[4];
+        ph[0] = pack_f16(s[2 * j][0] * f0, s[2 * j][1] * f0);
+        ph[1] = pack_f16(s[2 * j][2] * f1, s[2 * j][3] * f1);
+        ph[2] = pack_f16(s[2 * j + 1][0] * f0, s[2 * j + 1][1] * f0);
+        ph[3] = pack_f16(s[2 * j + 1][2] * f1, s[2 * j + 1][3] * f1);
+        const int mi = lane >> 3;
+        const int key = kw0 + j * 16 + ((mi & 1) << 3) + (lane & 7);
+        const int ka = key0 + j * 16 + 2 * (lane & 3);
+#pragma unroll
+        for (int G = 0; G < C::D / 32; ++G) {
+            const int chunk = 2 * G + (mi >> 1);
+            uint32_t r[4];
+            ldsm_x4_t(vbase + key * 128 + ((chunk ^ (key & 7)) << 4), r[0], r[1], r[2], r[3]);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const uint32_t pa = interleave_bytes(r[2 * c]);
+                const uint32_t pb = interleave_bytes(r[2 * c + 1]);
+                uint32_t e0 = e4m3x2_lo_to_f16x2(pa), e1 = e4m3x2_lo_to_f16x2(pb);
+                uint32_t d0 = e4m3x2_hi_to_f16x2(pa), d1 = e4m3x2_hi_to_f16x2(pb);
+                if (MASK) {
+                    e0 = keep_keys(e0, ka, key_end);
+                    d0 = keep_keys(d0, ka, key_end);
+                    e1 = keep_keys(e1, ka + 8, key_end);
+                    d1 = keep_keys(d1, ka + 8, key_end);
+                }
+                const int te = 2 * (2 * G + c);
+                mma_f16h(o[te], ph, e0, e1);
+                mma_f16h(o[te + 1], ph, d0, d1);
+            }
+        }
+    }
+}
+
 // Wait (bounded) for a phase: when every lane's first test finds it complete the warp
 // goes on at once; otherwise lane 0 waits, broadcasts the outcome, and every lane
 // gets acquire ordering with one more test of the completed phase (it cannot move on
@@ -811,7 +959,7 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::NSTAGE; ++s) {
-            mbar_init(smem_u32(&X.full[s]), 1);
+            mbar_init(smem_u32(&X.full[s]), C::FULL_COUNT);
             mbar_init(smem_u32(&X.empty[s]), C::NWC);
         }
         mbar_init(smem_u32(&X.sched_req), 1);
@@ -839,6 +987,11 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
             return warp_wait(smem_u32(&X.empty[stage]), ((item / C::NSTAGE) & 1) ^ 1, abort_flag, a.err,
                              SITE_EMPTY_WAIT, lane);
         };
+        // block scales: every lane's own arrival on a full stage, once its copies (if any) have landed
+        auto arrive_scales = [&](int stage) {
+            if constexpr (C::BS)
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&X.full[stage])) : "memory");
+        };
         if (lane == 0) mbar_arrive(smem_u32(&X.sched_req));
         while (!stop) {
             if (!warp_wait(smem_u32(&X.sched_ready), nslot & 1, abort_flag, a.err, SITE_FULL_WAIT, lane)) break;
@@ -852,6 +1005,7 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     had_tma &= ~(1u << stage);
                     mbar_arrive(smem_u32(&X.full[stage]));
                 }
+                arrive_scales(stage);
                 ++item;
                 break;
             }
@@ -876,6 +1030,7 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     had_tma &= ~(1u << stage);
                     mbar_arrive(smem_u32(&X.full[stage]));
                 }
+                arrive_scales(stage);
                 ++item;
                 continue;
             }
@@ -895,6 +1050,21 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     for (int u = 0; u < C::S; ++u) phys[u] = __shfl_sync(0xffffffffu, pid, min(j + u, 31));
                     int stage;
                     if (!acquire(stage)) { stop = true; break; }
+                    if constexpr (C::BS) {
+                        // lanes 0..15 take the stage's key scales, 16..31 its value scales: entry i is
+                        // block i % nb of the stage's page i / nb
+                        const int i = lane & 15, nb = C::P >> a.scale_shift, u = i / nb;
+                        const int page = __shfl_sync(0xffffffffu, pid, min(j + u, 31));
+                        if (u < np && page >= 0 && page < a.num_pages) {
+                            const float* src = (lane < 16 ? a.k_scales : a.v_scales) +
+                                               ((size_t)page * a.num_kv_heads + t.kv_head) * nb + i % nb;
+                            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                                             smem_u32(&X.scales[stage][lane >> 4][i])),
+                                         "l"(src)
+                                         : "memory");
+                        }
+                        arrive_scales(stage);
+                    }
                     if (lane == 0) {
                         StageHdr& hd = X.hdr[stage];
                         hd.t = t;
@@ -941,6 +1111,7 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 pid = pid_next;
             }
         }
+        if constexpr (C::BS) asm volatile("cp.async.wait_all;" ::: "memory");
         // make sure no copy issued by this CTA is still landing in shared memory
         if (lane == 0) {
             for (int s = 0; s < C::NSTAGE; ++s) {
@@ -1020,6 +1191,12 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                 }
                 const bool empty = !(L > 0.f);
                 const float inv = empty ? 0.f : a.v_scale / L;   // (E4M3 values: times their scale)
+                if constexpr (C::BS) {
+                    // the outputs' units: 2^mv of each warp, not 2^m
+#pragma unroll
+                    for (int u = 0; u < C::NWC; ++u)
+                        if (u < nsrc && M != -INFINITY) f[u] = exp2f(X.comb_mv[src0 + u][sr] - M);
+                }
                 const float lse = empty ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
                 const int row = t.row_begin + rr;
                 const int i = row / g;
@@ -1081,6 +1258,7 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         uint32_t qa[C::KT][4];
         float o[C::DT][4];
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        [[maybe_unused]] float mv0 = -INFINITY, mv1 = -INFINITY;   // block scales: the units of o
         int lim0 = 0, lim1 = 0;          // last key index visible to rows qr, qr + 8
         uint32_t item = 0, nfin = 0;
         while (true) {
@@ -1166,6 +1344,7 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 #pragma unroll
                 for (int n = 0; n < C::DT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
                 m0 = m1 = -INFINITY;
+                mv0 = mv1 = -INFINITY;
                 l0 = l1 = 0.f;
             }
             if (!(flags & F_EMPTY)) {
@@ -1178,7 +1357,15 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     const uint32_t kbase = smem_u32(sbase + (size_t)u * C::PAGE_BYTES);
                     const int kw0 = (ch * C::KPW) % C::P;
                     const int key_page = (page + u * max(1, t.page_stride)) * C::P;
-                    if constexpr (C::F8) {
+                    if constexpr (C::BS) {
+                        const float *ks = X.scales[stage][0], *vs = X.scales[stage][1];
+                        if (flags & F_MASK)
+                            attend_keys_bs<C, true>(kbase, kw0, key_page, t.key_end, lim0, lim1, a.scale_log2, ks, vs,
+                                                    ch * C::KPW, a.scale_shift, qa, o, m0, m1, mv0, mv1, l0, l1, lane);
+                        else
+                            attend_keys_bs<C, false>(kbase, kw0, key_page, t.key_end, lim0, lim1, a.scale_log2, ks, vs,
+                                                     ch * C::KPW, a.scale_shift, qa, o, m0, m1, mv0, mv1, l0, l1, lane);
+                    } else if constexpr (C::F8) {
                         if (flags & F_MASK)
                             attend_keys_f8<C, true>(kbase, kw0, key_page, t.key_end, lim0, lim1, a.scale_log2, qa, o,
                                                     m0, m1, l0, l1, lane);
@@ -1274,6 +1461,10 @@ gqa_engine_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     X.comb_m[w][qr + 8] = m1;
                     X.comb_l[w][qr] = lt0;
                     X.comb_l[w][qr + 8] = lt1;
+                    if constexpr (C::BS) {
+                        X.comb_mv[w][qr] = mv0;
+                        X.comb_mv[w][qr + 8] = mv1;
+                    }
                 }
                 if (w == 0 && lane == 0) {
                     X.fin_t = t;
@@ -1344,9 +1535,9 @@ cudaError_t make_map(CUtensorMap* map, const void* base, int D, int P, long long
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int P, int S, bool F8 = false, bool T8 = false>
+template <int D, int P, int S, bool F8 = false, bool T8 = false, bool BS = false>
 cudaError_t launch_cfg(const KernelArgs& a, int num_pages_total, cudaStream_t s) {
-    using C = Cfg<D, P, S, F8, T8>;
+    using C = Cfg<D, P, S, F8, T8, BS>;
     const long long rows = (long long)num_pages_total * a.num_kv_heads * P;
     if (rows >= (1LL << 31)) return cudaErrorInvalidValue;
     if ((((uintptr_t)a.k_cache) & 15) || (((uintptr_t)a.v_cache) & 15)) return cudaErrorMisalignedAddress;
@@ -1399,6 +1590,11 @@ cudaError_t launch_gqa_engine(const KernelArgs& a, int num_pages_total, int rows
     // nothing to attend and (fused) nothing to reduce: no launch
     if (a.num_tasks <= 0 && !(a.fused && a.num_red > 0)) return cudaSuccess;
     const int D = a.head_dim_qk, P = a.page_size;
+    if (a.kv_fp8 == 2) {
+        if (D == 128 && P == 64) return launch_cfg<128, 64, 4, true, false, true>(a, num_pages_total, s);
+        if (D == 128 && P == 128) return launch_cfg<128, 128, 2, true, false, true>(a, num_pages_total, s);
+        return cudaErrorNotSupported;
+    }
     if (a.kv_fp8) {
         // E4M3 codes: 128 keys (16 KiB of K and of V) per stage, six stages
         if (D == 128 && P == 64) return launch_cfg<128, 64, 4, true>(a, num_pages_total, s);

@@ -126,7 +126,11 @@ struct KernelArgs {
     int32_t fused;             // 1: the launch also produces the merged output
     int32_t inject;            // test hook (splitkv_debug_set_inject): 1 = the task claimer
                                // withholds every task, so the kernel's bounded waits expire
-    int32_t kv_fp8;            // 1: k_cache / v_cache hold E4M3 codes (GQA engine only)
+    int32_t kv_fp8;            // k_cache / v_cache hold E4M3 codes: 1 under one scale per tensor, 2
+                               // under block scales
+    const float* k_scales;     // kv_fp8 2: block scales [page][num_kv_heads][page_size >> scale_shift]
+    const float* v_scales;
+    int32_t scale_shift;       // log2 of a block's tokens
     float v_scale;             // value of a V code = e4m3 value * v_scale (1 otherwise; the key
                                // scale is folded into scale_log2)
     int32_t part_bf16;         // 1: o_part holds bf16 partial outputs (LSE stays float32)
@@ -135,6 +139,10 @@ struct KernelArgs {
     void* v_half;              // chunk tiles: f16 copy of the chunk requests' value pages,
                                // [slot][num_kv_heads][page_size][head_dim]; MLA over an E4M3
                                // cache: bf16 copy of the batch's latent pages [slot][page_size][576]
+    void* k_half;              // chunk tiles over block scales: bf16 copy of the key codes, laid out as
+                               // v_half (which then holds the value codes)
+    const float* k_unit;       // and the scales of every 16 tokens, [slot][num_kv_heads][page_size / 16]:
+    const float* v_unit;       // a key's times scale_log2, a value's
     const VhPage* vh_pages;    // the copy's slots
     int32_t num_vh_pages;
     int32_t lat_copy;          // MLA: 1 when the kernel reads the bf16 latent copy (slot =
@@ -193,6 +201,8 @@ bool chunk_tc_supports(int bf16, int head_dim, int page_size, int group);
 // f16 copy of the chunk requests' value pages (the chunk tiles' P V operand); run before
 // launch_chunk_partial on the same stream
 cudaError_t launch_chunk_value_convert(const KernelArgs& a, cudaStream_t s);
+// the same for a cache with block scales: codes of keys and values, and scales
+cudaError_t launch_chunk_block_convert(const KernelArgs& a, cudaStream_t s);
 cudaError_t launch_chunk_partial(const KernelArgs& a, long long total_q, int num_pages_total, cudaStream_t s);
 // Paired 128-row tiles (33..128 query rows of one (request, KV head) per block, two
 // independent blocks per CTA): which shapes the kernel takes, and its launch (task i =

@@ -74,7 +74,11 @@ splitkv_status cache_rows_args(const splitkv_problem* p, const splitkv_kv_rows* 
     a->part[0].head_stride = mla ? 0 : r->k_head_stride;
     a->part[0].cache = const_cast<void*>(p->k_cache);
     a->part[0].row_width = p->head_dim_qk;
-    a->part[0].scale = p->kv_fp8 ? p->k_scale : 1.f;
+    a->part[0].scale = p->kv_fp8 == 1 ? p->k_scale : 1.f;
+    if (p->kv_fp8 == 2) {
+        while ((1 << a->scale_shift) < p->scale_block) ++a->scale_shift;
+        a->part[0].scales = const_cast<float*>(p->k_block_scales);
+    }
     a->part[1] = a->part[0];
     a->part[1].rows = r->v;
     a->part[1].token_stride = r->v_token_stride;
@@ -89,7 +93,8 @@ splitkv_status cache_rows_args(const splitkv_problem* p, const splitkv_kv_rows* 
         a->part[0].width = a->part[1].width = p->head_dim_qk;
         a->part[1].head_stride = r->v_head_stride;
         a->part[1].cache = const_cast<void*>(p->v_cache);
-        a->part[1].scale = p->kv_fp8 ? p->v_scale : 1.f;
+        a->part[1].scale = p->kv_fp8 == 1 ? p->v_scale : 1.f;
+        if (p->kv_fp8 == 2) a->part[1].scales = const_cast<float*>(p->v_block_scales);
     }
     for (int k = 0; k < 2; ++k) {
         const CachePart& c = a->part[k];
@@ -107,6 +112,12 @@ splitkv_status check_rows_ptrs(const splitkv_problem* p, const CacheRowsArgs& a,
     splitkv_status s;
     if ((s = check_ptr(p->k_cache, "k_cache", false))) return s;
     if (p->kind == SPLITKV_GQA && (s = check_ptr(p->v_cache, "v_cache", false))) return s;
+    if (p->kv_fp8 == 2) {
+        if (((uintptr_t)p->k_block_scales | (uintptr_t)p->v_block_scales) & 3)
+            return fail_with(SPLITKV_ERR_INVALID_ARG, "block scales are not aligned to their elements");
+        if ((s = check_ptr(p->k_block_scales, "k_block_scales", false))) return s;
+        if ((s = check_ptr(p->v_block_scales, "v_block_scales", false))) return s;
+    }
     if ((s = check_ptr(a.part[0].rows, "rows k", false))) return s;
     if (a.part[1].width > 0 && (s = check_ptr(a.part[1].rows, "rows v", false))) return s;
     if ((s = check_ptr(p->page_table, "page_table", false))) return s;
@@ -160,7 +171,7 @@ LatentArgs layer_args(const splitkv_problem* p, const splitkv_latent_layer* l, i
     return a;
 }
 
-int cache_kind(const splitkv_problem* p) { return p->kv_fp8 ? 2 : p->dtype == SPLITKV_BF16 ? 1 : 0; }
+int cache_kind(const splitkv_problem* p) { return p->kv_fp8 ? p->kv_fp8 + 1 : p->dtype == SPLITKV_BF16 ? 1 : 0; }
 
 }  // namespace
 
@@ -528,7 +539,9 @@ splitkv_status splitkv_kv_append(const splitkv_problem* prob, const splitkv_kv_r
     if (a.rows == 0) return ok();
     if ((s = check_rows_ptrs(prob, a, dev_error_word))) return s;
     if ((s = check_ptr(prob->qo_indptr, "qo_indptr", false))) return s;
-    cudaError_t e = launch_kv_append(a, cache_kind(prob), rows->dtype == SPLITKV_F32, (cudaStream_t)stream);
+    const int f32 = rows->dtype == SPLITKV_F32;
+    cudaError_t e = prob->kv_fp8 == 2 ? launch_block_append(a, f32, (cudaStream_t)stream)
+                                      : launch_kv_append(a, cache_kind(prob), f32, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "kv_append launch");
     return ok();
 }
@@ -613,6 +626,99 @@ splitkv_status splitkv_verify_drafts(const splitkv_verify* v, int32_t* dev_error
     a.vocab = v->vocab;
     cudaError_t e = launch_verify_drafts(a, (cudaStream_t)stream);
     if (e != cudaSuccess) return cuda_fail(e, "verify_drafts launch");
+    return ok();
+}
+
+splitkv_status splitkv_assign_pages(const splitkv_pages* p, int32_t* dev_error_word, splitkv_stream stream) {
+    if (!p) return fail_with(SPLITKV_ERR_INVALID_ARG, "pages arguments are NULL");
+    if (p->batch < 1) return fail_with(SPLITKV_ERR_INVALID_ARG, "batch %d < 1", p->batch);
+    if (p->batch > kMaxPagesBatch)
+        return fail_with(SPLITKV_ERR_UNSUPPORTED, "batch %d: assign_pages takes up to %d requests", p->batch, kMaxPagesBatch);
+    if (p->page_size < 1 || p->max_pages_per_req < 1 || p->capacity < 1)
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "page_size, max_pages_per_req and capacity must be >= 1");
+    if (p->num_slots < 0 || p->reserved != 0) return fail_with(SPLITKV_ERR_INVALID_ARG, "num_slots %d or reserved", p->num_slots);
+    if ((p->qo_indptr == nullptr) != (p->slots == nullptr && p->num_slots == 0))
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "qo_indptr and slots come together");
+    if ((uintptr_t)p->slots & 7) return fail_with(SPLITKV_ERR_INVALID_ARG, "slots are not aligned to their elements");
+    splitkv_status s;
+    if ((s = check_ptr(p->page_table, "page_table", false))) return s;
+    if ((s = check_ptr(p->held, "held", false))) return s;
+    if ((s = check_ptr(p->held_out, "held_out", false))) return s;
+    if ((s = check_ptr(p->seq_lens, "seq_lens", false))) return s;
+    if ((s = check_ptr(p->free_pages, "free_pages", false))) return s;
+    if ((s = check_ptr(p->free_count, "free_count", false))) return s;
+    if ((s = check_ptr(p->free_count_out, "free_count_out", false))) return s;
+    if ((s = check_ptr(p->qo_indptr, "qo_indptr", true))) return s;
+    if ((s = check_ptr(p->slots, "slots", p->num_slots == 0))) return s;
+    if ((s = check_ptr(dev_error_word, "dev_error_word", true))) return s;
+    PagesArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.page_table = p->page_table;
+    a.held = p->held;
+    a.held_out = p->held_out;
+    a.seq_lens = p->seq_lens;
+    a.free_pages = p->free_pages;
+    a.free_count = p->free_count;
+    a.free_count_out = p->free_count_out;
+    a.qo_indptr = p->num_slots > 0 ? p->qo_indptr : nullptr;
+    a.slots = p->slots;
+    a.err = dev_error_word;
+    a.batch = p->batch;
+    a.page_size = p->page_size;
+    a.max_pages = p->max_pages_per_req;
+    a.capacity = p->capacity;
+    a.num_slots = p->num_slots;
+    cudaError_t e = launch_assign_pages(a, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "assign_pages launch");
+    return ok();
+}
+
+splitkv_status splitkv_sample_tokens(const splitkv_sample* p, int32_t* dev_error_word, splitkv_stream stream) {
+    if (!p) return fail_with(SPLITKV_ERR_INVALID_ARG, "sample arguments are NULL");
+    if (p->rows < 0 || p->rows > (1 << 24)) return fail_with(SPLITKV_ERR_INVALID_ARG, "rows %d", p->rows);
+    if (p->vocab < 1 || p->vocab > (1 << 19)) return fail_with(SPLITKV_ERR_INVALID_ARG, "vocab %d outside [1, 2^19]", p->vocab);
+    if (p->dtype != SPLITKV_F32 && p->dtype != SPLITKV_BF16)
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "logits dtype %d is not F32 or BF16", p->dtype);
+    if (p->reserved != 0) return fail_with(SPLITKV_ERR_INVALID_ARG, "reserved must be 0");
+    if (p->logits_stride < p->vocab || (p->probs && p->probs_stride < p->vocab))
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "row strides must be at least vocab");
+    if (((uintptr_t)p->logits & (p->dtype == SPLITKV_F32 ? 3 : 1)) || ((uintptr_t)p->probs & 3))
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "logits or probs are not aligned to their elements");
+    if ((p->sample_u == nullptr) != (p->out_tokens == nullptr) && p->rows > 0)
+        return fail_with(SPLITKV_ERR_INVALID_ARG, "sample_u and out_tokens come together");
+    if (!p->out_tokens && !p->probs && p->rows > 0) return fail_with(SPLITKV_ERR_INVALID_ARG, "neither out_tokens nor probs");
+    if (p->rows == 0) return ok();
+    const uintptr_t in = (uintptr_t)p->logits, out = (uintptr_t)p->probs;
+    const uintptr_t in_end = in + (uintptr_t)((p->rows - 1) * p->logits_stride + p->vocab) * (p->dtype == SPLITKV_F32 ? 4 : 2);
+    const uintptr_t out_end = out + (uintptr_t)((p->rows - 1) * p->probs_stride + p->vocab) * 4;
+    if (out && in < out_end && out < in_end) return fail_with(SPLITKV_ERR_INVALID_ARG, "probs overlaps logits");
+    splitkv_status s;
+    if ((s = check_ptr(p->logits, "logits", false))) return s;
+    if ((s = check_ptr(p->temperature, "temperature", true))) return s;
+    if ((s = check_ptr(p->top_k, "top_k", true))) return s;
+    if ((s = check_ptr(p->top_p, "top_p", true))) return s;
+    if ((s = check_ptr(p->min_p, "min_p", true))) return s;
+    if ((s = check_ptr(p->sample_u, "sample_u", true))) return s;
+    if ((s = check_ptr(p->out_tokens, "out_tokens", true))) return s;
+    if ((s = check_ptr(p->probs, "probs", true))) return s;
+    if ((s = check_ptr(dev_error_word, "dev_error_word", true))) return s;
+    SampleArgs a;
+    std::memset(&a, 0, sizeof a);
+    a.logits = p->logits;
+    a.logits_stride = p->logits_stride;
+    a.temperature = p->temperature;
+    a.top_k = p->top_k;
+    a.top_p = p->top_p;
+    a.min_p = p->min_p;
+    a.u = p->sample_u;
+    a.tokens = p->out_tokens;
+    a.probs = p->probs;
+    a.probs_stride = p->probs_stride;
+    a.err = dev_error_word;
+    a.rows = p->rows;
+    a.vocab = p->vocab;
+    cudaError_t e = launch_sample_tokens(a, p->dtype == SPLITKV_BF16, (cudaStream_t)stream);
+    if (e != cudaSuccess) return cuda_fail(e, "sample_tokens launch");
     return ok();
 }
 

@@ -38,6 +38,7 @@ struct CachePart {
     int32_t row_width;
     int32_t col;
     float scale;           // E4M3: value = code * scale
+    float* scales;         // block scales [page][heads][page_size >> scale_shift] in its place, or null
 };
 
 struct CacheRowsArgs {
@@ -52,7 +53,45 @@ struct CacheRowsArgs {
     int32_t page_size;
     int32_t num_pages;
     int32_t max_pages;
+    int32_t scale_shift;       // log2 of the tokens of a block scale
     int32_t* err;              // may be null
+};
+
+// ---- pages and slots -------------------------------------------------------
+constexpr int32_t kMaxPagesBatch = 8192;
+struct PagesArgs {
+    int32_t* page_table;
+    const int32_t* held;
+    int32_t* held_out;
+    const int32_t* seq_lens;
+    int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* free_count_out;
+    const int32_t* qo_indptr;  // null without slots
+    int64_t* slots;
+    int32_t* err;              // may be null
+    int32_t batch;
+    int32_t page_size;
+    int32_t max_pages;
+    int32_t capacity;
+    int32_t num_slots;
+};
+
+// ---- the next tokens from logits ---------------------------------------------
+struct SampleArgs {
+    const void* logits;
+    int64_t logits_stride;
+    const float* temperature;  // settings: null where they are off for every row
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    const float* u;            // null without tokens
+    int32_t* tokens;
+    float* probs;              // may be null
+    int64_t probs_stride;
+    int32_t* err;              // may be null
+    int32_t rows;
+    int32_t vocab;
 };
 
 // ---- verification of drafted tokens -----------------------------------------
@@ -75,9 +114,12 @@ struct VerifyArgs {
     int32_t vocab;
 };
 
-// cache_kind / rows_f32: 0 f32, 1 bf16, 2 E4M3 cache entries; rows float32 or bf16
+// cache_kind / rows_f32: 0 f32, 1 bf16, 2 E4M3, 3 (gather) E4M3 with block scales; rows float32 or bf16
 cudaError_t launch_kv_append(const CacheRowsArgs& a, int cache_kind, int rows_f32, cudaStream_t s);
 cudaError_t launch_kv_gather(const CacheRowsArgs& a, int cache_kind, int rows_f32, cudaStream_t s);
+cudaError_t launch_block_append(const CacheRowsArgs& a, int rows_f32, cudaStream_t s);   // kind 3
+cudaError_t launch_assign_pages(const PagesArgs& a, cudaStream_t s);
+cudaError_t launch_sample_tokens(const SampleArgs& a, int logits_bf16, cudaStream_t s);
 cudaError_t launch_verify_drafts(const VerifyArgs& a, cudaStream_t s);
 
 }  // namespace skv
