@@ -682,8 +682,9 @@ typedef struct {
  *    probabilities of 0.  Infinite logits share all the weight.  T = 0 is the largest logit's
  *    lowest token, whatever the other settings.
  *    Random numbers of 1 and more draw the last token with weight, negative ones and NaN the first.
- *  Weights are whole multiples of 2^-44 of the largest, computed to 2^-40 of themselves, so that their sums do
- *    not depend on any order; probs are float32.
+ *  Weights are whole multiples of a unit (2^-44 of the power of two just above the largest), computed to
+ *    2^-40 of themselves (2^-38 where |m| / T is some hundreds), so that their sums do not depend on any order;
+ *    probs are float32.
  *  dev_error_word: device int32 or NULL.  A negative or NaN temperature reports
  *    DEVICE_CHECK and gives token -1 and probabilities of 0.
  */

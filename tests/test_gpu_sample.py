@@ -2,7 +2,7 @@
 distributions to half a step of float32 and the errors of the weights behind them.
 
 A drawn token can differ from float64's only where sample_u times the total lies within the sums' error of a
-border between two tokens.  A weight is rounded to a multiple of 2^-44 of the largest (half of that: 2^-45, for
+border between two tokens.  A weight is rounded to a unit of at most 2^-43 of the largest (half of that: 2^-44, for
 each of V tokens) after an exponential whose error is below 2^-40 of itself (of the total, for all together; the
 product with top_p or sample_u doubles it), and float64's own sums stay below 2^-40 of the total too.  The rows here are few
 and their numbers fixed, and each test asserts that no border is that near."""
@@ -86,7 +86,7 @@ def check(x, u, t=None, k=None, p=None, mp=None):
     f32 = lambda v, r, off: off if v is None else float(np.float32(v[r]))  # noqa: E731
     for r in range(rows):
         want, token, near, total = reference(host[r], f32(t, r, 1.0), 0 if k is None else k[r], f32(p, r, 1.0), f32(mp, r, 0.0), u[r])
-        assert near > V * 2.0 ** -45 + 4 * 2.0 ** -40 * total, f"row {r}: a border within {near:.2e} (total {total:.3g})"
+        assert near > V * 2.0 ** -44 + 4 * 2.0 ** -40 * total, f"row {r}: a border within {near:.2e} (total {total:.3g})"
         # (probabilities below float32's normal numbers may be 0)
         assert ((got[r] > 0) == (want > 0))[(want == 0) | (want > 1e-37)].all(), f"row {r}: kept tokens differ"
         # half a step of the result, half of one of each rounded factor, and the weights' 2^-40
