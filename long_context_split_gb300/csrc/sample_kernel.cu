@@ -293,13 +293,15 @@ struct Row {
     // f(values, v) for the lane's batches of kBatch tokens of [a, b) (-infinity past its end)
     template <typename F>
     __device__ __forceinline__ void batches(int a, int b, int lane, F f) const {
-        for (int v = a + lane * VEC; v < b; v += kLoads * kStep) {
+        for (int base = a; base < b; base += kLoads * kStep) {
+            const int v = base + lane * VEC;
             float t[kLoads][VEC], flat[kBatch];
 #pragma unroll
             for (int k = 0; k < kLoads; ++k) load(t[k], v + k * kStep, b);
 #pragma unroll
             for (int j = 0; j < kBatch; ++j) flat[j] = t[j / VEC][j % VEC];
             f(flat, v);
+            __syncwarp();                  // (a warp that f has split would go on in parts: up to three times slower)
         }
     }
     // f(value, token) for the tokens that `keep` (value, token) holds for (never for -infinity): few
@@ -787,18 +789,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
                 });
             }
             cluster_sync();
+            // each CTA sums a slice of the bins over the cluster (into its list, empty yet), then all read the slices
+            const int slice = (kBins + cluster - 1) / cluster;
+            for (int i = threadIdx.x; i < slice && rank * slice + i < kBins; i += kThreads) {
+                const int b = rank * slice + i;
+                u64 s = 0;
+                for (int c = 0; c < cluster; ++c)
+                    s += (u64)load_u32(remote(&S.part[0][b], c)) + ((u64)load_u32(remote(&S.part[1][b], c)) << kLimb) +
+                         ((u64)load_u32(remote(&S.part[2][b], c)) << (2 * kLimb));
+                S.list[i] = s;
+            }
+            cluster_sync();
             u64 sum[kPer], own = 0;
 #pragma unroll
-            for (int j = 0; j < kPer; ++j) sum[j] = 0;
-            for (int c = 0; c < cluster; ++c)
-#pragma unroll
-                for (int j = 0; j < kPer; ++j) {
-                    const int i = kPer * threadIdx.x + j;
-                    sum[j] += (u64)load_u32(remote(&S.part[0][i], c)) + ((u64)load_u32(remote(&S.part[1][i], c)) << kLimb) +
-                              ((u64)load_u32(remote(&S.part[2][i], c)) << (2 * kLimb));
-                }
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) own += sum[j];
+            for (int j = 0; j < kPer; ++j) {
+                const int b = kPer * threadIdx.x + j;
+                sum[j] = load_u64(remote(&S.list[b % slice], b / slice));
+                own += sum[j];
+            }
             u64 incl = own, zero = 0, all_s, all_z;
             block_scan(S, incl, zero, all_s, all_z);
             if (level == 0) need = by_count ? (u64)k : needed_of(all_s, p);
