@@ -227,8 +227,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 
 // The same for E4M3 caches with block scales: bf16 key codes (every E4M3 value is a bf16 and an
 // f16 number, so no product is rounded before its scale), f16 value codes, and a scale
-// for every 16 tokens and head, of keys times the score scale.  Slots past a request's last key hold zeros,
-// and so do the scales of 16 such slots.  Bound by HBM: 2 bytes read, 4 written per key-value pair of elements.
+// for every 16 tokens and head, of keys times the score scale.  Slots past a request's last key hold zeros.  Bound by HBM: 2 bytes read, 4 written per key-value pair of elements.
 __global__ void __launch_bounds__(256) chunk_block_convert_kernel(KernelArgs a) {
     constexpr int U = 2;
     const int P = a.page_size, H = a.num_kv_heads;
@@ -247,7 +246,8 @@ __global__ void __launch_bounds__(256) chunk_block_convert_kernel(KernelArgs a) 
             const int t = i % (P / 16) * 16;                           // first slot of the unit
             const size_t at = (((size_t)(ok ? phys : 0) * H + i / (P / 16)) * P + t) >> a.scale_shift;
             const bool used = ok && t < rows;
-            const_cast<float*>(a.k_unit)[(size_t)slot * units + i] = used ? a.k_scales[at] * a.scale_log2 : 0.f;
+            // (a masked score, -infinity, keeps its sign under a scale of 0 taken as 2^-126)
+            const_cast<float*>(a.k_unit)[(size_t)slot * units + i] = fmaxf(used ? a.k_scales[at] * a.scale_log2 : 0.f, 0x1p-126f);
             const_cast<float*>(a.v_unit)[(size_t)slot * units + i] = used ? a.v_scales[at] : 0.f;
         }
         for (int i0 = threadIdx.x; i0 < per_page; i0 += U * blockDim.x) {
@@ -287,43 +287,68 @@ __global__ void __launch_bounds__(256) chunk_block_convert_kernel(KernelArgs a) 
     if (bad_page) set_error(a.err, ERR_DEVICE_CHECK | SITE_PAGE_RANGE);
 }
 
-// the largest raw score of each 16 of a unit's 64 keys (keys j < valid when MASK)
-template <bool MASK>
-__device__ __forceinline__ void row_max16(const uint32_t (&sr)[64], int valid, float (&mx)[4]) {
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-        mx[h] = -INFINITY;
-#pragma unroll
-        for (int j = 16 * h; j < 16 * h + 16; ++j)
-            if (!MASK || j < valid) mx[h] = fmaxf(mx[h], __uint_as_float(sr[j]));
-    }
+// ---- the softmax of a unit with block scales: a thread's serial work per unit sets the pace, so
+// maxima take three operands, and scaling, products and sums two values per instruction ----
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
-// write_p16 with block scales: P = 2^(s c[h] - base) is summed, P f[h] is written
-template <bool MASK>
+// the largest raw score of 16 keys
+__device__ __forceinline__ float max16(const uint32_t* s) {
+    float m = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
+#pragma unroll
+    for (int j = 3; j < 15; j += 2) m = max3(m, __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+    return fmaxf(m, __uint_as_float(s[15]));
+}
+
+// P = 2^(s c[h] - base) is summed, P f[h] is written as f16 pairs (key 2k in the low half of column k)
 __device__ __forceinline__ float write_p16_blocks(const uint32_t (&sr)[64], const float (&c)[4], const float (&f)[4], float base,
-                                                  int key0, int limit, uint32_t pcol) {
-    float part[4];
+                                                  uint32_t pcol) {
+    uint64_t sum[4];
+    const uint64_t shift = pack2(-base, -base);
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
+        const uint64_t scale = pack2(c[h], c[h]), weight = pack2(f[h], f[h]);
         uint32_t pk[8];
-        part[h] = 0.f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int j = 16 * h + 2 * e;
-            float x0 = ex2_ftz(fmaf(__uint_as_float(sr[j]), c[h], -base));
-            float x1 = ex2_ftz(fmaf(__uint_as_float(sr[j + 1]), c[h], -base));
-            if (MASK) {
-                if (key0 + j > limit) x0 = 0.f;
-                if (key0 + j + 1 > limit) x1 = 0.f;
-            }
-            part[h] += x0 + x1;
-            __half2 p2 = __floats2half2_rn(x0 * f[h], x1 * f[h]);
-            pk[e] = *reinterpret_cast<uint32_t*>(&p2);
+            float x0, x1;
+            unpack2(fma2(pack2(__uint_as_float(sr[j]), __uint_as_float(sr[j + 1])), scale, shift), x0, x1);
+            const uint64_t p = pack2(ex2_ftz(x0), ex2_ftz(x1));
+            sum[h] = e == 0 ? p : add2(sum[h], p);
+            unpack2(mul2(p, weight), x0, x1);
+            const __half2 p2 = __floats2half2_rn(x0, x1);
+            pk[e] = *reinterpret_cast<const uint32_t*>(&p2);
         }
         SKV_ST8(pcol + 8 * h, pk);
     }
-    return (part[0] + part[1]) + (part[2] + part[3]);
+    float a, b;
+    unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+    return a + b;
 }
 
 // BS: block scales.  Keys and values are the copies' codes; a score takes its key's scale in place
@@ -609,7 +634,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             const bool direct = fused && ct.r.n_splits == 1;   // write the final output
             float m = -INFINITY, l = 0.f;
             [[maybe_unused]] float mv = -INFINITY;
-            // block scales of unit u, read a unit ahead
+            // block scales of the next unit, read behind the last one's P
             [[maybe_unused]] float4 kn = make_float4(0.f, 0.f, 0.f, 0.f), vn = kn;
             auto read_scales = [&](int u) {
                 if constexpr (BS) {
@@ -622,8 +647,6 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             };
             if (nu > 0) read_scales(0);
             for (int u = 0; u < nu; ++u) {
-                [[maybe_unused]] const float kc[4] = {kn.x, kn.y, kn.z, kn.w}, vc[4] = {vn.x, vn.y, vn.z, vn.w};
-                if (BS && u + 1 < nu) read_scales(u + 1);
                 const uint32_t gi = sn;       // this tile's unit index: S/P buffer gi & 1
                 const int b2 = (int)(gi & 1);
                 if (!warp_wait(smem_u32(&B.s_full[t][b2]), (gi >> 1) & 1, abort_flag, lane)) { give_up(SITE_FULL_WAIT); ok = false; break; }
@@ -640,14 +663,20 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 // row max of the raw scores (the scale, > 0 on this path, is applied after)
                 float mx, my = -INFINITY;
                 if constexpr (BS) {
-                    float mxr[4];
-                    if (unmasked) row_max16<false>(sr, 64, mxr); else row_max16<true>(sr, limit - key0 + 1, mxr);
+                    if (!unmasked) {
+#pragma unroll
+                        for (int j = 0; j < 64; ++j)
+                            if (key0 + j > limit) sr[j] = 0xFF800000u;   // -infinity
+                    }
+                    const float kc[4] = {kn.x, kn.y, kn.z, kn.w}, vc[4] = {vn.x, vn.y, vn.z, vn.w};
                     mx = -INFINITY;
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        const float x = mxr[h] * kc[h];   // (-inf * 0, no key: NaN, which fmaxf passes over)
+                        const float x = max16(sr + 16 * h) * kc[h];
                         mx = fmaxf(mx, x);
-                        my = fmaxf(my, x + (float)((int)(__float_as_uint(vc[h]) >> 23) - 126));   // 2^.. > v
+                        // 2^up > v: v's exponent bits, as the low bits of 2^23 + ..
+                        const float up = __uint_as_float(0x4B000000u | (__float_as_uint(vc[h]) >> 23)) - (8388608.f + 126.f);
+                        my = fmaxf(my, x + up);
                     }
                 } else {
                     const float mxr = unmasked ? row_max64<false>(sr, 64) : row_max64<true>(sr, limit - key0 + 1);
@@ -706,10 +735,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 const uint32_t pcol = lane_addr + kColS + kKeys * b2;
                 if constexpr (BS) {
                     // from units of 2^m to 2^mv (at most 2^107 apart where a value's scale is not 0)
-                    const float to = exp2f(fminf(base - (mv == -INFINITY ? 0.f : mv), 126.f));
-                    const float f[4] = {vc[0] * to, vc[1] * to, vc[2] * to, vc[3] * to};
-                    l += unmasked ? write_p16_blocks<false>(sr, kc, f, base, key0, limit, pcol)
-                                  : write_p16_blocks<true>(sr, kc, f, base, key0, limit, pcol);
+                    const float to = ex2_ftz(fminf(base - (mv == -INFINITY ? 0.f : mv), 126.f));
+                    const float kc[4] = {kn.x, kn.y, kn.z, kn.w}, f[4] = {vn.x * to, vn.y * to, vn.z * to, vn.w * to};
+                    l += write_p16_blocks(sr, kc, f, base, pcol);
+                    if (u + 1 < nu) read_scales(u + 1);
                 } else {
                     l += unmasked ? write_p16<false>(sr, c2, base, key0, limit, pcol)
                                   : write_p16<true>(sr, c2, base, key0, limit, pcol);
