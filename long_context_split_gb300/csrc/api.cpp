@@ -603,7 +603,8 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
         long long rows = (long long)pl->q_len[b] * g;
         rpt[b] = pl->rows_per_task;
         if (pl->path == 1 && P >= 64 && rows > 16) rpt[b] = 64;
-        // (block scales: no paired tiles)
+        // (block scales: no paired tiles, and chunk tiles from 65 rows: 16 requests of 80 to 128 rows after 8,000 tokens
+        // 304 us, on the engine's wide blocks 345 to 366; of 64 rows 305 against 212)
         if (chunk_ok && rows > (prob->kv_fp8 == 2 ? 64 : 128)) {
             rpt[b] = 256;
             is_chunk[b] = 1;
@@ -618,6 +619,16 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
         seqs[b].q_len = pl->q_len[b];
     }
     model::Params mp = model_params(pp, prob->num_q_heads, pl->path, P);
+    // Block scales: fewer chunk tasks than SMs have their histories split into about one round of them, at
+    // least 8 units (512 keys) each, and do not run beside the engine.  (128 rows of 8 KV heads after 30,000
+    // tokens, 8 tasks: 499 us unsplit, 110 in 144 tasks.)
+    long long chunk_tasks = 0, chunk_units = 0;
+    for (int b = 0; b < B; ++b) {
+        if (is_chunk[b] != 1) continue;
+        chunk_tasks += seqs[b].tasks_per_split;
+        chunk_units += (long long)seqs[b].tasks_per_split * ((pl->seq_len[b] + 63) / 64);
+    }
+    const bool split_chunks = prob->kv_fp8 == 2 && pp.mode == SPLITKV_PLAN_CRITICAL_WAVE && chunk_tasks > 0 && chunk_tasks < device_sms();
     // Chunk tiles beside the engine: when every chunk request stays unsplit (its tiles write
     // the final rows, so the engine's reduction phase needs nothing from them) and no request
     // runs on the paired tiles, the two kernels run at once on disjoint SMs, split in
@@ -625,7 +636,7 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
     // measured for these kernels on GB300).
     {
         long long n_chunk = 0, n_eng = 0, n_pair = 0;
-        bool unsplit = true, rows8 = true;   // rows8: every engine task of at most 8 rows
+        bool unsplit = !split_chunks, rows8 = true;   // rows8: every engine task of at most 8 rows
         double flops = 0.0, kv_bytes = 0.0;
         for (int b = 0; b < B; ++b) {
             const int cs = pp.mode == SPLITKV_PLAN_UNIFORM ? pp.uniform_splits
@@ -676,6 +687,12 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
             if (is_chunk[b] == 1) splits[b] = std::max(1, std::min(pp.min_splits, seqs[b].tiles));
             else if (is_chunk[b] == 2) pair.push_back(b);
             else eng.push_back(b);
+        }
+        if (split_chunks) {
+            const long long sms = device_sms(), each = std::max(8ll, (chunk_units + sms - 1) / sms);
+            for (int b = 0; b < B; ++b)
+                if (is_chunk[b] == 1)
+                    splits[b] = std::max(splits[b], (int)std::min<long long>({pp.max_splits, seqs[b].tiles, (pl->seq_len[b] + 63) / 64 / each}));
         }
         for (int part = 0; part < 2; ++part) {
             const std::vector<int>& idx = part == 0 ? pair : eng;

@@ -10,8 +10,9 @@
 // What bounds it: bytes (rows read once, codes written once) for prompts, and for
 // a few rows the chain row -> request -> length -> page id -> scale.  A unit (block,
 // head, keys or values) is taken by 1, 2, 4 or 8 warps, as many as hold its rows in
-// registers between the maximum and the quantisation (256 bytes a lane), so that rows are
-// read once; a CTA works on 8 warps' worth of units at a time.
+// registers between the maximum and the quantisation (128 bytes a lane, so that four CTAs fit an SM; 256 for the
+// largest), so that rows are read once; a CTA works on 8 warps' worth of units at a time, on as many rows as leave
+// five CTAs an SM, so that the chain is waited for once for many rows.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -25,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kHold = 16;          // pieces of 16 bytes that a lane holds
+constexpr int kCtas = 5;           // CTAs per SM that the rows are shared out to
 constexpr int kMaxUnits = 128;     // rows, so at most as many blocks, of a CTA
 
 // One block with new tokens: its first new row, how many, and where they go
@@ -153,9 +154,10 @@ __device__ __forceinline__ int find_units(const CacheRowsArgs& a, int r0, int n,
     return *count;
 }
 
-// W warps per unit; gridDim.y shares the (keys or values, head) pairs out
-template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(kThreads) block_append_kernel(CacheRowsArgs a, int rows_per_cta) {
+// W warps per unit, of which a lane holds kHold pieces; gridDim.y shares the (keys or values, head) pairs out.
+// per_shift: log2 of a row's pieces, -1 where that is not whole.
+template <typename T, int VEC, int W, int kHold>
+__global__ void __launch_bounds__(kThreads, kHold <= 8 ? 4 : 2) block_append_kernel(CacheRowsArgs a, int rows_per_cta, int per_shift) {
     __shared__ Unit units[kMaxUnits];
     __shared__ int count;
     __shared__ float warp_max[kWarps];
@@ -181,7 +183,10 @@ __global__ void __launch_bounds__(kThreads) block_append_kernel(CacheRowsArgs a,
         // ---- the largest magnitude, the rows kept in registers ----
         Piece<T, VEC> x[kHold];
         float top = 0.f;
-        auto at = [&](int k) { return rows + (size_t)(k / per) * p.token_stride + (k % per) * VEC; };
+        auto at = [&](int k) {
+            const int r = per_shift >= 0 ? k >> per_shift : k / per;
+            return rows + (size_t)r * p.token_stride + (k - r * per) * VEC;
+        };
         if (held) {
 #pragma unroll
             for (int k = 0; k < kHold; ++k)
@@ -250,15 +255,20 @@ __global__ void __launch_bounds__(kThreads) block_append_kernel(CacheRowsArgs a,
     }
 }
 
-template <typename T, int VEC, int W>
+template <typename T, int VEC, int W, int kHold>
 cudaError_t launch_w(const CacheRowsArgs& a, cudaStream_t s) {
-    // rows per CTA: a block's worth where requests bring that many, one where they bring one each
-    const int per = std::max(1, std::min({1 << a.scale_shift, kMaxUnits, a.rows / a.batch}));
-    const long long x = ((long long)a.rows + per - 1) / per;
+    const int sms = sm_count();
+    if (sms <= 0) return cudaErrorInvalidDevice;
     const int y = std::max(1, std::min(2 * a.heads, 2 * a.heads * W / kWarps));   // one unit per group of warps
+    const long long want = ((long long)a.rows * y + kCtas * sms - 1) / (kCtas * sms);
+    const int per = (int)std::max(1ll, std::min<long long>(kMaxUnits, want));
+    const long long x = ((long long)a.rows + per - 1) / per;
     if (x > 0x7fffffff) return cudaErrorInvalidValue;
+    const int pieces = a.part[0].width / VEC;
+    int shift = 0;
+    while ((1 << shift) < pieces) ++shift;
     ProfileScope ps(SPLITKV_KERNEL_KV_APPEND, s);
-    block_append_kernel<T, VEC, W><<<dim3((unsigned)x, (unsigned)y), kThreads, 0, s>>>(a, per);
+    block_append_kernel<T, VEC, W, kHold><<<dim3((unsigned)x, (unsigned)y), kThreads, 0, s>>>(a, per, (1 << shift) == pieces ? shift : -1);
     return cudaGetLastError();
 }
 
@@ -269,12 +279,13 @@ cudaError_t launch_t(const CacheRowsArgs& a, cudaStream_t s) {
     for (const CachePart& p : a.part)
         vec = vec && p.width % V == 0 && (a.rows == 1 || p.token_stride * sizeof(T) % 16 == 0) &&
               (a.heads == 1 || p.head_stride * sizeof(T) % 16 == 0) && !((uintptr_t)p.rows & 15) && !((uintptr_t)p.cache % V);
-    if (!vec) return launch_w<T, 1, 8>(a, s);
+    if (!vec) return launch_w<T, 1, 8, 8>(a, s);
     const size_t bytes = ((size_t)a.part[0].width * sizeof(T)) << a.scale_shift;   // of a unit
-    if (bytes <= 8192) return launch_w<T, V, 1>(a, s);
-    if (bytes <= 16384) return launch_w<T, V, 2>(a, s);
-    if (bytes <= 32768) return launch_w<T, V, 4>(a, s);
-    return launch_w<T, V, 8>(a, s);
+    if (bytes <= 4096) return launch_w<T, V, 1, 8>(a, s);
+    if (bytes <= 8192) return launch_w<T, V, 2, 8>(a, s);
+    if (bytes <= 16384) return launch_w<T, V, 4, 8>(a, s);
+    if (bytes <= 32768) return launch_w<T, V, 8, 8>(a, s);
+    return launch_w<T, V, 8, 16>(a, s);
 }
 
 }  // namespace

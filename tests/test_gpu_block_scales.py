@@ -251,6 +251,21 @@ def test_splits_interleaved_and_two_stage(params):
     check_attention(batch, *att.two_stage(), ref=(o, l, bound, lse_bound))
 
 
+@pytest.mark.parametrize("params", [dict(), dict(mode="uniform", uniform_splits=3), dict(mode="uniform", uniform_splits=4, partial_dtype=skv.BF16),
+                                    dict(mode="uniform", uniform_splits=30)])
+def test_split_chunks(params):
+    """Chunk tiles whose histories are split (by the planner, where there are few of them), beside decoding requests."""
+    batch = BlockBatch([1500, 300, 2100], [40, 1, 17], heads=2, group=8, page=64, block=32, seed=51, spread=2.0, poison=True)
+    att = skv.SplitKVAttention(batch.problem, skv.plan_params(**params) if params else None)
+    assert att.plan.num_chunk_tasks > 0 and att.plan.splits()[0] > 1 and att.plan.overlap_ctas == 0
+    o, l, bound, lse_bound = batch.attention()
+    if params.get("partial_dtype") == skv.BF16:
+        bound = bound + 2.0 ** -8 * 448.0 * np.nanmax(batch.vs)
+    check_attention(batch, *att.decode(), ref=(o, l, bound, lse_bound))
+    check_attention(batch, *att.two_stage(), ref=(o, l, bound, lse_bound))
+    att.check_device_error()
+
+
 @pytest.mark.parametrize("page,block,dim,heads,group", [(16, 16, 128, 2, 4), (64, 32, 64, 1, 8), (128, 64, 64, 2, 2), (32, 16, 128, 1, 3)])
 def test_other_shapes_on_the_float32_path(page, block, dim, heads, group):
     batch = BlockBatch([1, 100, 333], [1, 3, 20], heads=heads, group=group, dim=dim, page=page, block=block, seed=60, spread=3.0,
