@@ -67,6 +67,23 @@ __device__ __forceinline__ float finite_abs(float x) {
     return a <= FLT_MAX ? a : 0.f;
 }
 
+// The largest magnitude of pieces, as bits: magnitudes order as integers do (those of infinities and NaN above
+// all), two bf16 in a word.
+template <typename T, int VEC>
+struct Largest {
+    uint32_t bits = 0;
+    __device__ __forceinline__ void add(const Piece<T, VEC>& r) {
+#pragma unroll
+        for (int j = 0; j < (VEC * (int)sizeof(T) + 3) / 4; ++j) {
+            if constexpr (sizeof(T) == 4) bits = max(bits, r.w[j] & 0x7FFFFFFFu);
+            else bits = __vmaxu2(bits, r.w[j] & 0x7FFF7FFFu);
+        }
+    }
+    __device__ __forceinline__ float value() const {
+        return __uint_as_float(sizeof(T) == 4 ? bits : max(bits >> 16, bits & 0xFFFFu) << 16);
+    }
+};
+
 // The smallest power of two, from 2^-126 on, whose 448-fold is not below a.  448 = 1.75 * 2^8.
 __device__ __forceinline__ float pow2_scale(float a) {
     const uint32_t bits = __float_as_uint(a);
@@ -85,15 +102,15 @@ __device__ __forceinline__ uint32_t encode4(float x0, float x1, float x2, float 
 }
 
 // x / s in float32, correctly rounded: a power of two's reciprocal is exact
+template <bool POW2>
 struct Quotient {
-    float s, inv;
-    bool exact;
-    __device__ explicit Quotient(float scale) : s(scale), inv(1.f / scale), exact(is_pow2(scale)) {}
-    __device__ __forceinline__ float operator()(float x) const { return exact ? x * inv : __fdiv_rn(x, s); }
+    float s;             // its reciprocal for a power of two
+    __device__ explicit Quotient(float scale) : s(POW2 ? 1.f / scale : scale) {}
+    __device__ __forceinline__ float operator()(float x) const { return POW2 ? x * s : __fdiv_rn(x, s); }
 };
 
-template <typename T, int VEC>
-__device__ __forceinline__ void store_codes(uint8_t* to, const Piece<T, VEC>& r, const Quotient& q) {
+template <typename T, int VEC, bool POW2>
+__device__ __forceinline__ void store_codes(uint8_t* to, const Piece<T, VEC>& r, const Quotient<POW2>& q) {
     if constexpr (VEC == 8) {
         uint2 v;
         v.x = encode4(q(element<T, VEC>(r, 0)), q(element<T, VEC>(r, 1)), q(element<T, VEC>(r, 2)), q(element<T, VEC>(r, 3)));
@@ -191,11 +208,18 @@ __global__ void __launch_bounds__(kThreads, kHold <= 8 ? 4 : 2) block_append_ker
 #pragma unroll
             for (int k = 0; k < kHold; ++k)
                 if (lane + k * kLanes < pieces) load_piece<T, VEC>(x[k], at(lane + k * kLanes));
+            Largest<T, VEC> all;
 #pragma unroll
-            for (int k = 0; k < kHold; ++k) {
-                if (lane + k * kLanes >= pieces) break;
+            for (int k = 0; k < kHold; ++k)
+                if (lane + k * kLanes < pieces) all.add(x[k]);
+            top = all.value();
+            if (!(top <= FLT_MAX)) {       // an infinity or NaN among them
+                top = 0.f;
 #pragma unroll
-                for (int j = 0; j < VEC; ++j) top = fmaxf(top, finite_abs(element<T, VEC>(x[k], j)));
+                for (int k = 0; k < kHold; ++k)
+                    if (lane + k * kLanes < pieces)
+#pragma unroll
+                        for (int j = 0; j < VEC; ++j) top = fmaxf(top, finite_abs(element<T, VEC>(x[k], j)));
             }
         } else {
             for (int k = lane; k < pieces; k += kLanes) {
@@ -219,38 +243,41 @@ __global__ void __launch_bounds__(kThreads, kHold <= 8 ? 4 : 2) block_append_ker
         if (!on) continue;
         const bool keep = was > 0.f && top <= 448.f * was;
         const float now = keep ? was : pow2_scale(top);
-        const Quotient q(now);
-        if (u.old > 0 && !keep) {
-            // ---- older codes under the new scale ----
-            uint8_t* old = codes - (size_t)u.old * width;
-            for (int k = lane; k < u.old * per; k += kLanes) {
-                uint8_t* c = old + (size_t)k * VEC;
-                if constexpr (VEC == 1) {
-                    const float v = __half2float(__half(__nv_cvt_fp8_to_halfraw(*c, __NV_E4M3)));
-                    *c = encode1(q(v * was));
-                } else {
+        auto quantise = [&](auto q) {
+            if (u.old > 0 && !keep) {
+                // ---- older codes under the new scale ----
+                uint8_t* old = codes - (size_t)u.old * width;
+                for (int k = lane; k < u.old * per; k += kLanes) {
+                    uint8_t* c = old + (size_t)k * VEC;
+                    if constexpr (VEC == 1) {
+                        const float v = __half2float(__half(__nv_cvt_fp8_to_halfraw(*c, __NV_E4M3)));
+                        *c = encode1(q(v * was));
+                    } else {
 #pragma unroll
-                    for (int g = 0; g < VEC / 4; ++g) {
-                        const uint32_t w = ((uint32_t*)c)[g];
-                        const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3)));
-                        const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3)));
-                        ((uint32_t*)c)[g] = encode4(q(lo.x * was), q(lo.y * was), q(hi.x * was), q(hi.y * was));
+                        for (int g = 0; g < VEC / 4; ++g) {
+                            const uint32_t w = ((uint32_t*)c)[g];
+                            const float2 lo = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3)));
+                            const float2 hi = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3)));
+                            ((uint32_t*)c)[g] = encode4(q(lo.x * was), q(lo.y * was), q(hi.x * was), q(hi.y * was));
+                        }
                     }
                 }
             }
-        }
-        if (held) {
+            if (held) {
 #pragma unroll
-            for (int k = 0; k < kHold; ++k) {
-                const int e = lane + k * kLanes;
-                if (e < pieces) store_codes<T, VEC>(codes + (size_t)e * VEC, x[k], q);
+                for (int k = 0; k < kHold; ++k) {
+                    const int e = lane + k * kLanes;
+                    if (e < pieces) store_codes<T, VEC>(codes + (size_t)e * VEC, x[k], q);
+                }
+            } else {
+                for (int k = lane; k < pieces; k += kLanes) {
+                    load_piece<T, VEC>(x[0], at(k));
+                    store_codes<T, VEC>(codes + (size_t)k * VEC, x[0], q);
+                }
             }
-        } else {
-            for (int k = lane; k < pieces; k += kLanes) {
-                load_piece<T, VEC>(x[0], at(k));
-                store_codes<T, VEC>(codes + (size_t)k * VEC, x[0], q);
-            }
-        }
+        };
+        if (is_pow2(now)) quantise(Quotient<true>(now));
+        else quantise(Quotient<false>(now));
         if (lane == 0 && !(u.old > 0 && keep)) *scale_at = now;
     }
 }

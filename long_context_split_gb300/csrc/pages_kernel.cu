@@ -10,7 +10,7 @@
 //
 // What bounds it: latency (a batch's lengths -> sums -> ids -> table), and for prompts
 // the slots, 8 bytes a token.  One cluster of up to 8 CTAs does the call in one
-// launch: each CTA sums the whole batch for itself (a few thousand requests at most), a
+// launch (many slots take another, on all SMs): each CTA sums the whole batch for itself (a few thousand requests at most), a
 // cluster barrier stands between the last read of held / free_count and their
 // update in place, then all threads share out ids and slots.
 #include <algorithm>
@@ -42,9 +42,48 @@ __device__ __forceinline__ int upper(const int* at, int n, int x) {
 
 __device__ __forceinline__ int clip(long long x) { return (int)min(x, (long long)INT_MAX); }
 
-// CHUNK consecutive slots per thread and step (one search for all of them)
-template <int CHUNK>
-__global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(PagesArgs a, int cluster) {
+// The slot of row r of request b's rows lo .. hi - 1, `page_of(j)` the request's page j or -1
+template <typename F>
+__device__ __forceinline__ long long slot_of(const PagesArgs& a, int lo, int hi, int len, int r, int& page_j, int& page, F page_of) {
+    if (lo < 0 || lo > r || hi > a.num_slots || hi - lo > len) return -1;
+    const int pos = len - (hi - r), j = pos / a.page_size;
+    if (j != page_j) {
+        page_j = j;
+        page = page_of(j);
+    }
+    return page < 0 ? -1 : (long long)page * a.page_size + (pos - j * a.page_size);
+}
+
+// Many slots, from the tables that assign_pages_kernel has just written: kSlots consecutive ones per thread, one
+// search of the rows' bounds for all of them.
+constexpr int kSlots = 8, kSlotThreads = 256;
+__global__ void __launch_bounds__(kSlotThreads) slots_kernel(PagesArgs a) {
+    extern __shared__ int qo[];
+    for (int i = threadIdx.x; i <= a.batch; i += kSlotThreads) qo[i] = a.qo_indptr[i];
+    __syncthreads();
+    const int rows = min(a.num_slots, qo[a.batch]);
+    const long long r0 = ((long long)blockIdx.x * kSlotThreads + threadIdx.x) * kSlots;
+    if (r0 >= rows) return;
+    int b = upper(qo + 1, a.batch, (int)r0), page_j = -1, page = -1, len = 0, held = 0, known = -1;
+#pragma unroll
+    for (int c = 0; c < kSlots; ++c) {
+        const int r = (int)r0 + c;
+        if (r >= rows) break;
+        while (b < a.batch && qo[b + 1] <= r) ++b;
+        if (b < a.batch && b != known) {
+            known = b;
+            page_j = -1;
+            len = max(0, a.seq_lens[b]);
+            held = a.held_out[b];
+        }
+        a.slots[r] = b < a.batch ? slot_of(a, qo[b], qo[b + 1], len, r, page_j, page, [&](int j) {
+            return j < held ? a.page_table[(size_t)b * a.max_pages + j] : -1;
+        }) : -1;
+    }
+}
+
+// With few slots those too, one per thread and step
+__global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(PagesArgs a, int cluster, int with_slots) {
     extern __shared__ int smem[];
     __shared__ long long warp_sum[2][kWarps];
     const int B = a.batch, P = a.page_size;
@@ -138,47 +177,34 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(PagesArgs a, 
         a.page_table[(size_t)b * a.max_pages + held[b] + (k - k0)] = taken_page(k);
     }
     // ---- slots: a token's page is one that its request held, or one just taken ----
-    if (a.qo_indptr) {
+    if (with_slots) {
         const int rows = min(a.num_slots, qo[B]);
-        for (long long r0 = (long long)t * CHUNK; r0 < rows; r0 += (long long)step * CHUNK) {
-            int b = upper(qo + 1, B, (int)r0), page_j = -1, page = -1;
-#pragma unroll
-            for (int c = 0; c < CHUNK; ++c) {
-                const int r = (int)r0 + c;
-                if (r >= rows) break;
-                while (b < B && qo[b + 1] <= r) { ++b; page_j = -1; }
-                long long slot = -1;
-                if (b < B) {
-                    const int lo = qo[b], hi = qo[b + 1], len = tokens(b);
-                    if (lo >= 0 && lo <= r && hi <= a.num_slots && hi - lo <= len) {
-                        const int pos = len - (hi - r), j = pos / P;
-                        if (j != page_j) {
-                            page_j = j;
-                            const int need = pages(len);
-                            if (j < held[b]) page = a.page_table[(size_t)b * a.max_pages + j];
-                            else if (need <= a.max_pages && b < served) page = taken_page((b ? grow_at[b - 1] : 0) + j - held[b]);
-                            else page = -1;
-                        }
-                        if (page >= 0) slot = (long long)page * P + pos % P;
-                    }
-                }
-                a.slots[r] = slot;
-            }
+        for (int r = t; r < rows; r += step) {
+            const int b = upper(qo + 1, B, r);
+            int page_j = -1, page = -1;
+            a.slots[r] = b < B ? slot_of(a, qo[b], qo[b + 1], tokens(b), r, page_j, page, [&](int j) {
+                const int need = pages(tokens(b));
+                if (j < held[b]) return a.page_table[(size_t)b * a.max_pages + j];
+                return need <= a.max_pages && b < served ? taken_page((b ? grow_at[b - 1] : 0) + j - held[b]) : -1;
+            }) : -1;
         }
     }
     if (bad && a.err) atomicCAS(a.err, 0, ERR_DEVICE_CHECK | bad);
 }
 
-template <int CHUNK>
-cudaError_t launch(const PagesArgs& a, int cluster, cudaStream_t s) {
+}  // namespace
+
+cudaError_t launch_assign_pages(const PagesArgs& a, cudaStream_t s) {
     static std::atomic<uint64_t> done{0};
-    const size_t smem = ((size_t)4 * a.batch + 1) * sizeof(int);
-    cudaError_t e = allow_smem((const void*)assign_pages_kernel<CHUNK>, ((size_t)4 * kMaxPagesBatch + 1) * sizeof(int), done);
+    cudaError_t e = allow_smem((const void*)assign_pages_kernel, ((size_t)4 * kMaxPagesBatch + 1) * sizeof(int), done);
     if (e != cudaSuccess) return e;
+    // up to 4096 slots within the call's one launch, more on all SMs behind it (239k slots: 34 us in one launch of 8 CTAs)
+    const bool apart = a.num_slots > 4096;
+    const int cluster = std::min(kMaxCluster, std::max(1, (apart ? a.num_slots / 16 : a.num_slots) / kThreads));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)cluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = ((size_t)4 * a.batch + 1) * sizeof(int);
     cfg.stream = s;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -187,14 +213,11 @@ cudaError_t launch(const PagesArgs& a, int cluster, cudaStream_t s) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     ProfileScope ps(SPLITKV_KERNEL_ASSIGN_PAGES, s);
-    return cudaLaunchKernelEx(&cfg, assign_pages_kernel<CHUNK>, a, cluster);
-}
-
-}  // namespace
-
-cudaError_t launch_assign_pages(const PagesArgs& a, cudaStream_t s) {
-    const int cluster = std::min(kMaxCluster, std::max(1, (a.num_slots + 2 * kThreads - 1) / (2 * kThreads)));
-    return a.num_slots >= 8 * kThreads ? launch<8>(a, cluster, s) : launch<1>(a, cluster, s);
+    e = cudaLaunchKernelEx(&cfg, assign_pages_kernel, a, cluster, apart ? 0 : 1);
+    if (e != cudaSuccess || !apart) return e;
+    const int per = kSlots * kSlotThreads;
+    slots_kernel<<<(unsigned)(((long long)a.num_slots + per - 1) / per), kSlotThreads, ((size_t)a.batch + 1) * sizeof(int), s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace skv
