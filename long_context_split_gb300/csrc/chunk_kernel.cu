@@ -49,6 +49,7 @@
 #include <cuda_fp16.h>
 
 #include "tc_common.cuh"
+#include "tc_issue.cuh"
 #include "partial_io.cuh"
 #include "trace.cuh"
 
@@ -316,6 +317,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// 8 tensor-memory columns, for rescaling O beside 64 live scores
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+}
+
 // the largest raw score of 16 keys
 __device__ __forceinline__ float max16(const uint32_t* s) {
     float m = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]));
@@ -516,7 +524,80 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         // products.  Waits are bounded hardware waits; descriptors are precomputed, the
         // k-steps unrolled to constant offsets.
         const int t = warp == 1 ? 0 : 1;
-        if (lane == 0) {
+        if constexpr (BS) {
+            // The same by the warp in step, one elected lane issuing (tc_issue.cuh); both forms of the schedule and its
+            // barriers are those below.
+            const uint32_t leader = elect_one();
+            constexpr uint32_t id_s = idesc_bf16(kRows, kKeys, 0), id_o = idesc_f16(kRows, D, 1);
+            const uint64_t qd = desc_sw128(smem_u32(sQ + t * C::Q_TILE), 16, 1024);
+            const uint64_t kd0 = desc_sw128(smem_u32(sStage), 16, 1024);
+            const uint64_t vd0 = desc_sw128(smem_u32(sStage + C::TILE_BYTES), C::KV_BOX, 1024);
+            const uint32_t ocol = tmem + t * kTmemTile, bufcol = ocol + kColS;
+            uint32_t item = 0, qn = 0, pc = 0, tn = 0;
+            bool ok = true;
+            Ring<NS> ring;
+            while (ok) {
+                const int task = ring.next(B, abort_flag, lane, true);
+                if (task == -2) { give_up(SITE_FULL_WAIT); break; }
+                if (task < 0) break;
+                const ChunkTask ct = chunk_task(a, task);
+                if (ct.empty) continue;
+                const uint32_t item0 = item;
+                item += ct.n_units;
+                const int nu = t ? ct.nu[1] : ct.nu[0];
+                if (!spin_warp(smem_u32(&B.q_full), qn & 1, abort_flag)) { give_up(SITE_FULL_WAIT); break; }
+                ++qn;
+                if (nu == 0) {
+                    if (lane == 0) mbar_arrive(smem_u32(&B.q_empty));
+                    __syncwarp();
+                    continue;
+                }
+                tc_fence_after();
+                auto issue_s = [&](int u) -> bool {
+                    const uint32_t gi = item0 + u, stage = gi % NS, gs = pc + u;
+                    if (!spin_warp(smem_u32(&B.stage_full[stage]), (gi / NS) & 1, abort_flag)) return false;
+                    tc_fence_after();
+                    const uint32_t scol = bufcol + kKeys * (gs & 1);
+                    const uint64_t kd = kd0 + (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t ad = qd + (uint64_t)((((kk >> 2) * C::Q_BOX) + (kk & 3) * 32) >> 4);
+                        const uint64_t bd = kd + (uint64_t)((((kk >> 2) * C::KV_BOX) + (kk & 3) * 32) >> 4);
+                        if (kk == 0) mma_f16_if<0>(scol, ad, bd, id_s, leader);
+                        else mma_f16_if<1>(scol, ad, bd, id_s, leader);
+                    }
+                    mma_commit_if(smem_u32(&B.s_full[t][gs & 1]), leader);
+                    return true;
+                };
+                auto issue_pv = [&](int u) -> bool {
+                    if (u == 0 && !spin_warp(smem_u32(&B.o_empty[t]), (tn & 1) ^ 1, abort_flag)) return false;
+                    const uint32_t gp = pc + u, stage = (item0 + u) % NS;
+                    if (!spin_warp(smem_u32(&B.p_full[t][gp & 1]), (gp >> 1) & 1, abort_flag)) return false;
+                    tc_fence_after();
+                    const uint32_t pcol = bufcol + kKeys * (gp & 1);
+                    const uint64_t vd = vd0 + (uint64_t)(stage * (C::STAGE_BYTES >> 4));
+                    if (u == 0) mma_f16_ts_if<0>(ocol, pcol, vd, id_o, leader);
+                    else mma_f16_ts_if<1>(ocol, pcol, vd, id_o, leader);
+#pragma unroll
+                    for (int kk = 1; kk < 4; ++kk)
+                        mma_f16_ts_if<1>(ocol, pcol + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o, leader);
+                    mma_commit_if(smem_u32(&B.stage_empty[t][stage]), leader);
+                    return true;
+                };
+                ok = issue_s(0);
+                for (int u = 0; ok && u + 1 < nu; ++u) ok = issue_s(u + 1) && issue_pv(u);
+                if (ok) mma_commit_if(smem_u32(&B.q_empty), leader);
+                if (ok) ok = issue_pv(nu - 1);
+                if (!ok) { give_up(SITE_FULL_WAIT); break; }
+                mma_commit_if(smem_u32(&B.o_full[t]), leader);
+                pc += nu;
+                ++tn;
+            }
+            // every product issued here completes before tensor memory is released
+            __syncwarp();
+            mma_commit_if(smem_u32(&B.drain[t]), leader);
+            if (!spin_warp_drain(smem_u32(&B.drain[t]), 0, abort_flag)) set_error(a.err, ERR_TIMEOUT | SITE_DRAIN);
+        } else if (lane == 0) {
             constexpr uint32_t id_s = idesc_bf16(kRows, kKeys, 0);
             constexpr uint32_t id_o = idesc_f16(kRows, D, 1);     // P and V both f16
             const uint64_t qd = desc_sw128(smem_u32(sQ + t * C::Q_TILE), 16, 1024);
@@ -609,6 +690,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         const uint32_t lane_addr = tmem + ((uint32_t)((warp & 3) << 5) << 16) + t * kTmemTile;
         const bool fused = a.fused != 0;
         const float c2 = a.scale_log2;
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            if constexpr (BS) return spin_warp(bar, parity, abort_flag);
+            else return warp_wait(bar, parity, abort_flag, lane);
+        };
         uint32_t sn = 0, on = 0, item = 0;   // item: ring position of the task's first unit
         uint32_t ph = 0;                     // per stage: phase parity of this tile's next release
         bool ok = true;
@@ -649,7 +734,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             for (int u = 0; u < nu; ++u) {
                 const uint32_t gi = sn;       // this tile's unit index: S/P buffer gi & 1
                 const int b2 = (int)(gi & 1);
-                if (!warp_wait(smem_u32(&B.s_full[t][b2]), (gi >> 1) & 1, abort_flag, lane)) { give_up(SITE_FULL_WAIT); ok = false; break; }
+                if (!wait(smem_u32(&B.s_full[t][b2]), (gi >> 1) & 1)) { give_up(SITE_FULL_WAIT); ok = false; break; }
                 tc_fence_after();
                 uint32_t sr[64];
                 SKV_LD32(lane_addr + kColS + kKeys * b2, sr);
@@ -714,12 +799,23 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         // barrier moves on only with this tile's next release, which needs this
                         // softmax's next P: it is at most one phase behind
                         const int rs = (int)((item0 + u - 1) % NS);
-                        if (!warp_wait(smem_u32(&B.stage_empty[t][rs]), ((ph >> rs) & 1u) ^ 1u, abort_flag, lane)) {
+                        if (!wait(smem_u32(&B.stage_empty[t][rs]), ((ph >> rs) & 1u) ^ 1u)) {
                             give_up(SITE_EMPTY_WAIT); ok = false; break;
                         }
                         tc_fence_after();
                     }
-                    if (!BS) l *= scale_o;
+                    if constexpr (BS) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 8) {
+                            uint32_t o[8];
+                            tmem_ld8(lane_addr + c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale_o);
+                            SKV_ST8(lane_addr + c, o);
+                        }
+                    } else {
+                    l *= scale_o;
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
                         SKV_LD32(lane_addr + c, o);
@@ -727,6 +823,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
 #pragma unroll
                         for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * scale_o);
                         SKV_ST32(lane_addr + c, o);
+                    }
                     }
                 }
                 // P over this unit's S; the buffer's previous P was read by P V of unit gi - 2,
@@ -754,7 +851,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
             if (!ok) break;
             if (nu > 0) {
                 // ---- epilogue: O / l ----
-                if (!warp_wait(smem_u32(&B.o_full[t]), on & 1, abort_flag, lane)) { give_up(SITE_FULL_WAIT); ok = false; break; }
+                if (!wait(smem_u32(&B.o_full[t]), on & 1)) { give_up(SITE_FULL_WAIT); ok = false; break; }
                 ++on;
                 tc_fence_after();
             }
