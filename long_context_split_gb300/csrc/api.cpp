@@ -620,15 +620,20 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
     }
     model::Params mp = model_params(pp, prob->num_q_heads, pl->path, P);
     // Block scales: fewer chunk tasks than SMs have their histories split into about one round of them, at
-    // least 8 units (512 keys) each, and do not run beside the engine.  (128 rows of 8 KV heads after 30,000
+    // least 8 units (512 keys) each, and do not run beside the engine, where that saves more than the reduction
+    // costs (about 1.05 us a unit and task; 20 us and 3 ns a row).  (128 rows of 8 KV heads after 30,000
     // tokens, 8 tasks: 499 us unsplit, 110 in 144 tasks.)
-    long long chunk_tasks = 0, chunk_units = 0;
+    long long chunk_tasks = 0, chunk_units = 0, chunk_longest = 0, chunk_rows = 0;
     for (int b = 0; b < B; ++b) {
         if (is_chunk[b] != 1) continue;
         chunk_tasks += seqs[b].tasks_per_split;
         chunk_units += (long long)seqs[b].tasks_per_split * ((pl->seq_len[b] + 63) / 64);
+        chunk_longest = std::max(chunk_longest, (pl->seq_len[b] + 63) / 64ll);
+        chunk_rows += seqs[b].vectors;
     }
-    const bool split_chunks = prob->kv_fp8 == 2 && pp.mode == SPLITKV_PLAN_CRITICAL_WAVE && chunk_tasks > 0 && chunk_tasks < device_sms();
+    const double chunk_split_us = 1.05 * std::max(8.0, (double)chunk_units / device_sms()) + 20.0 + 0.003 * (double)chunk_rows;
+    const bool split_chunks = prob->kv_fp8 == 2 && pp.mode == SPLITKV_PLAN_CRITICAL_WAVE && chunk_tasks > 0 &&
+                              chunk_tasks < device_sms() && chunk_split_us < 1.05 * (double)chunk_longest;
     // Chunk tiles beside the engine: when every chunk request stays unsplit (its tiles write
     // the final rows, so the engine's reduction phase needs nothing from them) and no request
     // runs on the paired tiles, the two kernels run at once on disjoint SMs, split in
