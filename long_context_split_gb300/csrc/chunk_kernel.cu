@@ -229,35 +229,37 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 // The same for E4M3 caches with block scales: bf16 key codes (every E4M3 value is a bf16 and an
 // f16 number, so no product is rounded before its scale), f16 value codes, and a scale
 // for every 16 tokens and head, of keys times the score scale.  Slots past a request's last key hold zeros.  Bound by HBM: 2 bytes read, 4 written per key-value pair of elements.
+// A CTA takes a head of a page at a time.
 __global__ void __launch_bounds__(256) chunk_block_convert_kernel(KernelArgs a) {
-    constexpr int U = 2;
-    const int P = a.page_size, H = a.num_kv_heads;
-    const int c16 = a.head_dim_v / 16;                                 // pieces of 16 codes per row
-    const int per_page = H * P * c16, units = H * (P / 16);
+    constexpr int U = 4, c16 = 8;                                      // pieces of 16 codes per row (128 wide)
+    const int P = a.page_size, H = a.num_kv_heads;                     // (P 64 or 128)
+    const int pieces = P * c16, units = P / 16;
     bool bad_page = false;
-    for (int slot = blockIdx.x; slot < a.num_vh_pages; slot += gridDim.x) {
+    for (int u = blockIdx.x; u < a.num_vh_pages * H; u += gridDim.x) {
+        const int slot = u / H;
         const VhPage vp = a.vh_pages[slot];
         const ReqDesc r = a.reqs[vp.b];
         const int rows = r.seq_len - vp.j * P;                         // keys of the page in use
         const int phys = a.page_table[r.page_row + vp.j];
         const bool ok = phys >= 0 && phys < a.num_pages;
         if (!ok && rows > 0) bad_page = true;
-        const size_t from = (size_t)(ok ? phys : 0) * per_page, to = (size_t)slot * per_page;
-        for (int i = threadIdx.x; i < units; i += blockDim.x) {
-            const int t = i % (P / 16) * 16;                           // first slot of the unit
-            const size_t at = (((size_t)(ok ? phys : 0) * H + i / (P / 16)) * P + t) >> a.scale_shift;
+        const size_t block = (size_t)(ok ? phys : 0) * H + (u - slot * H);   // (page, head)
+        const size_t from = block * pieces, to = (size_t)u * pieces;
+        if (threadIdx.x < units) {
+            const int t = threadIdx.x * 16;                            // first slot of the unit
+            const size_t at = (block * P + t) >> a.scale_shift;
             const bool used = ok && t < rows;
             // (a masked score, -infinity, keeps its sign under a scale of 0 taken as 2^-126)
-            const_cast<float*>(a.k_unit)[(size_t)slot * units + i] = fmaxf(used ? a.k_scales[at] * a.scale_log2 : 0.f, 0x1p-126f);
-            const_cast<float*>(a.v_unit)[(size_t)slot * units + i] = used ? a.v_scales[at] : 0.f;
+            const_cast<float*>(a.k_unit)[(size_t)u * units + threadIdx.x] = fmaxf(used ? a.k_scales[at] * a.scale_log2 : 0.f, 0x1p-126f);
+            const_cast<float*>(a.v_unit)[(size_t)u * units + threadIdx.x] = used ? a.v_scales[at] : 0.f;
         }
-        for (int i0 = threadIdx.x; i0 < per_page; i0 += U * blockDim.x) {
+        for (int i0 = threadIdx.x; i0 < pieces; i0 += U * blockDim.x) {
             uint4 k[U], v[U];
 #pragma unroll
             for (int x = 0; x < U; ++x) {
                 const int idx = i0 + x * blockDim.x;
                 k[x] = v[x] = make_uint4(0u, 0u, 0u, 0u);
-                if (idx < per_page && ok && (idx / c16) % P < rows) {
+                if (idx < pieces && ok && idx / c16 < rows) {
                     k[x] = __ldcs((const uint4*)a.k_cache + from + idx);
                     v[x] = __ldcs((const uint4*)a.v_cache + from + idx);
                 }
@@ -265,7 +267,7 @@ __global__ void __launch_bounds__(256) chunk_block_convert_kernel(KernelArgs a) 
 #pragma unroll
             for (int x = 0; x < U; ++x) {
                 const int idx = i0 + x * blockDim.x;
-                if (idx >= per_page) continue;
+                if (idx >= pieces) continue;
                 const uint32_t kw[4] = {k[x].x, k[x].y, k[x].z, k[x].w}, vw[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
                 uint32_t kb[8], vh[8];
 #pragma unroll
@@ -1016,13 +1018,13 @@ cudaError_t launch_chunk_value_convert(const KernelArgs& a, cudaStream_t s) {
 
 cudaError_t launch_chunk_block_convert(const KernelArgs& a, cudaStream_t s) {
     if (a.num_vh_pages <= 0) return cudaSuccess;
-    if ((((uintptr_t)a.k_cache) & 15) || (((uintptr_t)a.v_cache) & 15) || (a.head_dim_v % 16) || (a.page_size % 64))
+    if ((((uintptr_t)a.k_cache) & 15) || (((uintptr_t)a.v_cache) & 15) || a.head_dim_v != 128 || (a.page_size != 64 && a.page_size != 128))
         return cudaErrorMisalignedAddress;
     int dev = 0, sms = 0;
     cudaError_t e;
     if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-    const int blocks = std::min(sms * 8, a.num_vh_pages);   // one slot per CTA at a time
+    const int blocks = (int)std::min<long long>(sms * 8, (long long)a.num_vh_pages * a.num_kv_heads);
     {
         ProfileScope ps(SPLITKV_KERNEL_CHUNK_VCONV, s);
         chunk_block_convert_kernel<<<blocks, 256, 0, s>>>(a);
