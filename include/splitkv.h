@@ -129,7 +129,12 @@ typedef struct {
                                         kv_fp8 = 1 are UNSUPPORTED.
                                         2: E4M3 codes with a scale for each block of scale_block
                                         tokens and KV head (the fields below), GQA only; what
-                                        else kv_fp8 = 1 asks for holds here too. */
+                                        else kv_fp8 = 1 asks for holds here too.  Requests with
+                                        more than 64 query rows per KV head run on the chunk tiles
+                                        where these apply otherwise (splitkv_plan_num_chunk_tasks),
+                                        over a bf16 and f16 copy of their pages' codes (exact) that
+                                        a pre-pass writes into the workspace: 512 bytes per cached
+                                        token and KV head of theirs. */
     float k_scale;                   /* kv_fp8 1: finite, > 0 */
     float v_scale;                   /* kv_fp8 1: finite, > 0 */
     int32_t reserved0;               /* 0 */
@@ -225,7 +230,8 @@ void splitkv_plan_destroy(splitkv_plan_t *plan);
 int32_t splitkv_plan_num_tasks(const splitkv_plan_t *plan);
 /* Tasks that run on the tcgen05 chunk-tile kernel (up to 256 query rows each, as two
  * 128-row tiles): GQA bf16 requests with more than 128 query rows per KV head, D 64/128,
- * page 64/128, group size dividing 128, scale > 0, contiguous splits, bf16 cache.
+ * page 64/128, group size dividing 128, scale > 0, contiguous splits, bf16 cache; or an E4M3
+ * cache with block scales, D 128, from 65 rows on.
  * Included in splitkv_plan_num_tasks.  -1 on NULL. */
 int32_t splitkv_plan_num_chunk_tasks(const splitkv_plan_t *plan);
 /* Tasks that run on the tcgen05 paired-tile kernel: GQA requests of the same shapes
@@ -815,7 +821,8 @@ typedef enum {
     SPLITKV_KERNEL_MLA = 2,          /* tcgen05 absorbed-MLA partial attention */
     SPLITKV_KERNEL_CHUNK = 3,        /* tcgen05 GQA chunk tiles */
     SPLITKV_KERNEL_MERGE = 4,        /* merge_states */
-    SPLITKV_KERNEL_CHUNK_VCONV = 5,  /* f16 copy of the chunk requests' value pages (before the chunk tiles) */
+    SPLITKV_KERNEL_CHUNK_VCONV = 5,  /* f16 copy of the chunk requests' value pages, with block scales copies of
+                                        their keys' and values' codes (before the chunk tiles) */
     SPLITKV_KERNEL_PAIR = 6,         /* tcgen05 paired row blocks (33..128 rows per KV head) */
     SPLITKV_KERNEL_MLA_LATENT = 7,   /* bf16 copy of an E4M3 latent cache's pages (before the MLA kernel) */
     SPLITKV_KERNEL_KV_APPEND = 8,    /* rows into the paged cache */

@@ -269,8 +269,8 @@ class AttentionProblem:
         self.kv_fp8 = k_cache.dtype == torch.uint8
         if self.kv_fp8 != (k_scale is not None and v_scale is not None):
             raise TypeError("uint8 (E4M3) K/V caches come with k_scale and v_scale, other caches without")
-        blocks = isinstance(k_scale, torch.Tensor) and k_scale.dim() > 0
-        if blocks != (isinstance(v_scale, torch.Tensor) and v_scale.dim() > 0):
+        blocks = isinstance(k_scale, torch.Tensor) and k_scale.dim() > 1
+        if blocks != (isinstance(v_scale, torch.Tensor) and v_scale.dim() > 1):
             raise TypeError("k_scale and v_scale are both numbers or both block scales")
         self.scale_block = 0
         if blocks:

@@ -303,6 +303,67 @@ def test_graph_replays_follow_the_cache():
         check_attention(batch, out, lse, ref=batch.attention(want))
 
 
+@pytest.mark.parametrize("seq,new,chunks", [([300, 1000, 65], [1, 1, 1], False), ([600, 90], [40, 1], True)])
+def test_withheld_tasks_time_out_and_the_context_survives(seq, new, chunks):
+    """The test hook withholds every task: the bounded waits of the engine and of the chunk tiles run out into an error
+    status, and the next launch is right."""
+    batch = BlockBatch(seq, new, heads=2, group=8, page=64, block=16, seed=55)
+    att = skv.SplitKVAttention(batch.problem, skv.plan_params("uniform", uniform_splits=2))
+    assert (att.plan.num_chunk_tasks > 0) == chunks
+    skv.debug_set_inject(1)
+    try:
+        att.decode()
+        torch.cuda.synchronize()
+    finally:
+        skv.debug_set_inject(0)
+    assert skv.read_device_error(att.error_word, clear=True)[0] == skv.ERR_TIMEOUT
+    check_attention(batch, *att.decode())
+    att.check_device_error()
+
+
+def test_bad_pages_are_reported_and_do_not_reach_other_requests():
+    """A page id outside the pool: its request's rows are undefined, the others' right, in the engine and the tiles."""
+    for new in ([1, 1], [40, 40]):
+        batch = BlockBatch([300, 500], new, heads=2, group=4, page=64, block=16, seed=56)
+        ref = batch.attention()
+        batch.table_dev[0, 2] = batch.num_pages + 7
+        att = skv.SplitKVAttention(batch.problem)
+        out, lse = att.decode()
+        assert skv.read_device_error(att.error_word, clear=True)[0] == skv.ERR_DEVICE_CHECK
+        t = new[0]
+        o, l, bound, lse_bound = ref
+        assert (np.abs(out[t:].double().cpu().numpy() - o[t:]) <= bound[t:]).all()
+
+
+def test_decode_without_a_workspace_of_its_own():
+    batch = BlockBatch([300, 1000, 65], [1, 2, 1], heads=2, group=8, page=64, block=32, seed=57)
+    plan = skv.splitkv_plan(batch.problem)
+    out = torch.empty(4, 16, 128, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(4, 16, device="cuda")
+    skv.splitkv_decode_static(batch.problem, plan, out, lse)
+    check_attention(batch, out, lse)
+    assert skv.read_static_device_error()[0] == skv.OK
+
+
+def test_two_batches_on_two_streams():
+    """Append and attention of two batches at once, each on its own stream."""
+    pair = [BlockBatch([700, 900], [30, 1], heads=2, group=8, page=64, block=16, seed=s) for s in (58, 59)]
+    rows = [rows_of(b, torch.bfloat16, seed=s) for b, s in zip(pair, (58, 59))]
+    want = [expected(b, *r) for b, r in zip(pair, rows)]
+    atts = [skv.SplitKVAttention(b.problem) for b in pair]
+    outs = [a.out_like() for a in atts]
+    streams = [torch.cuda.Stream() for _ in pair]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for b, r, a, o, s in zip(pair, rows, atts, outs, streams):
+            skv.kv_append(b.problem, *r, stream=s)
+            a.decode(*o, stream=s)
+    torch.cuda.synchronize()
+    for b, w, o in zip(pair, want, outs):
+        assert same_codes(b.k_dev.cpu().numpy(), w[0]) and np.array_equal(b.vs_dev.cpu().numpy(), w[3])
+        check_attention(b, *o, ref=b.attention(w))
+
+
 def test_pages_beyond_two_to_the_31_bytes():
     """Pages whose codes lie more than 2^31 bytes into the cache, and their scales."""
     pages, heads, page, dim = 20000, 16, 64, 128                      # 2.6 GB of codes each

@@ -220,6 +220,44 @@ def test_row_counts_take_other_cluster_sizes(rows):
     assert torch.equal(whole, one)
 
 
+def test_two_calls_at_once():
+    """Two batches of rows on two streams, and the same rows again: equal to each alone."""
+    x = [logits_of(20, 30000, seed=s, slope=slope) for s, slope in ((30, 1.6), (31, 0.7))]
+    u = torch.tensor(uniform(20, 32), device="cuda")
+    kw = dict(top_p=torch.full((20,), 0.95, device="cuda"))
+    alone = [skv.sample_tokens(y, u, **kw) for y in x]
+    streams = [torch.cuda.Stream() for _ in x]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            out = torch.empty(20, dtype=torch.int32, device="cuda")
+            s.wait_stream(torch.cuda.current_stream())
+            skv.sample_tokens(x[i], u, out_tokens=out, stream=s, **kw)
+            got[i].append(out)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, alone[i]) for o in got[i])
+
+
+def test_largest_vocabulary_and_many_rows():
+    """2^19 tokens, all alike but for a few (the sums come near their 64 bits), and more rows than CTAs."""
+    V = 1 << 19
+    x = torch.zeros(3, V, device="cuda")
+    x[1, 77], x[1, V - 1] = 1.0, 1.0
+    x[2] = -5.0
+    got = skv.sample_tokens(x, torch.tensor([0.5, 0.25, 1.0 - 2.0 ** -24], device="cuda"))
+    assert int(got[0]) == V // 2 and int(got[2]) == V - 1
+    check(x[1:2], [0.25])
+    check(x[:2], [0.5, 0.9], p=[0.75, 0.5], k=[0, 400000])
+    rows = logits_of(5000, 600, seed=33)
+    u = uniform(5000, 33)
+    many = skv.sample_tokens(rows, torch.tensor(u, device="cuda"), top_k=torch.full((5000,), 20, dtype=torch.int32, device="cuda"))
+    host = rows.cpu().numpy()
+    for r in range(0, 5000, 97):
+        assert int(many[r]) == reference(host[r], k=20, u=u[r])[1]
+
+
 def test_frequencies_follow_the_distribution():
     """1 / n of evenly spread numbers give each token its probability, within 1 / n."""
     n = 20000

@@ -61,8 +61,9 @@ def test_block_scales_of_wrong_shapes_and_types():
         problem(k_cache=torch.zeros(4, 2, 64, 128, dtype=torch.bfloat16))
     with pytest.raises(TypeError, match="GQA"):
         problem(kind="mla", heads=1)
-    # numbers, also as tensors without dimensions, stay one scale per tensor
+    # numbers, also as tensors of one entry, stay one scale per tensor
     assert problem(k_scale=torch.tensor(0.5), v_scale=0.25).scale_block == 0
+    assert problem(k_scale=torch.tensor([0.5]), v_scale=torch.tensor([0.25])).k_scale == 0.5
 
 
 @pytest.mark.parametrize("page,block", [(64, 8), (256, 256), (64, 1), (96, 48)])
