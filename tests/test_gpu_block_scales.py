@@ -303,6 +303,29 @@ def test_graph_replays_follow_the_cache():
         check_attention(batch, out, lse, ref=batch.attention(want))
 
 
+def test_chunk_tiles_beside_decoding_requests():
+    """Enough chunk tasks for all SMs and decoding requests: the two kernels run side by side on streams of their own."""
+    batch = BlockBatch([2000] * 8 + [700], [1] * 8 + [640], heads=8, group=8, page=64, block=16, seed=52, spread=2.0, poison=True)
+    att = skv.SplitKVAttention(batch.problem)
+    assert att.plan.overlap_ctas > 0 and att.plan.num_chunk_tasks >= 152
+    out, lse = att.out_like()
+    for _ in range(3):
+        att.decode(out, lse)
+    att.check_device_error()
+    # every decoding row, and chunk rows spread over the request
+    some = BlockBatch([2000] * 8, [1] * 8, heads=8, group=8, page=64, block=16, seed=52, spread=2.0, poison=True)
+    for name in ("k", "v", "ks", "vs", "table"):
+        setattr(some, name, getattr(batch, name))
+    some.q = batch.q[:8]
+    check_attention(some, out[:8], lse[:8])
+    for i in (0, 1, 63, 300, 639):
+        one = BlockBatch([61 + i], [1], heads=8, group=8, page=64, block=16, seed=52, spread=2.0)
+        for name in ("k", "v", "ks", "vs"):
+            setattr(one, name, getattr(batch, name))
+        one.table, one.q = batch.table[8:], batch.q[8 + i:9 + i]
+        check_attention(one, out[8 + i:9 + i], lse[8 + i:9 + i])
+
+
 @pytest.mark.parametrize("seq,new,chunks", [([300, 1000, 65], [1, 1, 1], False), ([600, 90], [40, 1], True)])
 def test_withheld_tasks_time_out_and_the_context_survives(seq, new, chunks):
     """The test hook withholds every task: the bounded waits of the engine and of the chunk tiles run out into an error
