@@ -593,6 +593,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
         return n;
     };
     bool done = false;                    // the token has been given, cut and total are known
+    // Few tokens are kept: the CTA's part of the distribution is cleared while the list is being worked on, and what
+    // the list keeps is written into it at the end (768 rows of 32,000 float32 logits: top_k of 50 79 -> 67 us, greedy 58 -> 49).
+    int own = 0;                          // the CTA's entries of the list
+    auto clear = [&]() {
+        if (!a.probs) return;
+        float* out = a.probs + (size_t)row * a.probs_stride;
+        if (VEC > 1 && !((uintptr_t)out & 15)) {
+            const int end = x.v1 & ~3;    // (segments start at multiples of a vector)
+            for (int v = x.v0 + 4 * lane; v < end; v += 128) *(float4*)(out + v) = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int v = max(x.v0, end) + lane; v < x.v1; v += 32) out[v] = 0.f;
+        } else {
+            for (int v = x.v0 + lane; v < x.v1; v += 32) out[v] = 0.f;
+        }
+    };
+    bool listed = false;                  // the distribution is to be written from the list
     u64 total = 0;
     if (none) {
         if (a.tokens && rank == 0 && threadIdx.x == 0) a.tokens[row] = -1;
@@ -601,6 +616,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
         // ---- the lowest token that has the largest logit ----
         uint32_t at = INT_MAX;
         x.some(lane, [&](float f, int) { return f == top; }, [&](float, int v) { at = min(at, (uint32_t)v); });
+        clear();
         at = __reduce_min_sync(0xffffffffu, at);
         if (lane == 0) S.warp_a[warp] = at;
         __syncthreads();
@@ -611,7 +627,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
         if (a.tokens && rank == 0 && threadIdx.x == 0) a.tokens[row] = (int)at;
         cut = Cut{top, (int)at};
         total = units_of(weight(top));
-        done = true;
+        if (rank == 0 && threadIdx.x == 0) S.list[0] = rank_of(top, (int)at);
+        own = rank == 0;
+        done = listed = true;
     } else if (fast) {
         // ---- candidates; where top_p is first to cut, the sum of all weights too ----
         const float least = fmaxf(cut.x, pivot);
@@ -622,7 +640,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
             const u64 sum = warp_sum(x.sum(x.v0, x.v1, lane, [&](float f, int) { return f >= cut.x; }, units));
             if (lane == 0) S.seg_sum[warp] = sum;
         }
+        clear();
         cluster_sync();
+        own = (int)S.listed;
         if (rank == 0) {
             const int n = collect();
             bool ok = n <= kList;
@@ -748,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
         if (done) {
             cut = cut_at(load_u64(remote(&S.cut, 0)));
             total = load_u64(remote(&S.total, 0));
+            listed = true;
         }
     }
     // ---- otherwise: top_k, then top_p, each the rank where a sum over descending ranks reaches its target ----
@@ -970,19 +991,24 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
         const float th = (float)total, tl = none ? 0.f : (float)(long long)(total - (u64)th);
         const float q = __fdiv_rn(17592186044416.f, none ? 1.f : th);
         const float ql = __fdiv_rn(__fmaf_rn(-q, tl, __fmaf_rn(-q, th, 17592186044416.f)), none ? 1.f : th);
+        auto share = [&](float f) {
+            const Weight y = weight(f);
+            return y.n < -126 ? 0.f : __fmaf_rn(y.hi, q, __fmaf_rn(y.hi, ql, y.lo * q)) * __uint_as_float((uint32_t)(y.n + 127) << 23);
+        };
+        if (listed) {
+            __syncthreads();                 // behind the zeros
+            for (int i = threadIdx.x; i < own; i += kThreads) {
+                const u64 r = S.list[i];
+                const float f = value_of((uint32_t)(r >> 32));
+                if (cut.keeps(f, token_of(r))) out[token_of(r)] = share(f);
+            }
+        }
         const bool vec = VEC > 1 && !((uintptr_t)out & 15);
-        for (int v = x.v0 + lane * VEC; v < x.v1; v += kStep) {
+        for (int v = listed ? x.v1 : x.v0 + lane * VEC; v < x.v1; v += kStep) {
             float f[VEC];
             x.load(f, v, x.v1);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float r = 0.f;
-                if (!none && cut.keeps(f[j], v + j)) {
-                    const Weight y = weight(f[j]);
-                    if (y.n >= -126) r = __fmaf_rn(y.hi, q, __fmaf_rn(y.hi, ql, y.lo * q)) * __uint_as_float((uint32_t)(y.n + 127) << 23);
-                }
-                f[j] = r;
-            }
+            for (int j = 0; j < VEC; ++j) f[j] = !none && cut.keeps(f[j], v + j) ? share(f[j]) : 0.f;
             if (vec && v + VEC <= x.v1) {
 #pragma unroll
                 for (int j = 0; j < VEC; j += 4) *(float4*)(out + v + j) = make_float4(f[j], f[(j + 1) % VEC], f[(j + 2) % VEC], f[(j + 3) % VEC]);

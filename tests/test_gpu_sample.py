@@ -209,6 +209,28 @@ def test_strided_and_unaligned_rows(dtype):
     assert (probs[:, :3] == -1).all() and (probs[:, 5006:] == -1).all() and (probs[:, 3:5006] > 0).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("offset,V", [(3, 5003), (4, 5003), (4, 5008), (8, 4097), (4, 3), (8, 70001)])
+def test_few_kept_tokens_in_strided_distributions(offset, V, dtype):
+    """Rows that keep few tokens, at bases and lengths that are multiples of a vector or not: what lies
+    beside the rows stays, what is not kept is zero."""
+    rows = 5
+    x = logits_of(rows, V, seed=21, dtype=dtype)
+    for kw in (dict(temperature=torch.zeros(rows, device="cuda")),
+               dict(top_k=torch.full((rows,), 3, dtype=torch.int32, device="cuda")),
+               dict(top_k=torch.full((rows,), 150, dtype=torch.int32, device="cuda")),
+               dict(top_p=torch.full((rows,), 0.3, device="cuda"))):
+        want = torch.full((rows, V), float("nan"), device="cuda")
+        skv.sample_tokens(x, None, probs_out=want, **kw)
+        wide = torch.full((rows, (V + offset + 9) // 4 * 4), -1.0, device="cuda")
+        skv.sample_tokens(x, None, probs_out=wide[:, offset:offset + V], **kw)
+        assert torch.equal(wide[:, offset:offset + V], want)
+        assert (wide[:, :offset] == -1).all() and (wide[:, offset + V:] == -1).all()
+        assert ((want > 0).sum(1) >= 1).all() and torch.allclose(want.double().sum(1), torch.ones(rows, device="cuda").double(), atol=1e-5)
+        if "top_k" in kw:
+            assert ((want > 0).sum(1) <= int(kw["top_k"][0])).all()
+
+
 @pytest.mark.parametrize("rows", [1, 40, 300])
 def test_row_counts_take_other_cluster_sizes(rows):
     x = logits_of(rows, 20000, seed=rows)
