@@ -231,8 +231,10 @@ struct Shared {
     uint32_t part[3][kBins];         // sums of weights, 15 bits apart; counts in the first
     u64 list[kList];
     u64 warp_a[kWarps], warp_b[kWarps];
-    u64 seg_sum[kWarps];
+    u64 seg_sum[kWarps], sums[2][kWarps];
     u64 best, low;                   // reduced over the cluster
+    u64 few_key[32], few_weight[32]; // select_key: the entries of the bin it looks for
+    uint32_t few;
     uint32_t warp_top[kWarps], warp_low[kWarps];   // keys of the largest lane maximum and of the r-th largest
     uint32_t tops[kMaxCluster * kWarps], lows[kMaxCluster * kWarps];   // the whole cluster's
     uint32_t pivot;
@@ -244,27 +246,17 @@ struct Shared {
     Cut first_cut;
 };
 
-// sums of two values over the threads up to this one, and in all
-__device__ __forceinline__ void block_scan(Shared& S, u64& a, u64& b, u64& all_a, u64& all_b) {
+// the sum over the threads up to this one, and in all
+__device__ __forceinline__ u64 block_scan(Shared& S, u64 a, u64& all) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     a = warp_scan(a, lane);
-    b = warp_scan(b, lane);
     __syncthreads();
-    if (lane == 31) {
-        S.warp_a[warp] = a;
-        S.warp_b[warp] = b;
-    }
+    if (lane == 31) S.warp_a[warp] = a;
     __syncthreads();
-    u64 xa = lane < kWarps ? S.warp_a[lane] : 0, xb = lane < kWarps ? S.warp_b[lane] : 0;
-    xa = warp_scan(xa, lane);
-    xb = warp_scan(xb, lane);
-    all_a = __shfl_sync(0xffffffffu, xa, kWarps - 1);
-    all_b = __shfl_sync(0xffffffffu, xb, kWarps - 1);
-    const u64 ea = __shfl_sync(0xffffffffu, xa, max(warp - 1, 0)), eb = __shfl_sync(0xffffffffu, xb, max(warp - 1, 0));
-    if (warp > 0) {
-        a += ea;
-        b += eb;
-    }
+    const u64 x = warp_scan(lane < kWarps ? S.warp_a[lane] : 0, lane);
+    all = __shfl_sync(0xffffffffu, x, kWarps - 1);
+    const u64 before = __shfl_sync(0xffffffffu, x, max(warp - 1, 0));
+    return warp > 0 ? a + before : a;
 }
 
 // A row of logits, in a warp's segment [v0, v1) of the vocabulary
@@ -385,9 +377,16 @@ __device__ __forceinline__ int pivot_rank(int cluster) {
     return cluster == 1 ? 28 : cluster == 2 ? 22 : cluster == 3 ? 17 : cluster == 4 ? 14 : cluster == 5 ? 12 : cluster == 6 ? 10 : 8;
 }
 
+__device__ __forceinline__ void clear_bins(Shared& S) {
+    static_assert(offsetof(Shared, part) % 16 == 0 && sizeof S.part % (16 * kThreads) == 0, "cleared 16 bytes at a time");
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof S.part / (16 * kThreads)); ++i) ((uint4*)S.part)[i * kThreads + threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // The key at which the weights, summed over the CTA's entries in descending order of their keys from `above` on,
-// reach `need` (they do; keys differ, but for weights of 0).  kList / kThreads entries per thread.  Each round spreads the range of the keys
-// over the bins and goes on with the bin of the crossing, until that holds one key (11 bits a round: 6 at most).
+// reach `need` (they do; keys differ, but for weights of 0).  kList / kThreads entries per thread.  The range of the
+// keys is spread over the bins; of the bin of the crossing up to 32 entries are compared with one another, where it
+// holds more (11 bits a round: 6 rounds at most) its range is spread again.
 constexpr int kOwn = kList / kThreads;
 __device__ __forceinline__ u64 select_key(Shared& S, const u64 (&key)[kOwn], const u64 (&weight)[kOwn], u64 above, u64 need) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -407,32 +406,31 @@ __device__ __forceinline__ u64 select_key(Shared& S, const u64 (&key)[kOwn], con
             S.warp_a[warp] = most;
             S.warp_b[warp] = low;
         }
-        for (int i = threadIdx.x; i < kBins; i += kThreads) S.part[0][i] = S.part[1][i] = S.part[2][i] = 0;
+        clear_bins(S);
+        if (threadIdx.x == 0) S.few = 0;
         __syncthreads();
         hi = warp_max(lane < kWarps ? S.warp_a[lane] : 0);
         lo = ~warp_max(lane < kWarps ? S.warp_b[lane] : 0);
-        if (lo == hi) break;
         const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 11);
 #pragma unroll
         for (int j = 0; j < kOwn; ++j)
             if (weight[j] && key[j] >= lo && key[j] <= hi) {
                 const int b = (int)((hi - key[j]) >> shift);
-                atomicAdd(&S.part[0][b], (uint32_t)weight[j] & 0x7FFFu);
-                atomicAdd(&S.part[1][b], (uint32_t)(weight[j] >> kLimb) & 0x7FFFu);
-                atomicAdd(&S.part[2][b], (uint32_t)(weight[j] >> (2 * kLimb)));
+                const uint32_t w0 = (uint32_t)weight[j] & 0x7FFFu, w1 = (uint32_t)(weight[j] >> kLimb) & 0x7FFFu, w2 = (uint32_t)(weight[j] >> (2 * kLimb));
+                if (w0) atomicAdd(&S.part[0][b], w0);
+                if (w1) atomicAdd(&S.part[1][b], w1);
+                if (w2) atomicAdd(&S.part[2][b], w2);
             }
         __syncthreads();
         constexpr int kPer = kBins / kThreads;
-        u64 sum[kPer], own = 0, zero = 0, t0, t1;
+        u64 sum[kPer], own = 0, all;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             const int i = kPer * threadIdx.x + j;
             sum[j] = S.part[0][i] + ((u64)S.part[1][i] << kLimb) + ((u64)S.part[2][i] << (2 * kLimb));
             own += sum[j];
         }
-        u64 incl = own;
-        block_scan(S, incl, zero, t0, t1);
-        u64 c = above + incl - own;
+        u64 c = above + block_scan(S, own, all) - own;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
             if (c < need && c + sum[j] >= need) S.found = Found{kPer * (int)threadIdx.x + j, c};
@@ -444,6 +442,24 @@ __device__ __forceinline__ u64 select_key(Shared& S, const u64 (&key)[kOwn], con
         const u64 h = hi - ((u64)f.bin << shift);
         lo = h - lo >= (1ull << shift) ? h - (1ull << shift) + 1 : lo;
         hi = h;
+#pragma unroll
+        for (int j = 0; j < kOwn; ++j)
+            if (weight[j] && key[j] >= lo && key[j] <= hi) {
+                const uint32_t i = atomicAdd(&S.few, 1u);
+                if (i < 32) {
+                    S.few_key[i] = key[j];
+                    S.few_weight[i] = weight[j];
+                }
+            }
+        __syncthreads();
+        const int n = (int)S.few;
+        if (n <= 32) {
+            const u64 mine = lane < n ? S.few_key[lane] : 0ull, w = lane < n ? S.few_weight[lane] : 0ull;
+            u64 before = above;
+            for (int j = 0; j < n; ++j) before += S.few_key[j] > mine ? S.few_weight[j] : 0ull;
+            const unsigned at = __ballot_sync(0xffffffffu, lane < n && before < need && before + w >= need);
+            return __shfl_sync(0xffffffffu, mine, max(__ffs(at) - 1, 0));
+        }
     }
     return hi;
 }
@@ -653,13 +669,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
                     for (int i = lane; i < warps; i += 32) all += load_u64(remote(&S.seg_sum[i % kWarps], i / kWarps));
                     all = warp_sum(all);
                 }
-                // the sum over the CTA, and how many threads' `on` holds
+                // the sum over the CTA, and how many threads' `on` holds (each array of its own: no thread is behind)
                 int kept = 0;
-                auto total_of = [&](u64 y, bool on) {
-                    u64 c = on, s, all_c;
-                    block_scan(S, y, c, s, all_c);
-                    kept = (int)all_c;
-                    return s;
+                auto total_of = [&](u64 (&part)[kWarps], u64 y, bool on) {
+                    y = warp_sum(y);
+                    if (lane == 0) part[warp] = y;
+                    kept = __syncthreads_count(on);
+                    return warp_sum(lane < kWarps ? part[lane] : 0);
                 };
                 if (n <= kThreads / 2) {
                     // ---- few: each entry counts what is before it, two threads an entry ----
@@ -680,12 +696,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
                     place += __shfl_xor_sync(0xffffffffu, place, 1);
                     before += __shfl_xor_sync(0xffffffffu, before, 1);
                     bool stay = e < n && (!want_k || place < k);
-                    sum = total_of(stay && half == 0 ? w0 : 0ull, stay && half == 0);
+                    sum = total_of(S.sums[0], stay && half == 0 ? w0 : 0ull, stay && half == 0);
                     if (want_p) {
                         const u64 need = needed_of(sum_all ? all : sum, p);
                         ok = sum >= need;
                         stay = stay && before < need;
-                        sum = total_of(stay && half == 0 ? w0 : 0ull, stay && half == 0);
+                        sum = total_of(S.sums[1], stay && half == 0 ? w0 : 0ull, stay && half == 0);
                     }
                     if (e < n && half == 0 && !stay) weights[e] = 0;
                     if (stay && half == 0 && place == kept - 1) S.cut = mine;
@@ -712,14 +728,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
                         key[j] = e < n ? S.list[e] : 0ull;
                         wt[j] = e < n ? units(value_of((uint32_t)(key[j] >> 32))) : 0ull;
                     }
-                    auto keep_from = [&](u64 least) {    // and their sum
+                    auto keep_from = [&](u64 (&part)[kWarps], u64 least) {    // and their sum
                         u64 y = 0;
 #pragma unroll
                         for (int j = 0; j < kOwn; ++j) {
                             wt[j] = key[j] >= least ? wt[j] : 0ull;
                             y += wt[j];
                         }
-                        return total_of(y, false);
+                        return total_of(part, y, false);
                     };
                     if (want_k && n > k) {
                         u64 one[kOwn];
@@ -727,13 +743,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
                         for (int j = 0; j < kOwn; ++j) one[j] = threadIdx.x + j * kThreads < n ? 1ull : 0ull;
                         last = select_key(S, key, one, 0, (u64)k);
                     }
-                    sum = keep_from(last);
+                    sum = keep_from(S.sums[0], last);
                     if (want_p) {
                         const u64 need = needed_of(sum_all ? all : sum, p);
                         ok = sum >= need;
                         if (ok) {
                             last = select_key(S, key, wt, 0, need);
-                            sum = keep_from(last);
+                            sum = keep_from(S.sums[1], last);
                         }
                     }
                     if (last == 0) {                     // everything in the list: the least rank
@@ -785,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
         float x_lo = 0.f, x_hi = 0.f;     // values of those ranks
         constexpr int kPer = kBins / kThreads;
         while (level < 8) {               // (11 bits of the ranks each)
-            for (int i = threadIdx.x; i < kBins; i += kThreads) S.part[0][i] = S.part[1][i] = S.part[2][i] = 0;
+            clear_bins(S);
             if (threadIdx.x == 0) S.listed = 0;
             __syncthreads();
             auto add = [&](int b, u64 u) {
@@ -828,8 +844,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
                 sum[j] = load_u64(remote(&S.list[b % slice], b / slice));
                 own += sum[j];
             }
-            u64 incl = own, zero = 0, all_s, all_z;
-            block_scan(S, incl, zero, all_s, all_z);
+            u64 all_s;
+            const u64 incl = block_scan(S, own, all_s);
             if (level == 0) need = by_count ? (u64)k : needed_of(all_s, p);
             if (threadIdx.x == 0) S.found = Found{-1, 0};
             __syncthreads();
