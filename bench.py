@@ -173,7 +173,7 @@ def _source_hash(paths):
 KERNEL_SOURCES = {
     "gqa_engine_kernel": ["long_context_split_gb300/csrc/gqa_engine.cu", "long_context_split_gb300/csrc/internal.h"],
     "chunk_tc_kernel": ["long_context_split_gb300/csrc/chunk_kernel.cu", "long_context_split_gb300/csrc/tc_common.cuh",
-                        "long_context_split_gb300/csrc/internal.h"],
+                        "long_context_split_gb300/csrc/tc_issue.cuh", "long_context_split_gb300/csrc/internal.h"],
     "mla_partial_kernel": ["long_context_split_gb300/csrc/mla_kernel.cu", "long_context_split_gb300/csrc/tc_common.cuh",
                            "long_context_split_gb300/csrc/tc_issue.cuh", "long_context_split_gb300/csrc/internal.h"],
     "generic_partial_kernel": ["long_context_split_gb300/csrc/generic_kernel.cu", "long_context_split_gb300/csrc/internal.h"],

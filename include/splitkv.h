@@ -143,7 +143,8 @@ typedef struct {
        Scales are 0 or from 2^-100 to 2^100; those of blocks that no visible token
        lies in may be anything.  Scores take a key's scale in float32; a weight meets its value's
        scale in float32 and is rounded to f16 relative to the largest such product of its row
-       (of the keys that one warp has met), so that blocks of very different scales keep their bits. */
+       (of the keys that one warp has met), so that blocks of very different scales keep their bits.
+       The NaN code of a new token's value may reach the rows of the new tokens before it. */
     const float *k_block_scales;     /* device [num_pages][num_kv_heads][page_size / scale_block] */
     const float *v_block_scales;     /* the same */
     int32_t scale_block;             /* 16, 32, 64 or 128; divides page_size */

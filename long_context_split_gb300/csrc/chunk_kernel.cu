@@ -228,8 +228,10 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {
 
 // The same for E4M3 caches with block scales: bf16 key codes (every E4M3 value is a bf16 and an
 // f16 number, so no product is rounded before its scale), f16 value codes, and a scale
-// for every 16 tokens and head, of keys times the score scale.  Slots past a request's last key hold zeros.  Bound by HBM: 2 bytes read, 4 written per key-value pair of elements.
-// A CTA takes a head of a page at a time.
+// for every 16 tokens and head, of keys times the score scale.  Slots past a request's last key
+// hold zeros.  Bound by HBM: 2 bytes read, 4 written per key-value pair of elements (34,102 tokens
+// of 8 heads 45 us, 4.7 TB/s).  A CTA takes a head of a page at a time: with whole pages, small
+// batches left SMs idle (8 requests of 100 rows after 8,000 158 us in all, now 150).
 __global__ void __launch_bounds__(256) chunk_block_convert_kernel(KernelArgs a) {
     constexpr int U = 4, c16 = 8;                                      // pieces of 16 codes per row (128 wide)
     const int P = a.page_size, H = a.num_kv_heads;                     // (P 64 or 128)
@@ -364,6 +366,8 @@ __device__ __forceinline__ float write_p16_blocks(const uint32_t (&sr)[64], cons
 // BS: block scales.  Keys and values are the copies' codes; a score takes its key's scale in place
 // of the score scale, a weight its value's scale before it is rounded to f16, under a
 // running maximum of its own as in the decode engine (mv, the units of O; raised lazily, as m is).
+// Paced by the softmax, a row per thread, beside products of the same length: 2,540 tokens of 64
+// heads after 31,562, 1.36 PFLOP: 1,165 us, 1.17 PFLOP/s (a bf16 cache without scales 1,073).
 template <int D, bool BS>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,

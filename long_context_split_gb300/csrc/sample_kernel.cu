@@ -1,30 +1,33 @@
 // The next token of each row of logits, and the distribution it is drawn from.
 //
-// What it computes, with m the row's largest logit and T its temperature: weights
-// exp((x_i - m) / T); tokens ordered by (x descending, index ascending), the order of the
-// 64-bit number "rank" = (monotone image of x's bits, inverted index).  Every filter
-// keeps the tokens from some rank up, so that what is kept is one `cut`: min_p's follows
-// from m, top_k's is the k-th largest rank, top_p's the rank at which the
-// weights summed in descending order reach top_p of what is left.  The draw inverts the
+// What it computes, with m the row's largest logit and T its temperature: weights exp((x_i - m) / T);
+// tokens ordered by (x descending, index ascending), the order of the 64-bit number "rank" = (monotone
+// image of x's bits, inverted index).  Every filter keeps the tokens from some rank up, so that what
+// is kept is one `cut`: min_p's follows from m, top_k's is the k-th largest rank, top_p's the rank at
+// which the weights summed in descending order reach top_p of what is left.  The draw inverts the
 // distribution function over the kept tokens in index order.
 //
-// Arithmetic: which token a border falls on must not depend on the order of a sum, so a
-// weight is an integer, its value in units of 2^-44 of a power of two just above the largest, and sums are
-// integers.  Float64 runs at 1/64 of the float32 rate here, so exp is evaluated on pairs of float32 with a table
-// of 2^(j/128) (P. T. P. Tang, "Table-driven implementation of the exponential function in
-// IEEE floating-point arithmetic", ACM Trans. Math. Softw. 15, 1989): an error below 2^-40 of the
-// weight where |m| / T is below 700 or so, of 2^-38 up to there, in about 40 instructions.
+// Arithmetic: which token a border falls on must not depend on the order of a sum, so a weight is an
+// integer, its value in units of 2^-44 of a power of two just above the largest, and sums are
+// integers.  Float64 runs at 1/64 of the float32 rate here, so exp is evaluated on pairs of float32
+// with a table of 2^(j/128) (P. T. P. Tang, "Table-driven implementation of the exponential function
+// in IEEE floating-point arithmetic", ACM Trans. Math. Softw. 15, 1989): an error below 2^-40 of the
+// weight (2^-38 where |m| / T is some hundreds), in about 40 instructions.
 //
-// What bounds it: one pass over the logits from memory; the rest are passes over the
-// same row from L2, their instructions, and latency.  A cluster of CTAs takes a row, a warp a
-// contiguous segment of the vocabulary.  The first pass takes the maximum, and that of every lane: the
-// r-th largest of a CTA's thread maxima has at least r tokens from it up, and usually not
-// many more, so that one pass with one comparison a token collects the candidates of top_k, or of
-// top_p where it also sums all weights; CTA 0 has them (at most 2048) in shared memory, and all
-// else follows from them: a few are each compared with all others, more go through histograms of their ranks.  Where they do not reach top_p (a flat distribution) or top_k is large,
-// the cut is found in a histogram of the tokens and weights over 1024 bins of x, whose bin with the cut is
-// divided again while it holds more than 2048 tokens, down to equal logits told apart by index; the draw then
-// takes the segments' sums of what is kept, and the one segment of the draw, as the verification of drafts does.
+// What bounds it: one pass over the logits from memory; the rest are passes over the same row from L2,
+// their instructions, and latency.  128 rows of 128,000 bf16 logits: the largest alone 11 us, a draw
+// without filters 46 (40 instructions a token for its weight: issue slots), top_k 50 29, top_p 0.9 77,
+// over flat rows 243; one such row 5, 13, 10, 19 and 53 (a chain of passes and barriers).  A cluster
+// of CTAs takes a row, a warp a contiguous segment of the vocabulary.  The first pass takes the
+// maximum, and that of every lane: the r-th largest of a CTA's thread maxima has at least r tokens
+// from it up, and usually not many more, so that one pass with one comparison a token collects the
+// candidates of top_k, or of top_p where it also sums all weights; CTA 0 has them (at most 2048) in
+// shared memory, and all else follows from them: a few are each compared with all others, more go
+// through histograms of their ranks.  Where they do not reach top_p (a flat distribution) or top_k is
+// large, the cut is found in a histogram of the tokens and weights over 2048 bins of x, whose bin with
+// the cut is divided again while it holds more than 2048 tokens, down to equal logits told apart by
+// index; the draw then takes the segments' sums of what is kept, and the one segment of the draw, as
+// the verification of drafts does.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1060,7 +1063,7 @@ cudaError_t launch_sample_tokens(const SampleArgs& a, int logits_bf16, cudaStrea
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     // CTAs per row: as many as leave each 4096 tokens and run at once, or twice that where top_k or top_p make rows
-    // unequal (128 rows of 128,000 tokens with settings of their own 123 -> 81 us, with none 48 -> 59); enough for the
+    // unequal (128 rows of 128,000 tokens with settings of their own 123 -> 81 us; with none 48 -> 59, so those keep to the fewer); enough for the
     // histogram's sums
     int cluster = std::min({kMaxCluster, (a.vocab + 4095) / 4096, std::max(1, (a.top_k || a.top_p ? 4 : 2) * sms / a.rows)});
     cluster = std::max(cluster, (a.vocab + (1 << 17) - 1) >> 17);
