@@ -12,7 +12,7 @@
 // head, keys or values) is taken by 1, 2, 4 or 8 warps, as many as hold its rows in
 // registers between the maximum and the quantisation (128 bytes a lane, so that four CTAs fit an SM; 256 for the
 // largest), so that rows are read once; a CTA works on 8 warps' worth of units at a time, on as many rows as leave
-// five CTAs an SM, so that the chain is waited for once for many rows.  18,524 rows of 8 heads of 128
+// one round of CTAs, so that the chain is waited for once for many rows.  18,524 rows of 8 heads of 128
 // (bf16, blocks of 16): 24 us, 4.7 TB/s, issue slots half used and the ramp of a short launch (with 256 bytes a
 // lane throughout 61.6, magnitudes compared as floats 44); blocks of 64 22, float32 rows 45; 64 rows, one a
 // request, 5.9.
@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtas = 5;           // CTAs per SM that the rows are shared out to
 constexpr int kMaxUnits = 128;     // rows, so at most as many blocks, of a CTA
 
 // One block with new tokens: its first new row, how many, and where they go
@@ -290,6 +289,8 @@ cudaError_t launch_w(const CacheRowsArgs& a, cudaStream_t s) {
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int y = std::max(1, std::min(2 * a.heads, 2 * a.heads * W / kWarps));   // one unit per group of warps
+    // all CTAs at once, as many as fit (18,524 rows: 20.3 us; with five an SM 24.2, the fifth after the others)
+    constexpr int kCtas = kHold <= 8 ? 4 : 2;
     const long long want = ((long long)a.rows * y + kCtas * sms - 1) / (kCtas * sms);
     const int per = (int)std::max(1ll, std::min<long long>(kMaxUnits, want));
     const long long x = ((long long)a.rows + per - 1) / per;

@@ -31,7 +31,7 @@ constexpr int kMaxTokens = 64;    // tokens per block
 struct E4M3 {
     uint8_t code;
 };
-struct E4M3Blocks {   // with block scales (gather: 122k rows of 8 heads of 128 to bf16 130 us, 5.8 TB/s; such a
+struct E4M3Blocks {   // with block scales (gather: 122k rows of 8 heads of 128 to bf16 124.5 us, 6.0 TB/s; such a
                       // cache is written by block_append_kernel)
     uint8_t code;
 };
@@ -205,14 +205,17 @@ __device__ __forceinline__ void locate(const CacheRowsArgs& a, int r0, int n, lo
 // stay in registers as they were read (kUnroll tokens of them) until they are converted and
 // stored.  Append converts more per byte read and wants warps: 64 bytes in flight a thread and
 // five blocks an SM (22.6k tokens into E4M3: 29.2 us; 37.5 with 128 bytes and three blocks);
-// gather wants loads: 128 bytes and four blocks (651 MB: 107.5 us; 123 with five blocks).
+// gather wants loads: 128 bytes and four blocks (651 MB: 107.5 us; 123 with five blocks); with block
+// scales, which take registers too, 64 bytes and five blocks (752 MB: 124.5 us; 130.5 with 128 and four,
+// 157 with 64 and six, 141 with 32 and four).
 template <typename Rows, typename Cache, int VEC, bool APPEND>
-__global__ void __launch_bounds__(kThreads, APPEND ? 5 : 4) cache_rows_kernel(CacheRowsArgs a, int tokens_per_block) {
+__global__ void __launch_bounds__(kThreads, APPEND || (std::is_same_v<Cache, E4M3Blocks> && VEC == 16) ? 5 : 4)
+cache_rows_kernel(CacheRowsArgs a, int tokens_per_block) {
     using Src = std::conditional_t<APPEND, Rows, Cache>;
     using Dst = std::conditional_t<APPEND, Cache, Rows>;
     constexpr bool kBlocks = std::is_same_v<Cache, E4M3Blocks>;
     constexpr int kSrc = VEC * (int)sizeof(Src), kDst = VEC * (int)sizeof(Dst);
-    constexpr int kUnroll = VEC == 1 ? 4 : std::min(8, std::max(2, (APPEND ? 64 : 128) / kSrc));
+    constexpr int kUnroll = VEC == 1 || (kBlocks && VEC == 16) ? 4 : std::min(8, std::max(2, (APPEND ? 64 : 128) / kSrc));
     __shared__ long long where[kMaxTokens];
     const int r0 = blockIdx.x * tokens_per_block;
     const int n = min(tokens_per_block, a.rows - r0);
