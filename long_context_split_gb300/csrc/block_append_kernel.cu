@@ -13,9 +13,9 @@
 // registers between the maximum and the quantisation (128 bytes a lane, so that four CTAs fit an SM; 256 for the
 // largest), so that rows are read once; a CTA works on 8 warps' worth of units at a time, on as many rows as leave
 // one round of CTAs, so that the chain is waited for once for many rows.  18,524 rows of 8 heads of 128
-// (bf16, blocks of 16): 24 us, 4.7 TB/s, issue slots half used and the ramp of a short launch (with 256 bytes a
-// lane throughout 61.6, magnitudes compared as floats 44); blocks of 64 22, float32 rows 45; 64 rows, one a
-// request, 5.9.
+// (bf16, blocks of 16): 20 us, 5.7 TB/s, the rest the ramp of a short launch (61.6 with 256 bytes a lane throughout,
+// 44 with magnitudes compared as floats, 24 with five CTAs an SM); blocks of 64 22, of 128 24, float32 rows 36; 64 rows,
+// one a request, 5.9.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
