@@ -206,6 +206,18 @@ def test_decode_against_float64(lengths, page, block, heads, group, poison):
     att.check_device_error()
 
 
+@pytest.mark.parametrize("group,new", [(1, [33, 64, 17]), (8, [5, 8, 7]), (16, [3, 4, 2]), (5, [7, 12, 1])])
+@pytest.mark.parametrize("heads", [1, 24])
+def test_blocks_of_up_to_64_rows(group, new, heads):
+    """17 to 64 query rows of a KV head in one block: more rows than lanes where states are combined; split
+    (few heads) and unsplit requests."""
+    batch = BlockBatch([700, 64, 1300], new, heads=heads, group=group, page=64, block=32, seed=25, spread=2.0, poison=True)
+    att = skv.SplitKVAttention(batch.problem)
+    assert att.plan.num_chunk_tasks == 0
+    check_attention(batch, *att.decode())
+    att.check_device_error()
+
+
 @pytest.mark.parametrize("spread", [12.0])
 def test_scales_far_apart_keep_their_bits(spread):
     """Value scales from 2^-40 to 2^40 of one another: rows that weigh a block of tiny values alone
