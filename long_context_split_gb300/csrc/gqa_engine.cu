@@ -54,7 +54,8 @@
 // differ by any factor, the product is kept relative to a maximum of its own, mv =
 // max(s + e) with 2^e the power of two above v: w = p v 2^(m - mv) <= 1 is what is rounded
 // to f16, and the output accumulates in units of 2^mv (taken back to 2^m where the
-// warps' states are combined), while the sum of weights stays in units of 2^m.  Bound by HBM
+// warps' states are combined), while the sum of weights stays in units of 2^m.  The factor v 2^(m - mv) passes
+// float32's range where p is below 2^-128 (the product is at most 1) and so 0: it is held to the largest finite number.  Bound by HBM
 // as the other caches are: 32 requests of 32,768 tokens, 128 / 8 heads, 321 us, 6.70 TB/s of codes
 // and scales; one token of 64 heads after 4,065 17.4 us, a chain of launch, claim, copies,
 // products, states, reduction.
@@ -67,6 +68,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <mutex>
 
 #include "splitkv.h"
@@ -789,7 +791,8 @@ __device__ __forceinline__ void attend_keys_bs(uint32_t kbase, int kw0, int key_
     }
 #pragma unroll
     for (int j = 0; j < C::KSTEP_PV; ++j) {
-        const float f0 = vsc[j] * to0, f1 = vsc[j] * to1;
+        // (finite: a weight below float32's range, or of a key that its row may not see, is 0, and so is its product)
+        const float f0 = fminf(vsc[j] * to0, FLT_MAX), f1 = fminf(vsc[j] * to1, FLT_MAX);
         uint32_t ph[4];
         ph[0] = pack_f16(s[2 * j][0] * f0, s[2 * j][1] * f0);
         ph[1] = pack_f16(s[2 * j][2] * f1, s[2 * j][3] * f1);

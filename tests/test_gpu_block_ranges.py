@@ -1,0 +1,107 @@
+"""Attention over block scales at the ends of their range, and with scores so far apart that weights leave
+float32's range: every output finite and within ``block_util``'s bound."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import long_context_split_gb300 as skv
+from tests.block_util import BlockBatch, check_attention, encode
+
+pytestmark = pytest.mark.gpu
+
+P100, M100, ZEROS = 2.0 ** 100, 2.0 ** -100, 2.0 ** -126
+
+
+class RangeBatch(BlockBatch):
+    def attention(self, codes=None):
+        """``block_util``'s, with 2^-133 more: an output below the normal numbers is rounded by half of bf16's step there,
+        2^-134, and each float32 product behind it by 2^-150 (fewer than 2^16 of them here)."""
+        out, lse, bound, lse_bound = super().attention(codes)
+        return out, lse, bound + 2.0 ** -133, lse_bound
+
+
+class FarBatch(RangeBatch):
+    """Block j of 16 tokens has blocks[j % len(blocks)] = (score, value scale): queries of ones and keys of plus or minus
+    one under a key scale that makes every score of the block `score` binary orders.  What a float32
+    weight cannot hold counts for nothing: a key more than 126 binary orders below its row's largest may be lost, so that
+    its share is added to the bound (one order more, for the exponent's own rounding)."""
+
+    def __init__(self, seq, new, blocks, seed=0, page=64, **kw):
+        super().__init__(seq, new, page=page, block=16, seed=seed, **kw)
+        self.q.fill_(1.0)
+        self.q_dev.copy_(self.q)
+        one = int(encode(np.array([1.0]))[0])
+        for b, n in enumerate(self.seq):
+            for j in range(-(-n // 16)):
+                score, scale = blocks[j % len(blocks)]
+                p, t = int(self.table[b, j * 16 // page]), j * 16 % page // 16
+                self.k[p, :, 16 * t:16 * t + 16] = one | (0x80 if score < 0 else 0)
+                self.ks[p, :, t] = abs(score) * math.log(2.0) / (self.dim * self.scale)
+                self.vs[p, :, t] = scale
+        for dev, host in ((self.k_dev, self.k), (self.ks_dev, self.ks), (self.vs_dev, self.vs)):
+            dev.copy_(torch.from_numpy(host))
+
+    def attention(self, codes=None):
+        out, lse, bound, lse_bound = super().attention(codes)
+        for b, (L, t) in enumerate(zip(self.seq, self.new)):
+            kk, vv = self.values(self.k, self.ks, b, 0, L), np.abs(self.values(self.v, self.vs, b, 0, L))
+            for i in range(t):
+                n, r = L - t + i + 1, int(self.qo[b]) + i
+                for h in range(self.heads * self.group):
+                    s = kk[:n, h // self.group].sum(1) * self.scale
+                    p = np.exp(s - s.max())
+                    bound[r, h] += np.where(p < 2.0 ** -125, p, 0.0) @ vv[:n, h // self.group] / p.sum()
+        return out, lse, bound, lse_bound
+
+
+# a dominant block with a value scale far below that of a block whose weights leave float32's range
+FAR = [[(0, M100), (-g, P100)] for g in (100, 127, 130, 160, 220)] + [[(0, 0.0), (-g, 4.0)] for g in (100, 140, 200)] + \
+      [[(0, ZEROS), (-g, 8.0)] for g in (100, 128, 180)] + [[(0, 2.0 ** -70), (-130, 2.0 ** 60)], [(0, ZEROS), (-150, 2.0 ** 120)]]
+# requests of one new token; blocks of 16 to 64 query rows per KV head
+FORMS = [("one", [200, 64, 17], [1, 1, 1], 4), ("block", [200, 40], [16, 5], 4)]
+
+
+@pytest.mark.parametrize("form,seq,new,group", FORMS, ids=[f[0] for f in FORMS])
+@pytest.mark.parametrize("blocks", range(len(FAR)))
+def test_scores_and_scales_far_apart(blocks, form, seq, new, group):
+    batch = FarBatch(seq, new, FAR[blocks], heads=2, group=group, seed=blocks)
+    att = skv.SplitKVAttention(batch.problem)
+    assert att.plan.kernel_path == 1 and (att.plan.num_chunk_tasks > 0) == (form == "tiles")
+    check_attention(batch, *att.decode())
+    att.check_device_error()
+
+
+@pytest.mark.parametrize("blocks", range(len(FAR)))
+def test_scores_and_scales_far_apart_on_the_float32_path(blocks):
+    batch = FarBatch([100, 40], [1, 20], FAR[blocks], heads=2, group=2, dim=64, seed=blocks)
+    att = skv.SplitKVAttention(batch.problem)
+    assert att.plan.kernel_path == 0
+    check_attention(batch, *att.decode())
+
+
+@pytest.mark.parametrize("scales", [(0.0, 16.0), (ZEROS, 16.0), (M100, P100), (0.0, 2.0 ** 110)])
+@pytest.mark.parametrize("group,seq,new,first", [(4, 24, 15, 16), (2, 40, 31, 16)])
+def test_later_blocks_that_a_row_may_not_see(group, seq, new, first, scales):
+    """The first rows see blocks of the first scale alone (0: they are 0), whatever the scale of the new tokens behind them."""
+    blocks = [(0, scales[0])] * (first // 16) + [(0, scales[1])] * 8
+    batch = FarBatch([seq], [new], blocks, heads=2, group=group, seed=group)
+    att = skv.SplitKVAttention(batch.problem)
+    assert (att.plan.num_chunk_tasks > 0) == (group * new > 64)
+    out, lse = att.decode()
+    check_attention(batch, out, lse)
+    if scales[0] == 0.0:
+        assert (out[:first - (seq - new)] == 0).all()
+
+
+# the largest score at a block of scale 0, after blocks of small scales and beside one that decides the output
+LATE = [[(0, M100)] * 4 + [(30, 0.0), (5, M100), (0, 0.0), (0, 0.0)], [(0, M100)] * 4 + [(60, 0.0), (7, M100), (0, 0.0), (-9, M100)],
+        [(0, ZEROS)] * 4 + [(9, 0.0), (6, ZEROS), (0, 0.0), (2, ZEROS)]]
+
+
+@pytest.mark.parametrize("form,seq,new,group", FORMS, ids=[f[0] for f in FORMS])
+@pytest.mark.parametrize("blocks", range(len(LATE)))
+def test_the_largest_score_under_a_scale_of_zero(blocks, form, seq, new, group):
+    batch = FarBatch(seq, new, LATE[blocks], heads=2, group=group, seed=20 + blocks)
+    check_attention(batch, *skv.SplitKVAttention(batch.problem).decode())
