@@ -48,6 +48,8 @@
 #include "splitkv.h"
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "tc_common.cuh"
 #include "tc_issue.cuh"
 #include "partial_io.cuh"
@@ -837,9 +839,12 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 const float base = (m == -INFINITY) ? 0.f : m;
                 const uint32_t pcol = lane_addr + kColS + kKeys * b2;
                 if constexpr (BS) {
-                    // from units of 2^m to 2^mv (at most 2^107 apart where a value's scale is not 0)
+                    // from units of 2^m to 2^mv (at most 2^107 apart where a value's scale is not 0); finite, since a
+                    // weight below float32's range, or of a key that the row may not see, is 0
                     const float to = ex2_ftz(fminf(base - (mv == -INFINITY ? 0.f : mv), 126.f));
-                    const float kc[4] = {kn.x, kn.y, kn.z, kn.w}, f[4] = {vn.x * to, vn.y * to, vn.z * to, vn.w * to};
+                    const float kc[4] = {kn.x, kn.y, kn.z, kn.w};
+                    const float f[4] = {fminf(vn.x * to, FLT_MAX), fminf(vn.y * to, FLT_MAX), fminf(vn.z * to, FLT_MAX),
+                                        fminf(vn.w * to, FLT_MAX)};
                     l += write_p16_blocks(sr, kc, f, base, pcol);
                     if (u + 1 < nu) read_scales(u + 1);
                 } else {

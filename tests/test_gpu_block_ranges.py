@@ -59,8 +59,8 @@ class FarBatch(RangeBatch):
 # a dominant block with a value scale far below that of a block whose weights leave float32's range
 FAR = [[(0, M100), (-g, P100)] for g in (100, 127, 130, 160, 220)] + [[(0, 0.0), (-g, 4.0)] for g in (100, 140, 200)] + \
       [[(0, ZEROS), (-g, 8.0)] for g in (100, 128, 180)] + [[(0, 2.0 ** -70), (-130, 2.0 ** 60)], [(0, ZEROS), (-150, 2.0 ** 120)]]
-# requests of one new token; blocks of 16 to 64 query rows per KV head
-FORMS = [("one", [200, 64, 17], [1, 1, 1], 4), ("block", [200, 40], [16, 5], 4)]
+# requests of one new token; blocks of 16 to 64 query rows per KV head; more rows, on the chunk tiles
+FORMS = [("one", [200, 64, 17], [1, 1, 1], 4), ("block", [200, 40], [16, 5], 4), ("tiles", [300, 200], [40, 33], 8)]
 
 
 @pytest.mark.parametrize("form,seq,new,group", FORMS, ids=[f[0] for f in FORMS])
@@ -82,7 +82,7 @@ def test_scores_and_scales_far_apart_on_the_float32_path(blocks):
 
 
 @pytest.mark.parametrize("scales", [(0.0, 16.0), (ZEROS, 16.0), (M100, P100), (0.0, 2.0 ** 110)])
-@pytest.mark.parametrize("group,seq,new,first", [(4, 24, 15, 16), (2, 40, 31, 16)])
+@pytest.mark.parametrize("group,seq,new,first", [(4, 24, 15, 16), (2, 40, 31, 16), (8, 40, 33, 16), (8, 120, 70, 64)])
 def test_later_blocks_that_a_row_may_not_see(group, seq, new, first, scales):
     """The first rows see blocks of the first scale alone (0: they are 0), whatever the scale of the new tokens behind them."""
     blocks = [(0, scales[0])] * (first // 16) + [(0, scales[1])] * 8
@@ -100,7 +100,7 @@ LATE = [[(0, M100)] * 4 + [(30, 0.0), (5, M100), (0, 0.0), (0, 0.0)], [(0, M100)
         [(0, ZEROS)] * 4 + [(9, 0.0), (6, ZEROS), (0, 0.0), (2, ZEROS)]]
 
 
-@pytest.mark.parametrize("form,seq,new,group", FORMS, ids=[f[0] for f in FORMS])
+@pytest.mark.parametrize("form,seq,new,group", FORMS[:2], ids=[f[0] for f in FORMS[:2]])
 @pytest.mark.parametrize("blocks", range(len(LATE)))
 def test_the_largest_score_under_a_scale_of_zero(blocks, form, seq, new, group):
     batch = FarBatch(seq, new, LATE[blocks], heads=2, group=group, seed=20 + blocks)
