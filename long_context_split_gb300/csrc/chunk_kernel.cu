@@ -755,6 +755,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 const bool unmasked = __all_sync(0xffffffffu, key0 + kKeys - 1 <= limit);
                 // row max of the raw scores (the scale, > 0 on this path, is applied after)
                 float mx, my = -INFINITY;
+                [[maybe_unused]] float most = 0.f;   // of the exponents of the unit's value scales, 0 at least
                 if constexpr (BS) {
                     if (!unmasked) {
 #pragma unroll
@@ -770,6 +771,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         // 2^up > v: v's exponent bits, as the low bits of 2^23 + ..
                         const float up = __uint_as_float(0x4B000000u | (__float_as_uint(vc[h]) >> 23)) - (8388608.f + 126.f);
                         my = fmaxf(my, x + up);
+                        most = fmaxf(most, up);
                     }
                 } else {
                     const float mxr = unmasked ? row_max64<false>(sr, 64) : row_max64<true>(sr, limit - key0 + 1);
@@ -790,7 +792,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                         l *= exp2f(m - mx);
                         m = mx;
                     }
-                    if (my > mv + kRescaleThreshold) {
+                    // (mv is not left behind where a factor v 2^(m - mv) nears the end of float32's range: m - mv is 126
+                    // at most, and a factor beyond that range meets weights of 0 alone)
+                    if (my > mv + (m - mv + most > 118.f ? 0.f : kRescaleThreshold)) {
                         scale_o = exp2f(mv - my);
                         mv = my;
                         need = true;
@@ -839,9 +843,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 const float base = (m == -INFINITY) ? 0.f : m;
                 const uint32_t pcol = lane_addr + kColS + kKeys * b2;
                 if constexpr (BS) {
-                    // from units of 2^m to 2^mv (at most 2^107 apart where a value's scale is not 0); finite, since a
-                    // weight below float32's range, or of a key that the row may not see, is 0
-                    const float to = ex2_ftz(fminf(base - (mv == -INFINITY ? 0.f : mv), 126.f));
+                    // from units of 2^m to 2^mv; finite, since a weight below float32's range, or of a key that the row
+                    // may not see, is 0
+                    const float to = ex2_ftz(base - (mv == -INFINITY ? 0.f : mv));
                     const float kc[4] = {kn.x, kn.y, kn.z, kn.w};
                     const float f[4] = {fminf(vn.x * to, FLT_MAX), fminf(vn.y * to, FLT_MAX), fminf(vn.z * to, FLT_MAX),
                                         fminf(vn.w * to, FLT_MAX)};

@@ -100,7 +100,7 @@ LATE = [[(0, M100)] * 4 + [(30, 0.0), (5, M100), (0, 0.0), (0, 0.0)], [(0, M100)
         [(0, ZEROS)] * 4 + [(9, 0.0), (6, ZEROS), (0, 0.0), (2, ZEROS)]]
 
 
-@pytest.mark.parametrize("form,seq,new,group", FORMS[:2], ids=[f[0] for f in FORMS[:2]])
+@pytest.mark.parametrize("form,seq,new,group", FORMS, ids=[f[0] for f in FORMS])
 @pytest.mark.parametrize("blocks", range(len(LATE)))
 def test_the_largest_score_under_a_scale_of_zero(blocks, form, seq, new, group):
     batch = FarBatch(seq, new, LATE[blocks], heads=2, group=group, seed=20 + blocks)
