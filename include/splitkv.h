@@ -140,10 +140,13 @@ typedef struct {
     int32_t reserved0;               /* 0 */
     /* Read only when kv_fp8 is 2 (a caller without these fields passes 0 or 1).  The value of a
        code in slot s of page p and KV head h is e4m3(code) * scales[p][h][s / scale_block].
-       Scales are 0 or from 2^-100 to 2^100; those of blocks that no visible token
-       lies in may be anything.  Scores take a key's scale in float32; a weight meets its value's
+       Scales are 0 or from 2^-126 to 2^120, as splitkv_kv_append writes them; those of blocks that no
+       visible token lies in may be anything.  Scores take a key's scale in float32; a weight meets its value's
        scale in float32 and is rounded to f16 relative to the largest such product of its row
        (of the keys that one warp has met), so that blocks of very different scales keep their bits.
+       Scores, weights and sums of weighted values have float32's range, as over other caches: a key
+       whose score is more than 87 (126 binary orders) below its row's largest may count for nothing, whatever its value's scale,
+       and sums from 2^128 on are infinite.
        The NaN code of a new token's value may reach the rows of the new tokens before it. */
     const float *k_block_scales;     /* device [num_pages][num_kv_heads][page_size / scale_block] */
     const float *v_block_scales;     /* the same */

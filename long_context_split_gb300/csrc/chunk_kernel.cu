@@ -871,7 +871,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                 tc_fence_after();
             }
             const bool empty_row = !(l > 0.f);
-            const float inv = empty_row ? 0.f : BS ? exp2f(mv - m) / l : 1.f / l;
+            const float inv = empty_row ? 0.f : 1.f / l;
+            // block scales: the unit of O apart, so that scales near 2^-126 do not leave a factor below the normal numbers
+            [[maybe_unused]] const float unit = empty_row ? 0.f : exp2f(mv - m);
+            auto normalised = [&](uint32_t x) {
+                const float y = __uint_as_float(x) * inv;
+                if constexpr (BS) return y * unit;
+                else return y;
+            };
             const float lse = empty_row ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -891,8 +898,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
                             uint32_t w[4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                __nv_bfloat162 p2 = __floats2bfloat162_rn(__uint_as_float(o[j + 2 * e]) * inv,
-                                                                          __uint_as_float(o[j + 2 * e + 1]) * inv);
+                                __nv_bfloat162 p2 = __floats2bfloat162_rn(normalised(o[j + 2 * e]),
+                                                                          normalised(o[j + 2 * e + 1]));
                                 w[e] = *reinterpret_cast<uint32_t*>(&p2);
                             }
                             op[j / 8] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -901,15 +908,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
                             *(float4*)((float*)a.out + orow * D + c + j) =
-                                make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
-                                            __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
+                                make_float4(normalised(o[j]), normalised(o[j + 1]),
+                                            normalised(o[j + 2]), normalised(o[j + 3]));
                     }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
                         store_part4(a.o_part, a.part_bf16, st * D + c + j,
-                                    make_float4(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv,
-                                                __uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv));
+                                    make_float4(normalised(o[j]), normalised(o[j + 1]),
+                                                normalised(o[j + 2]), normalised(o[j + 3])));
                 }
             }
             if (valid) {

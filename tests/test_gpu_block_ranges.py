@@ -28,8 +28,10 @@ class FarBatch(RangeBatch):
     weight cannot hold counts for nothing: a key more than 126 binary orders below its row's largest may be lost, so that
     its share is added to the bound (one order more, for the exponent's own rounding)."""
 
-    def __init__(self, seq, new, blocks, seed=0, page=64, **kw):
+    def __init__(self, seq, new, blocks, seed=0, page=64, positive=False, **kw):
         super().__init__(seq, new, page=page, block=16, seed=seed, **kw)
+        if positive:
+            self.v &= 0x7F
         self.q.fill_(1.0)
         self.q_dev.copy_(self.q)
         one = int(encode(np.array([1.0]))[0])
@@ -40,7 +42,7 @@ class FarBatch(RangeBatch):
                 self.k[p, :, 16 * t:16 * t + 16] = one | (0x80 if score < 0 else 0)
                 self.ks[p, :, t] = abs(score) * math.log(2.0) / (self.dim * self.scale)
                 self.vs[p, :, t] = scale
-        for dev, host in ((self.k_dev, self.k), (self.ks_dev, self.ks), (self.vs_dev, self.vs)):
+        for dev, host in ((self.k_dev, self.k), (self.v_dev, self.v), (self.ks_dev, self.ks), (self.vs_dev, self.vs)):
             dev.copy_(torch.from_numpy(host))
 
     def attention(self, codes=None):
@@ -104,4 +106,39 @@ LATE = [[(0, M100)] * 4 + [(30, 0.0), (5, M100), (0, 0.0), (0, 0.0)], [(0, M100)
 @pytest.mark.parametrize("blocks", range(len(LATE)))
 def test_the_largest_score_under_a_scale_of_zero(blocks, form, seq, new, group):
     batch = FarBatch(seq, new, LATE[blocks], heads=2, group=group, seed=20 + blocks)
+    check_attention(batch, *skv.SplitKVAttention(batch.problem).decode())
+
+
+@pytest.mark.parametrize("form,seq,new,group", FORMS + [("long", [4000], [40], 8)], ids=[f[0] for f in FORMS] + ["long"])
+@pytest.mark.parametrize("scale", [ZEROS, 2.0 ** -110, 2.0 ** 110])
+def test_scales_at_the_ends_of_the_range(scale, form, seq, new, group):
+    batch = FarBatch(seq, new, [(0, scale), (-1, scale), (2, scale / 2 if scale > 1 else 2 * scale)], heads=2, group=group, seed=30)
+    check_attention(batch, *skv.SplitKVAttention(batch.problem).decode())
+
+
+@pytest.mark.parametrize("scale", [ZEROS, 2.0 ** -100, 2.0 ** 100])
+@pytest.mark.parametrize("group,new", [(4, 4), (16, 5)])
+def test_long_histories_at_the_ends_of_the_range(scale, group, new):
+    """Sums of many weights (and, on the tiles, of weights that grow by less than they rescale for), of values all positive."""
+    blocks = [(0, scale)] * 4 + [(7.5, scale)] * 996
+    batch = FarBatch([16000], [new], blocks, heads=1, group=group, seed=31, positive=True)
+    check_attention(batch, *skv.SplitKVAttention(batch.problem, skv.plan_params("uniform", uniform_splits=1)).decode())
+
+
+@pytest.mark.parametrize("group,new", [(4, 9), (4, 16), (8, 40)])
+def test_attention_over_what_the_append_writes(group, new):
+    """Rows of zeros (a scale of 2^-126), of the smallest and of large finite numbers beside ordinary ones, appended and attended over."""
+    batch = RangeBatch([90, 16 + new, new, new], [new] * 4, heads=2, group=group, page=64, block=16, seed=40)
+    g = torch.Generator().manual_seed(41)
+    k, v = (torch.randn(4 * new, 2, 128, generator=g) for _ in range(2))
+    k *= 0.05
+    v[:new // 2] = 0.0
+    v[new // 2:new] *= 2.0 ** 100
+    v[2 * new:2 * new + 16] = 0.0                  # a block of zeros, the next one (if any) of large values
+    v[2 * new + 16:3 * new] *= 2.0 ** 40
+    v[3 * new:] *= 2.0 ** -120
+    k, v = k.to(torch.bfloat16).cuda(), v.to(torch.bfloat16).cuda()
+    skv.kv_append(batch.problem, k, v)
+    batch.k, batch.ks, batch.v, batch.vs = (t.cpu().numpy() for t in (batch.k_dev, batch.ks_dev, batch.v_dev, batch.vs_dev))
+    assert (batch.vs == ZEROS).any() and batch.vs.max() > 2.0 ** 90
     check_attention(batch, *skv.SplitKVAttention(batch.problem).decode())
