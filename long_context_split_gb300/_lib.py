@@ -269,8 +269,15 @@ class AttentionProblem:
         self.kv_fp8 = k_cache.dtype == torch.uint8
         if self.kv_fp8 != (k_scale is not None and v_scale is not None):
             raise TypeError("uint8 (E4M3) K/V caches come with k_scale and v_scale, other caches without")
-        blocks = isinstance(k_scale, torch.Tensor) and k_scale.dim() > 1
-        if blocks != (isinstance(v_scale, torch.Tensor) and v_scale.dim() > 1):
+        # a tensor of one entry is a number, whatever its dimensions, but for a GQA cache of one page, head and block
+        one_block = kind == "gqa" and tuple(k_cache.shape[:2]) == (1, 1) and page_size in (16, 32, 64, 128)
+
+        def is_blocks(t):
+            return isinstance(t, torch.Tensor) and t.dim() > 1 and (
+                t.numel() != 1 or (one_block and t.dim() == 3 and t.dtype == torch.float32))
+
+        blocks = is_blocks(k_scale)
+        if blocks != is_blocks(v_scale):
             raise TypeError("k_scale and v_scale are both numbers or both block scales")
         self.scale_block = 0
         if blocks:
