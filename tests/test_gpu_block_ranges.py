@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import long_context_split_gb300 as skv
-from tests.block_util import BlockBatch, check_attention, encode
+from tests.block_util import VALUES, BlockBatch, check_attention, encode
 
 pytestmark = pytest.mark.gpu
 
@@ -28,10 +28,8 @@ class FarBatch(RangeBatch):
     weight cannot hold counts for nothing: a key more than 126 binary orders below its row's largest may be lost, so that
     its share is added to the bound (one order more, for the exponent's own rounding)."""
 
-    def __init__(self, seq, new, blocks, seed=0, page=64, positive=False, **kw):
+    def __init__(self, seq, new, blocks, seed=0, page=64, **kw):
         super().__init__(seq, new, page=page, block=16, seed=seed, **kw)
-        if positive:
-            self.v &= 0x7F
         self.q.fill_(1.0)
         self.q_dev.copy_(self.q)
         one = int(encode(np.array([1.0]))[0])
@@ -42,7 +40,7 @@ class FarBatch(RangeBatch):
                 self.k[p, :, 16 * t:16 * t + 16] = one | (0x80 if score < 0 else 0)
                 self.ks[p, :, t] = abs(score) * math.log(2.0) / (self.dim * self.scale)
                 self.vs[p, :, t] = scale
-        for dev, host in ((self.k_dev, self.k), (self.v_dev, self.v), (self.ks_dev, self.ks), (self.vs_dev, self.vs)):
+        for dev, host in ((self.k_dev, self.k), (self.ks_dev, self.ks), (self.vs_dev, self.vs)):
             dev.copy_(torch.from_numpy(host))
 
     def attention(self, codes=None):
@@ -116,13 +114,30 @@ def test_scales_at_the_ends_of_the_range(scale, form, seq, new, group):
     check_attention(batch, *skv.SplitKVAttention(batch.problem).decode())
 
 
-@pytest.mark.parametrize("scale", [ZEROS, 2.0 ** -100, 2.0 ** 100])
-@pytest.mark.parametrize("group,new", [(4, 4), (16, 5)])
-def test_long_histories_at_the_ends_of_the_range(scale, group, new):
-    """Sums of many weights (and, on the tiles, of weights that grow by less than they rescale for), of values all positive."""
-    blocks = [(0, scale)] * 4 + [(7.5, scale)] * 996
-    batch = FarBatch([16000], [new], blocks, heads=1, group=group, seed=31, positive=True)
-    check_attention(batch, *skv.SplitKVAttention(batch.problem, skv.plan_params("uniform", uniform_splits=1)).decode())
+def test_half_a_million_tokens_of_the_smallest_scale():
+    """On the chunk tiles: the sum of weights (after a first unit of scores 7.5 binary orders lower, which they do not
+    rescale for) times 2^126 is far beyond float32's normal numbers.  Every query is alike, so that a token's rows are."""
+    n, new, group, page = 516224, 5, 16, 64
+    g = torch.Generator(device="cuda").manual_seed(31)
+    v = torch.randint(0x20, 0x70, (n // page, 1, page, 128), generator=g, device="cuda", dtype=torch.uint8)
+    ks = torch.full((n // page, 1, 4), 7.5 * math.log(2.0) / math.sqrt(128.0), device="cuda")
+    ks[0] = 0.0
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    problem = skv.AttentionProblem(
+        q=torch.ones(new, group, 128, dtype=torch.bfloat16, device="cuda"), k_cache=torch.full_like(v, 0x38), v_cache=v,
+        page_table=torch.arange(n // page, dtype=torch.int32, device="cuda")[None].contiguous(), seq_lens=i32([n]), qo_indptr=i32([0, new]),
+        num_q_heads=group, num_kv_heads=1, head_dim_qk=128, head_dim_v=128, page_size=page, scale=1.0 / math.sqrt(128.0),
+        seq_lens_host=[n], qo_indptr_host=[0, new], k_scale=ks, v_scale=torch.full_like(ks, ZEROS))
+    att = skv.SplitKVAttention(problem, skv.plan_params("uniform", uniform_splits=1))
+    assert att.plan.num_chunk_tasks > 0
+    out, _ = att.decode()
+    x = torch.from_numpy(VALUES).cuda()[v.view(n, 128).long()]                     # (in units of the scale)
+    w = torch.exp2(torch.where(torch.arange(n, device="cuda") < 64, -7.5, 0.0).double())
+    for i in range(new):
+        m = n - new + i + 1
+        want = (w[:m] @ x[:m]) / w[:m].sum()
+        # bf16's rounding, f16's of the weights and 2^-11 for the scores' and the float32 sums' errors (all values positive)
+        assert ((out[i].double() * 2.0 ** 126 - want).abs() <= want * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -11)).all()
 
 
 @pytest.mark.parametrize("group,new", [(4, 9), (4, 16), (8, 40)])
