@@ -634,7 +634,7 @@ typedef struct {
     int32_t *free_pages;             /* [capacity]: the ids of the free pages, the next one to be taken last */
     const int32_t *free_count;       /* [1]: how many there are */
     int32_t *free_count_out;         /* [1], after the call (may be free_count itself) */
-    const int32_t *qo_indptr;        /* [batch + 1], or NULL without slots */
+    const int32_t *qo_indptr;        /* [batch + 1], or NULL without slots (not read where num_slots is 0) */
     int64_t *slots;                  /* [num_slots], or NULL: the cache slot, page * page_size + offset, of every new token:
                                         entry qo_indptr[b] + i is that of token seq_lens[b] - q_len + i */
     int32_t num_slots;               /* entries of slots; those from qo_indptr[batch] on are left as they were */

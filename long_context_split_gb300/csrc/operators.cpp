@@ -637,7 +637,8 @@ splitkv_status splitkv_assign_pages(const splitkv_pages* p, int32_t* dev_error_w
     if (p->page_size < 1 || p->max_pages_per_req < 1 || p->capacity < 1)
         return fail_with(SPLITKV_ERR_INVALID_ARG, "page_size, max_pages_per_req and capacity must be >= 1");
     if (p->num_slots < 0 || p->reserved != 0) return fail_with(SPLITKV_ERR_INVALID_ARG, "num_slots %d or reserved", p->num_slots);
-    if ((p->qo_indptr == nullptr) != (p->slots == nullptr && p->num_slots == 0))
+    // (row bounds without slots: a step without new tokens, whose empty buffer may have no address)
+    if (p->qo_indptr == nullptr ? p->slots != nullptr || p->num_slots > 0 : p->slots == nullptr && p->num_slots > 0)
         return fail_with(SPLITKV_ERR_INVALID_ARG, "qo_indptr and slots come together");
     if ((uintptr_t)p->slots & 7) return fail_with(SPLITKV_ERR_INVALID_ARG, "slots are not aligned to their elements");
     splitkv_status s;
