@@ -655,7 +655,8 @@ typedef struct {
  *    negative length counts as 0 and reports it too, as do a held or free count out of
  *    range (taken as the nearest one in range) and pages given back beyond `capacity`
  *    (dropped).  Slots of tokens without a page are -1, so are all those of a request whose
- *    qo_indptr entries decrease, leave num_slots or exceed its length (reported).
+ *    qo_indptr entries decrease, leave num_slots or exceed its length (reported).  A row that two
+ *    requests claim (entries that decrease in between) gets the value of one of them.
  */
 splitkv_status splitkv_assign_pages(const splitkv_pages *p, int32_t *dev_error_word, splitkv_stream stream);
 
