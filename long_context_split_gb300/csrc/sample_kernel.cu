@@ -47,7 +47,7 @@ constexpr int kBins = 4 * kThreads;
 // Bins of 1/80 of a factor of two in weight (of exp(x) for counts) below the largest, so fine that a warp's tokens
 // seldom meet in one, and after half of them of 1/16
 constexpr float kFine = 80.f, kCoarse = 0.2f;
-constexpr int kList = 2048;          // tokens that are sorted in shared memory
+constexpr int kList = 2048;          // tokens that CTA 0 selects from in shared memory
 constexpr int kOne = 44;             // weights are in units of 2^-44
 constexpr int kTable = 128;
 constexpr int kLimb = 15;            // a histogram's weights in three parts, each summed in 32 bits over 2^17 tokens
@@ -374,8 +374,10 @@ struct Row {
 };
 
 // A pivot: of the 16 C warps' r-th largest lane maxima the m-th largest, so that at least r m tokens reach
-// it.  top_k takes m of at most 10 C and r = ceil(k / m); top_p the r below and m = 8 C, for about
-// 1100 candidates where tokens fall on lanes at random (512 C ln(32 / (32 - r))).
+// it.  top_k takes m of at most 10 C and r = ceil(k / m), top_p the r below and m = 8 C, for about
+// 1100 candidates where tokens fall on lanes at random (512 C ln(32 / (32 - r))).  top_k takes candidates while its r is no
+// larger (k up to 280 with one CTA a row, 440, 510, 560, 600, 600, 560 and 640 with more): top_k of 512 over 128 rows of
+// 128,000 bf16 logits 43 us, by histograms 113; of 280 over 768 rows of 32,000 65 to 72, 156; of 640 over one row 16, 37.
 __device__ __forceinline__ int pivot_rank(int cluster) {
     return cluster == 1 ? 28 : cluster == 2 ? 22 : cluster == 3 ? 17 : cluster == 4 ? 14 : cluster == 5 ? 12 : cluster == 6 ? 10 : 8;
 }
@@ -504,7 +506,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_tokens_kernel(SampleArgs a
     if (invalid && a.err && rank == 0 && threadIdx.x == 0) atomicCAS(a.err, 0, ERR_DEVICE_CHECK | SITE_TOKEN_RANGE);
     const bool greedy = temp == 0.f || p <= 0.f;
     bool want_k = !greedy && k > 0 && k < V, want_p = !greedy && p < 1.f;
-    const bool fast = want_k ? k <= 200 : want_p;            // candidates from the lanes' maxima
+    // candidates from the lanes' maxima, where r is no more than top_p's and their number as far from the list's end
+    const bool fast = want_k ? k <= 10 * cluster * pivot_rank(cluster) : want_p;
     // ---- the largest logit, and logits that enough candidates reach ----
     float top, pivot = -INFINITY;
     {
