@@ -95,6 +95,21 @@ def test_later_blocks_that_a_row_may_not_see(group, seq, new, first, scales):
         assert (out[:first - (seq - new)] == 0).all()
 
 
+@pytest.mark.parametrize("form,seq,new,group", FORMS, ids=[f[0] for f in FORMS])
+@pytest.mark.parametrize("reach", [20.0, 90.0, 200.0])
+@pytest.mark.parametrize("seed", range(3))
+def test_random_scores_and_scales(seed, reach, form, seq, new, group):
+    """Scores and value scales of every block drawn from ranges wider and narrower than float32's, some scales 0."""
+    g = np.random.default_rng(seed)
+    blocks = [(float(g.uniform(-reach, reach)), 0.0 if g.random() < 0.2 else 2.0 ** float(g.uniform(max(-126.0, -reach), min(100.0, reach))))
+              for _ in range(13)]
+    batch = FarBatch(seq, new, blocks, heads=2, group=group, seed=50 + seed)
+    for params in (None, dict(uniform_splits=3)):
+        att = skv.SplitKVAttention(batch.problem, skv.plan_params("uniform", **params) if params else None)
+        check_attention(batch, *att.decode())
+        att.check_device_error()
+
+
 # the largest score at a block of scale 0, after blocks of small scales and beside one that decides the output
 LATE = [[(0, M100)] * 4 + [(30, 0.0), (5, M100), (0, 0.0), (0, 0.0)], [(0, M100)] * 4 + [(60, 0.0), (7, M100), (0, 0.0), (-9, M100)],
         [(0, ZEROS)] * 4 + [(9, 0.0), (6, ZEROS), (0, 0.0), (2, ZEROS)]]
