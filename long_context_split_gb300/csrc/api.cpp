@@ -603,8 +603,9 @@ splitkv_status splitkv_plan(const splitkv_problem* prob, const splitkv_plan_para
         long long rows = (long long)pl->q_len[b] * g;
         rpt[b] = pl->rows_per_task;
         if (pl->path == 1 && P >= 64 && rows > 16) rpt[b] = 64;
-        // (block scales: no paired tiles, and chunk tiles from 65 rows: 16 requests of 80 to 128 rows after 8,000 tokens
-        // 304 us, on the engine's wide blocks 345 to 366; of 64 rows 305 against 212)
+        // (block scales: no paired tiles, and chunk tiles from 65 rows.  16 requests after 500 tokens: 72 to 128 rows 26 to 28 us,
+        // on the engine's wide blocks 42 to 47; 64 rows 26, 29.  After 8,000 tokens, since the engine's warps wait in step: 72
+        // and 80 rows 305 against 265, 96 and 128 302 to 306 against 301; 64 rows 303 against 162; 192 rows 329 against 445.)
         if (chunk_ok && rows > (prob->kv_fp8 == 2 ? 64 : 128)) {
             rpt[b] = 256;
             is_chunk[b] = 1;

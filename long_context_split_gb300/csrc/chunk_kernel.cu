@@ -369,7 +369,7 @@ __device__ __forceinline__ float write_p16_blocks(const uint32_t (&sr)[64], cons
 // of the score scale, a weight its value's scale before it is rounded to f16, under a
 // running maximum of its own as in the decode engine (mv, the units of O; raised lazily, as m is).
 // Paced by the softmax, a row per thread, beside products of the same length: 2,540 tokens of 64
-// heads after 31,562, 1.36 PFLOP: 1,165 us, 1.17 PFLOP/s (a bf16 cache without scales 1,073).
+// heads after 31,562, 1.36 PFLOP: 1,170 us, 1.16 PFLOP/s (a bf16 cache without scales 1,073).
 template <int D, bool BS>
 __global__ void __launch_bounds__(kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
@@ -534,7 +534,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constan
         const int t = warp == 1 ? 0 : 1;
         if constexpr (BS) {
             // The same by the warp in step, one elected lane issuing (tc_issue.cuh); both forms of the schedule and its
-            // barriers are those below.
+            // barriers are those below.  (Over block scales 1,242 -> 1,213 us.  Tried on the bf16 tiles of a mixed batch, 48 decoding requests
+            // and two chunks of 2,048 tokens: issue alone no change, 2.17 ms, with the softmax warps' waits in step too 2.11.)
             const uint32_t leader = elect_one();
             constexpr uint32_t id_s = idesc_bf16(kRows, kKeys, 0), id_o = idesc_f16(kRows, D, 1);
             const uint64_t qd = desc_sw128(smem_u32(sQ + t * C::Q_TILE), 16, 1024);
